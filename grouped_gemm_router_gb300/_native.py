@@ -23,6 +23,9 @@ MOE_ERR_DEVICE_TIMEOUT = -5
 MOE_FFN_CHAINED = 1
 CHAINED_MAX_D = 256
 
+MOE_BF16 = 0
+MOE_FP32 = 1
+
 MAX_EXPERTS = 128
 MAX_TOPK = 16
 MAX_DIM = 8192
@@ -46,7 +49,7 @@ class MoeError(RuntimeError):
         super().__init__(f"{where}: {status_str(status)} ({status})")
 
 
-_vp, _sz, _i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_vp, _sz, _i32, _f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
 _SIGNATURES = {
     "moe_ffn_workspace_size": (_sz, [MoeDims, _i32, _i32]),
@@ -66,6 +69,9 @@ _SIGNATURES = {
     "moe_grouped_down": (_i32, [_vp, _vp, _vp, _vp, MoeDims, _vp, _vp, _vp]),
     "moe_grouped_ffn_chained": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, MoeDims, _vp, _vp, _vp]),
     "moe_combine": (_i32, [_vp, _vp, _vp, _vp, MoeDims, _vp, _vp]),
+    "moe_layer_norm_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_layer_norm_backward_scratch_size": (_sz, [_i32, _i32]),
+    "moe_layer_norm_backward": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_permute_noalloc": (_i32, [_vp, MoeDims, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_device_error": (_i32, []),
     "moe_selftest_wait_timeout": (_i32, [_i32, _vp, _vp]),

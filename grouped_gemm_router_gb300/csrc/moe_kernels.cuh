@@ -134,6 +134,38 @@ cudaError_t launch_router_bwd(const BwdLayout& L, const uint16_t* x_sorted, cons
                               const int32_t* offsets, const float* lbar, float* part, float* dWg,
                               float* dbias, cudaStream_t s, bool pdl);
 
+// ---- layer norm (layer_norm.cu) ----
+constexpr int kLnMaxPartials = 512;  // most partial rows of the weight gradients
+struct LayerNormArgs {
+  const void* x;     // [T, D], fp32 or bf16
+  int x_fp32;
+  const void* add;   // [T, D] bf16 or nullptr
+  const float* weight;
+  const float* bias;  // or nullptr
+  float eps;
+  int T, D;
+  void* y;     // [T, D] bf16
+  void* h;     // [T, D] in x's type, with add
+  float* mean;
+  float* rstd;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
+struct LayerNormBwdArgs {
+  const void* dy;  // [T, D] bf16
+  const void* x;   // [T, D], fp32 or bf16
+  int x_fp32;
+  const float* weight;
+  const float* mean;
+  const float* rstd;
+  const void* d_stream;  // [T, D] in x's type or nullptr
+  int T, D;
+  void* dx;       // [T, D] in x's type
+  float* dweight;
+  float* dbias;  // or nullptr
+  float* part;   // [<= kLnMaxPartials, 2, D]
+};
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, cudaStream_t s);
+
 // 2-D bf16 TMA descriptor of a row-major [rows, cols] matrix with a
 // {box_cols, box_rows} box: 128-byte swizzle (64-byte for 32-column boxes),
 // zero fill outside the tensor (grouped_gemm.cu).

@@ -372,6 +372,75 @@ def moe_combine(y, weights, inv, ys=None, out=None):
     return out
 
 
+_STREAM_TYPES = {torch.bfloat16: N.MOE_BF16, torch.float32: N.MOE_FP32}
+
+
+def _stream_type(x):
+    """The C ABI's element type of a residual stream x."""
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [T, D]")
+    if x.dtype not in _STREAM_TYPES:
+        raise ValueError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    return _STREAM_TYPES[x.dtype]
+
+
+def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
+    """Layer norm of a residual stream x [T, D] (bf16 or fp32), the input of
+    the MoE layer: dict(y [T, D] bf16, mean [T] fp32, rstd [T] fp32).  With
+    `add` [T, D] bf16 (a sublayer's output) the stream becomes h = x + add,
+    rounded to x's type, and that is what is normalised; the dict then holds
+    h too.  weight, bias: [D] fp32.  Any D up to 8192."""
+    kind = _stream_type(x)
+    T, D = x.shape
+    _need(x, "x", x.dtype)
+    _need(weight, "weight", torch.float32, (D,))
+    _need(bias, "bias", torch.float32, (D,))
+    _need(add, "add", torch.bfloat16, (T, D))
+    _need(y, "y", torch.bfloat16, (T, D))
+    dev = x.device
+    if y is None:
+        y = torch.empty(T, D, dtype=torch.bfloat16, device=dev)
+    out = dict(y=y, mean=torch.empty(T, dtype=torch.float32, device=dev),
+               rstd=torch.empty(T, dtype=torch.float32, device=dev))
+    if add is not None:
+        out["h"] = torch.empty_like(x)
+    st = lib.moe_layer_norm_forward(x.data_ptr(), kind, None if add is None else add.data_ptr(), weight.data_ptr(),
+                                    None if bias is None else bias.data_ptr(), eps, T, D, y.data_ptr(),
+                                    None if add is None else out["h"].data_ptr(), out["mean"].data_ptr(),
+                                    out["rstd"].data_ptr(), torch.cuda.current_stream().cuda_stream)
+    check(st, "moe_layer_norm_forward")
+    return out
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
+    """Gradients of sum(dy * y) (+ sum(d_stream * h)) for layer_norm_forward:
+    dict(dx [T, D] in x's type, dweight [D] fp32, and with bias=True dbias [D]
+    fp32).  x: the rows that were normalised (the forward's h where it added);
+    mean, rstd: the forward's; dy [T, D] bf16; d_stream [T, D] in x's type:
+    the gradient that reaches these rows past the norm."""
+    kind = _stream_type(x)
+    T, D = x.shape
+    _need(x, "x", x.dtype)
+    _need(dy, "dy", torch.bfloat16, (T, D))
+    _need(weight, "weight", torch.float32, (D,))
+    _need(mean, "mean", torch.float32, (T,))
+    _need(rstd, "rstd", torch.float32, (T,))
+    _need(d_stream, "d_stream", x.dtype, (T, D))
+    dev = x.device
+    out = dict(dx=torch.empty_like(x), dweight=torch.empty(D, dtype=torch.float32, device=dev))
+    if bias:
+        out["dbias"] = torch.empty(D, dtype=torch.float32, device=dev)
+    nscratch = int(lib.moe_layer_norm_backward_scratch_size(T, D))
+    scratch = torch.empty(max(nscratch, 16), dtype=torch.uint8, device=dev)
+    st = lib.moe_layer_norm_backward(dy.data_ptr(), x.data_ptr(), kind, weight.data_ptr(), mean.data_ptr(),
+                                     rstd.data_ptr(), None if d_stream is None else d_stream.data_ptr(), T, D,
+                                     out["dx"].data_ptr(), out["dweight"].data_ptr(),
+                                     out["dbias"].data_ptr() if bias else None, scratch.data_ptr(), nscratch,
+                                     torch.cuda.current_stream().cuda_stream)
+    check(st, "moe_layer_norm_backward")
+    return out
+
+
 def device_error() -> int:
     return int(lib.moe_device_error())
 

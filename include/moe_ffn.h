@@ -260,6 +260,43 @@ moe_status moe_grouped_ffn_chained(const void* x_sorted, const void* x, const vo
 moe_status moe_combine(const void* y, const float* ys, const float* weights, const int32_t* inv, moe_dims d,
                        void* out, void* stream);
 
+/* ---- Layer norm around the layer ---- */
+
+/* Element types of the entry points below that take more than one. */
+typedef enum { MOE_BF16 = 0, MOE_FP32 = 1 } moe_dtype;
+
+/* Layer norm of the residual stream, with the sum it starts from:
+ *   h = x (+ add), rounded once to x's type when `add` is given
+ *   y = (h - mean(h)) * rstd * weight (+ bias),  rstd = 1/sqrt(var(h) + eps)
+ * per row of D elements; mean and var (the mean squared distance from the
+ * mean) are fp32 sums over the h that is stored.
+ *   x [T, D] of type x_type; add [T, D] bf16 or NULL; weight, bias [D] fp32
+ *   (bias may be NULL); y [T, D] bf16; h [T, D] of x's type, exactly when
+ *   `add` is given (else NULL); mean, rstd [T] fp32.
+ * 1 <= D <= 8192, any D; 0 <= T <= 2^24; eps >= 0 and finite.  h may be x
+ * itself; no other output may overlap an input. */
+moe_status moe_layer_norm_forward(const void* x, moe_dtype x_type, const void* add, const float* weight,
+                                  const float* bias, float eps, int32_t T, int32_t D, void* y, void* h,
+                                  float* mean, float* rstd, void* stream);
+
+/* Bytes of scratch moe_layer_norm_backward needs (0 for a bad shape). */
+size_t moe_layer_norm_backward_scratch_size(int32_t T, int32_t D);
+
+/* Gradients of sum(dy * y) (+ sum(d_stream * h)) for the forward above:
+ *   n = (x - mean) * rstd, p = dy * weight,
+ *   dx = rstd * (p - mean(p) - n * mean(p * n)) (+ d_stream)
+ *   dweight = sum_t dy * n,  dbias = sum_t dy
+ *   dy [T, D] bf16; x [T, D] of type x_type: the rows that were normalised
+ *   (h where the forward added); d_stream [T, D] of x's type or NULL: the
+ *   gradient that reaches the same rows past the norm; dx [T, D] of x's type;
+ *   dweight [D], dbias [D] fp32 (dbias may be NULL).  dx may be d_stream
+ *   itself.  The sums over tokens run in a fixed order (the same bits every
+ *   time on one device).  T = 0 writes zero weight gradients. */
+moe_status moe_layer_norm_backward(const void* dy, const void* x, moe_dtype x_type, const float* weight,
+                                   const float* mean, const float* rstd, const void* d_stream, int32_t T,
+                                   int32_t D, void* dx, float* dweight, float* dbias, void* scratch,
+                                   size_t scratch_bytes, void* stream);
+
 /* ---- Allocation-free variant ---- */
 
 /* moe_permute without a caller-provided scratch buffer, for callers that
