@@ -43,6 +43,22 @@ class MoeOptions(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+MAX_STACKS = 16
+MAX_NS_STEPS = 16
+
+
+class MoeMatrixStack(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+                ("weight_bf16", ctypes.c_void_p), ("count", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
+
+
+class MoeMuonParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("coefficients", ctypes.c_void_p)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -72,6 +88,9 @@ _SIGNATURES = {
     "moe_layer_norm_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "moe_layer_norm_backward_scratch_size": (_sz, [_i32, _i32]),
     "moe_layer_norm_backward": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_newton_schulz_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "moe_newton_schulz": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _sz, _vp]),
+    "moe_muon_step": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
     "moe_permute_noalloc": (_i32, [_vp, MoeDims, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_device_error": (_i32, []),
     "moe_selftest_wait_timeout": (_i32, [_i32, _vp, _vp]),

@@ -166,6 +166,40 @@ struct LayerNormBwdArgs {
 };
 cudaError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, cudaStream_t s);
 
+// ---- Newton-Schulz and the Muon step (newton_schulz.cu) ----
+// Matrices of the stacks, all of short side m and long side n; a tall stack
+// holds n x m matrices.
+struct NsStack {
+  const void* grad;    // fp32 or bf16
+  float* momentum;     // or nullptr: plain orthogonalisation
+  void* weight;        // the result (bf16), or the weights that move
+  void* weight_bf16;   // with fp32 weights: their bf16 copy, or nullptr
+  int first;           // index of its first matrix among all
+  int tall;
+};
+struct NsStacks {
+  int n;
+  NsStack s[MOE_MAX_STACKS];
+};
+enum NsKind { kNsPlain, kNsWeightBf16, kNsWeightF32 };
+struct NsOutput {
+  int kind;
+  float keep, step;  // w <- keep w - step o
+};
+struct NsProblem {
+  NsStacks stacks;
+  int count, m, n;
+  int grad_fp32;
+  float momentum;
+  int nesterov;
+  int steps;
+  float coeff[MOE_MAX_NS_STEPS][3];
+  float eps;
+  NsOutput out;
+};
+size_t ns_workspace_bytes(int count, int m, int n);
+cudaError_t launch_newton_schulz(const NsProblem& p, void* workspace, cudaStream_t s);
+
 // 2-D bf16 TMA descriptor of a row-major [rows, cols] matrix with a
 // {box_cols, box_rows} box: 128-byte swizzle (64-byte for 32-column boxes),
 // zero fill outside the tensor (grouped_gemm.cu).

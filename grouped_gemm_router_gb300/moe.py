@@ -441,6 +441,110 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
     return out
 
 
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _ns_coefficients(coefficients, steps):
+    """steps x 3 C floats from one (a, b, c) for every step, or one for each."""
+    c = list(coefficients)
+    if c and not hasattr(c[0], "__len__"):
+        c = [c] * steps
+    if len(c) != steps or any(len(t) != 3 for t in c):
+        raise ValueError(f"coefficients: one (a, b, c), or {steps} of them")
+    return (ctypes.c_float * (3 * steps))(*(float(v) for t in c for v in t))
+
+
+def newton_schulz_workspace_size(count, rows, cols) -> int:
+    n = int(lib.moe_newton_schulz_workspace_size(count, rows, cols))
+    if n == 0 and count > 0:
+        raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, "moe_newton_schulz_workspace_size")
+    return n
+
+
+def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, workspace=None):
+    """Orthogonalises each matrix of g [rows, cols] or [B, rows, cols] (bf16
+    or fp32): X = G / (|G| + eps), then `steps` times
+    X <- a X + (b A + c A A) X with A = X X^T (X^T X where rows > cols).
+    Returns bf16 of g's shape.  coefficients: one (a, b, c) or one for each
+    step.  workspace: a uint8 CUDA tensor of newton_schulz_workspace_size
+    bytes."""
+    kind = _STREAM_TYPES.get(g.dtype)
+    if kind is None:
+        raise ValueError(f"g must be torch.bfloat16 or torch.float32, got {g.dtype}")
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected [rows, cols] or [B, rows, cols]")
+    _need(g, "g", g.dtype)
+    count = g.shape[0] if g.dim() == 3 else 1
+    rows, cols = g.shape[-2:]
+    c = _ns_coefficients(coefficients, steps)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    _need(out, "out", torch.bfloat16, g.shape)
+    nbytes = newton_schulz_workspace_size(count, rows, cols)
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=g.device)
+    _need(workspace, "workspace", torch.uint8)
+    st = lib.moe_newton_schulz(g.data_ptr(), kind, count, rows, cols, steps, c, eps, out.data_ptr(),
+                               workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    check(st, "moe_newton_schulz")
+    return out
+
+
+def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, steps=5,
+              coefficients=NS_COEFFICIENTS, eps=1e-7, scale=None, weights_bf16=None, workspace=None):
+    """One Muon step, in place, on lists of weight matrices or stacks of them
+    ([rows, cols] or [B, rows, cols]; the expert weights W1, W3, W2 as they
+    are):
+        m <- momentum m + g;  u = g + momentum m (nesterov) or m
+        w <- (1 - lr weight_decay) w - lr scale newton_schulz(u)
+    weights: all bf16, or all fp32, then with weights_bf16 (a list, entries
+    may be None) the bf16 copies that the layer reads are written too; grads:
+    all fp32 (as moe_ffn_backward returns them) or all bf16; momenta: fp32.
+    scale: by default 0.2 sqrt(max(rows, cols)).  Matrices of the same shape
+    up to transposition are worked on together.  workspace: a uint8 CUDA
+    tensor of the largest newton_schulz_workspace_size among those groups."""
+    n = len(weights)
+    low = [None] * n if weights_bf16 is None else list(weights_bf16)
+    if not (len(grads) == len(momenta) == len(low) == n):
+        raise ValueError("weights, grads, momenta and weights_bf16 must have the same length")
+    if n == 0:
+        return
+    wtype, gtype = weights[0].dtype, grads[0].dtype
+    for t, name in ((wtype, "weights"), (gtype, "grads")):
+        if t not in _STREAM_TYPES:
+            raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t}")
+    groups = {}
+    for i, (w, g, m, b) in enumerate(zip(weights, grads, momenta, low)):
+        if w.dim() not in (2, 3):
+            raise ValueError(f"weights[{i}] has shape {tuple(w.shape)}, expected [rows, cols] or [B, rows, cols]")
+        _need(w, f"weights[{i}]", wtype)
+        _need(g, f"grads[{i}]", gtype, w.shape)
+        _need(m, f"momenta[{i}]", torch.float32, w.shape)
+        _need(b, f"weights_bf16[{i}]", torch.bfloat16, w.shape)
+        if b is not None and wtype != torch.float32:
+            raise ValueError("weights_bf16 are the copies of fp32 weights")
+        rows, cols = w.shape[-2:]
+        stack = N.MoeMatrixStack(w.data_ptr(), g.data_ptr(), m.data_ptr(), None if b is None else b.data_ptr(),
+                                 w.shape[0] if w.dim() == 3 else 1, rows, cols)
+        groups.setdefault((min(rows, cols), max(rows, cols)), []).append(stack)
+    c = _ns_coefficients(coefficients, steps)
+    calls = [(key, group[i:i + N.MAX_STACKS]) for key, group in groups.items()
+             for i in range(0, len(group), N.MAX_STACKS)]
+    sizes = [newton_schulz_workspace_size(sum(s.count for s in group), *key) for key, group in calls]
+    if workspace is None:
+        workspace = torch.empty(max(*sizes, 256), dtype=torch.uint8, device=weights[0].device)
+    _need(workspace, "workspace", torch.uint8)
+    if workspace.numel() < max(sizes):
+        raise N.MoeError(N.MOE_ERR_WORKSPACE, "moe_muon_step")
+    stream = torch.cuda.current_stream().cuda_stream
+    for key, group in calls:
+        p = N.MoeMuonParams(lr, momentum, weight_decay, 0.2 * key[1] ** 0.5 if scale is None else scale, eps,
+                            int(bool(nesterov)), steps, ctypes.addressof(c))
+        st = lib.moe_muon_step((N.MoeMatrixStack * len(group))(*group), len(group), _STREAM_TYPES[gtype],
+                               _STREAM_TYPES[wtype], ctypes.byref(p), workspace.data_ptr(), workspace.numel(), stream)
+        check(st, "moe_muon_step")
+
+
 def device_error() -> int:
     return int(lib.moe_device_error())
 

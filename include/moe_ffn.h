@@ -297,6 +297,60 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, moe_dtype x_ty
                                    int32_t D, void* dx, float* dweight, float* dbias, void* scratch,
                                    size_t scratch_bytes, void* stream);
 
+/* ---- Orthogonalised updates of the expert matrices ---- */
+
+#define MOE_MAX_STACKS 16    /* stacks in one moe_muon_step call */
+#define MOE_MAX_NS_STEPS 16  /* Newton-Schulz steps */
+#define MOE_MAX_MATRICES 4096 /* matrices in one call */
+
+/* Bytes of device workspace for `count` matrices of rows x cols (or of
+ * cols x rows); 0 for a bad shape. */
+size_t moe_newton_schulz_workspace_size(int32_t count, int32_t rows, int32_t cols);
+
+/* Newton-Schulz orthogonalisation of each of `count` matrices G [rows, cols]:
+ *   X = G / (|G|_F + eps)
+ *   steps times, with the step's (a, b, c):
+ *     A = X X^T;  X <- a X + (b A + c A A) X     (X^T X where rows > cols)
+ *   grad [count, rows, cols] of type grad_type; out [count, rows, cols] bf16;
+ *   coefficients: steps x 3 floats in host memory, read before the call
+ *   returns.  The products take fp16 operands and fp32 sums, the linear term
+ *   keeps X to 22 bits.  The coefficients have to keep the singular values of
+ *   X below 5 (those in common use keep them below 1.3).  A matrix with an
+ *   element that is no finite number, or with a sum of squares past fp32,
+ *   becomes NaN; the others of the stack do not.
+ * 1 <= rows, cols <= 8192; 0 <= count <= MOE_MAX_MATRICES;
+ * 1 <= steps <= MOE_MAX_NS_STEPS. */
+moe_status moe_newton_schulz(const void* grad, moe_dtype grad_type, int32_t count, int32_t rows, int32_t cols,
+                             int32_t steps, const float* coefficients, float eps, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* One stack of weight matrices of moe_muon_step. */
+typedef struct {
+  void* weight;        /* [count, rows, cols], updated in place */
+  const void* grad;    /* [count, rows, cols] */
+  float* momentum;     /* [count, rows, cols] fp32, updated in place */
+  void* weight_bf16;   /* with fp32 weights: [count, rows, cols] bf16, written
+                        * with the updated weights; or NULL */
+  int32_t count, rows, cols;
+} moe_matrix_stack;
+
+typedef struct {
+  float lr, momentum, weight_decay, scale, eps;
+  int32_t nesterov;           /* 0 or 1 */
+  int32_t steps;
+  const float* coefficients;  /* steps x 3, host memory */
+} moe_muon_params;
+
+/* One Muon step on n_stacks stacks of matrices, all of the same shape up to
+ * transposition (W1, W3 [E, D, F] and W2 [E, F, D] of a layer go together):
+ *   m <- momentum m + g;  u = g + momentum m (nesterov) or m
+ *   w <- (1 - lr weight_decay) w - lr scale NS(u)
+ * with NS as in moe_newton_schulz.  `stacks` is host memory, read before the
+ * call returns.  The workspace is that of the stacks' total count. */
+moe_status moe_muon_step(const moe_matrix_stack* stacks, int32_t n_stacks, moe_dtype grad_type,
+                         moe_dtype weight_type, const moe_muon_params* params, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* ---- Allocation-free variant ---- */
 
 /* moe_permute without a caller-provided scratch buffer, for callers that
