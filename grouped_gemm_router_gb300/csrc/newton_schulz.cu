@@ -12,24 +12,44 @@
 // Precision.  The products run on the tensor cores with fp16 operands and
 // fp32 sums.  fp16 and not bf16 because every operand has a known range
 // (singular values below about 1.3, so entries do too): scaled by a power of
-// two it holds 3 bits more at the same rate.  The term a X is not part of a
-// product and keeps X to 22 bits, as an fp16 value and the fp16 of what it
-// leaves (hi + lo).  It matters where G has less than full rank (an expert
-// with fewer tokens than rows): what rounding leaves outside the row space
-// grows by a in every step, 485-fold in five with a = 3.4445, and nothing
-// contracts it.  The products do not need more bits: there A is small.
-// Simulated on gradients of rank m/4: 1.1e-2 to 2.6e-2 off without lo,
-// 1.9e-3 with it, of which 1.7e-3 is the bf16 rounding of the result (bf16
-// operands: 0.9e-1 to 2e-1 without, 0.8e-2 with it).
+// two it holds 3 bits more at the same rate.  Two things are kept apart:
+//  * The term a X is not part of a product and keeps X to about 14 bits, as
+//    fp16 and what that leaves in e5m2 (hi + lo; not for the last step's
+//    X).  e5m2 is the upper byte of an fp16, so it needs no scale and is
+//    cheap to widen.  It matters where G has less than full rank (an expert
+//    with fewer tokens than rows): what rounding leaves outside the row space
+//    grows by a in every step, 485-fold in five with a = 3.4445, and nothing
+//    contracts it.  The products need no more bits there: A is small.
+//  * In the last two steps B is close to -2.7 I and cancels most of a X, so
+//    the rounding of its diagonal would be the largest error left.  There the
+//    diagonal goes from product to product in fp32 and the stored B has
+//    zeros in its place.  (Not before: it would split what cancels outside
+//    the row space into two differently rounded halves.)
+// Simulated 2-norm errors, of which the bf16 rounding of the result is
+// 1.66e-3: full rank 1.8e-3 to 2.1e-3 (2.3e-3 to 2.6e-3 without the fp32
+// diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 without lo; with bf16 operands
+// 0.9e-1 to 2e-1).
 //
 // A and B are symmetric: only the tiles on and below the diagonal are
 // computed, and each is stored twice, once transposed.
 //
-// Every product is a persistent kernel over 256 x 256 tiles, run by CTA pairs
-// (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM, operands by TMA with
-// the 128-byte swizzle).  Warp roles, the stage ring and the two accumulators
-// are those of grouped_gemm.cu.
+// All products of all steps are one persistent launch over 256 x 256 tiles,
+// run by CTA pairs (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM,
+// operands by TMA with the 128-byte swizzle).  The tiles of all (product,
+// matrix) are numbered product by product and pair p takes tiles p, p +
+// pairs, ...  A tile waits until the product that it reads, of its own
+// matrix only, is complete (a counter per product and matrix), so one
+// product's last tiles run beside the next one's first.  The order makes
+// every tile depend on lower-numbered ones only and the launch is
+// cooperative, so the waits end; they are bounded all the same.
+//
+// Warp roles (one CTA per SM):
+//   warp 0      TMA producer (one lane) -- both CTAs load their own halves
+//   warp 1      TMEM allocator; MMA issuer (one lane, leader only)
+//   warps 2-17  epilogue
+//   warp 18     counts the tiles whose results are in memory
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -48,41 +68,28 @@ constexpr int kAtomBytes = 128 * 64 * 2;       // 128 rows x 64 k
 constexpr int kOperandBytes = 2 * kAtomBytes;  // one operand's half of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 3;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kBox = 32;                       // output boxes: 32 rows x 32 columns
-constexpr int kBoxBytes = kBox * kBox * 2;
-constexpr int kWarpStage = 2 * kBoxBytes;      // staging bytes of an epilogue warp
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 96 + 32 * kEpiWarps;
+constexpr int kBox = 32;                       // columns an epilogue warp takes from TMEM at a time
+constexpr int kWarpStage = 16 * kBox * 4;      // its fp32 box in shared memory: half of those rows
 constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kWarpStage + 1024;
 constexpr uint32_t kTmemCols = 512;
 
-// Powers of two that the fp16 copies carry.  X: entries of 1 / sqrt(m n) at
-// the start (1.2e-4 for 8192 x 8192) up to about 1.3 stay normal numbers;
-// overflow only beyond 16.  A and B: entries of X X^T from 1 / m down, beyond
-// 32 overflow.
+// The power of two that the fp16 copies of X carry: entries of 1 / sqrt(m n)
+// at the start (1.2e-4 for 8192 x 8192) up to about 1.3 stay normal numbers;
+// overflow only beyond 16.  A and B carry none: their entries count beside
+// the a of a X, so fp16's smallest step, 6e-8, is enough.
 constexpr float kScaleX = 4096.f;
-constexpr float kScaleA = 2048.f;
-constexpr float kScaleLo = 2048.f;  // lo = (x - hi) * 2^11, the size of hi again
 
 constexpr int kNormChunks = 256;    // most partial sums of squares of a matrix
 constexpr int kNormThreads = 256;
 
-// What a launch computes: A = X X^T, B = b A + c A A, X <- a X + B X, or the
-// last of these with the results written.
-enum Stage { kGram, kPoly, kApply, kLast };
+// The products of a step: A = X X^T, B = b A + c A A, X <- a X + B X.
+enum Product { kGram, kPoly, kApply };
 
 // ---------------------------------------------------------------------------
 // The first two kernels: momentum and norm, then X_0
 // ---------------------------------------------------------------------------
-struct Source {
-  const void* grad;
-  float* momentum;
-};
-
-MOE_DEV float load_grad(const void* p, bool fp32, size_t i) {
-  return fp32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
-}
-
 // The stack that matrix `mat` belongs to.
 MOE_DEV int stack_of(const NsStacks& st, int mat) {
   int s = 0;
@@ -90,26 +97,72 @@ MOE_DEV int stack_of(const NsStacks& st, int mat) {
   return s;
 }
 
-// m <- mu m + g (with momentum), partial sums of squares of
-// u = g, m or g + mu m.  Block (c, mat) takes elements [c, c + 1) * chunk.
-__global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsStacks st, const int grad_fp32,
-                                                               const float mu, const int nesterov,
-                                                               const size_t elems, const size_t chunk,
-                                                               float* __restrict__ partial) {
+// VEC consecutive values (4: one 16- or 8-byte load).
+template <int VEC>
+MOE_DEV void load_vals(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+    v[0] = *p;
+  }
+}
+template <int VEC>
+MOE_DEV void load_vals(const uint16_t* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+  } else {
+    v[0] = bf16_lo(*p);
+  }
+}
+
+// m <- mu m + g (with momentum), partial sums of squares of u = g, m or
+// g + mu m.  Block (c, mat) takes elements [c, c + 1) * chunk; the first of a
+// matrix also clears its counters.
+template <typename GT, int VEC>
+__global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const __grid_constant__ NsStacks st, const float mu,
+                                                               const int nesterov, const size_t elems,
+                                                               const size_t chunk, float* __restrict__ partial,
+                                                               unsigned int* __restrict__ done, const int products) {
   __shared__ float red[kNormThreads / 32];
   const int mat = blockIdx.y;
   const NsStack& s = st.s[stack_of(st, mat)];
   const size_t base = static_cast<size_t>(mat - s.first) * elems;
+  const GT* g = static_cast<const GT*>(s.grad) + base;
+  float* mom = s.momentum ? s.momentum + base : nullptr;
   const size_t lo = blockIdx.x * chunk, hi = lo + chunk < elems ? lo + chunk : elems;
+  if (blockIdx.x == 0 && threadIdx.x < products) done[static_cast<size_t>(mat) * products + threadIdx.x] = 0;
   float q = 0.f;
-  for (size_t i = lo + threadIdx.x; i < hi; i += kNormThreads) {
-    float u = load_grad(s.grad, grad_fp32, base + i);
-    if (s.momentum != nullptr) {
-      const float m = fmaf(mu, s.momentum[base + i], u);
-      s.momentum[base + i] = m;
-      u = nesterov ? fmaf(mu, m, u) : m;
+  constexpr int kStep = kNormThreads * VEC, kUnroll = 4;
+  for (size_t i0 = lo + threadIdx.x * VEC; i0 < hi; i0 += kStep * kUnroll) {
+    float u[kUnroll][VEC], m[kUnroll][VEC];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t i = i0 + k * kStep;
+      if (i < hi) {
+        load_vals<VEC>(g + i, u[k]);
+        if (mom != nullptr) load_vals<VEC>(mom + i, m[k]);
+      }
     }
-    q = fmaf(u, u, q);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const size_t i = i0 + k * kStep;
+      if (i >= hi) continue;
+      if (mom != nullptr) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          m[k][j] = fmaf(mu, m[k][j], u[k][j]);
+          u[k][j] = nesterov ? fmaf(mu, m[k][j], u[k][j]) : m[k][j];
+        }
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(mom + i) = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
+        else
+          mom[i] = m[k][0];
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) q = fmaf(u[k][j], u[k][j], q);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
@@ -123,17 +176,74 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsStacks st
   griddep_launch_dependents();
 }
 
+MOE_DEV uint32_t pack_half2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+MOE_DEV float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+
+MOE_DEV float half_minus(uint32_t h, float c) {  // the low half of h, minus c, in fp32
+  float d;
+  asm("sub.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(static_cast<uint16_t>(h)), "f"(c));
+  return d;
+}
+
+// lo is kept with its sign turned, as hi - x: that is one instruction, and so
+// is x = hi - lo.
+MOE_DEV uint32_t pack_lo2(float a, float b, uint32_t h) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(half_minus(h, a), half_minus(h >> 16, b)), __NV_SATFINITE, __NV_E5M2);
+}
+
+// Four values from two packed pairs of hi and four bytes of lo.
+MOE_DEV void unpack_hi_lo4(uint32_t h01, uint32_t h23, uint32_t lo, float (&x)[4]) {
+  const float2 l01 = unpack_half2(__byte_perm(lo, 0, 0x1404)), l23 = unpack_half2(__byte_perm(lo, 0, 0x3424));
+  x[0] = half_minus(h01, l01.x), x[1] = half_minus(h01 >> 16, l01.y);
+  x[2] = half_minus(h23, l23.x), x[3] = half_minus(h23 >> 16, l23.y);
+}
+
 // X_0 in 64 x 64 tiles (zeros past the matrix), transposed for a tall one.
-__global__ void __launch_bounds__(256) ns_load_kernel(const NsStacks st, const int grad_fp32, const float mu,
+template <typename GT, int VEC>
+__global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ NsStacks st, const float mu,
                                                       const int nesterov, const int m, const int n, const int mp,
                                                       const int np, const int chunks, const float eps,
                                                       const float* __restrict__ partial, __half* __restrict__ hi,
-                                                      __half* __restrict__ lo) {
+                                                      uint8_t* __restrict__ lo) {
   __shared__ float tile[64][65];
   __shared__ float red[8];
   griddep_wait();  // the partial sums and the momentum come from the previous kernel
   const int mat = blockIdx.y;
   const NsStack& s = st.s[stack_of(st, mat)];
+  const int ti = blockIdx.x / (np / 64), tj = blockIdx.x - ti * (np / 64);
+  const size_t base = static_cast<size_t>(mat - s.first) * m * n;
+  const GT* g = static_cast<const GT*>(s.grad) + base;
+  const float* mom = s.momentum ? s.momentum + base : nullptr;
+  // source tile: rows and columns of the stack's own matrix
+  const int rows = s.tall ? n : m, cols = s.tall ? m : n;
+  const int r0 = (s.tall ? tj : ti) * 64, c0 = (s.tall ? ti : tj) * 64;
+  constexpr int kPerRow = 64 / VEC, kRows = 256 / kPerRow, kTurns = 64 / kRows;
+  const int tr = threadIdx.x / kPerRow, tc = threadIdx.x % kPerRow * VEC;
+  float u[kTurns][VEC];
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int row = r0 + tr + k * kRows, col = c0 + tc;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) u[k][j] = 0.f;
+    if (row < rows && col < cols) {
+      const size_t i = static_cast<size_t>(row) * cols + col;
+      if (mom == nullptr) {
+        load_vals<VEC>(g + i, u[k]);
+      } else {
+        load_vals<VEC>(mom + i, u[k]);
+        if (nesterov) {
+          float v[VEC];
+          load_vals<VEC>(g + i, v);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) u[k][j] = fmaf(mu, u[k][j], v[j]);
+        }
+      }
+    }
+  }
   float q = threadIdx.x < chunks ? partial[static_cast<size_t>(mat) * kNormChunks + threadIdx.x] : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
@@ -145,34 +255,27 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsStacks st, const i
   // a sum of squares that is no number or past fp32 makes the matrix NaN,
   // which the caller sees, and not a silent zero
   const float inv = q < INFINITY ? kScaleX / (sqrtf(q) + eps) : NAN;
-  const int ti = blockIdx.x / (np / 64), tj = blockIdx.x - ti * (np / 64);
-  const size_t base = static_cast<size_t>(mat - s.first) * m * n;
-  const int a = threadIdx.x >> 6, b = threadIdx.x & 63;
-  for (int r = a; r < 64; r += 4) {
-    // source row and column: (i, j) of X, or (j, i) of a tall matrix
-    const int row = (s.tall ? tj : ti) * 64 + r, col = (s.tall ? ti : tj) * 64 + b;
-    const int rows = s.tall ? n : m, cols = s.tall ? m : n;
-    float u = 0.f;
-    if (row < rows && col < cols) {
-      const size_t i = base + static_cast<size_t>(row) * cols + col;
-      u = load_grad(s.grad, grad_fp32, i);
-      if (s.momentum != nullptr) u = nesterov ? fmaf(mu, s.momentum[i], u) : s.momentum[i];
-      u *= inv;
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int r = tr + k * kRows, c = tc + j;
+      const float v = r0 + r < rows && c0 + c < cols ? u[k][j] * inv : 0.f;
+      if (s.tall)
+        tile[c][r] = v;
+      else
+        tile[r][c] = v;
     }
-    if (s.tall)
-      tile[b][r] = u;
-    else
-      tile[r][b] = u;
-  }
   __syncthreads();
-  for (int r = a; r < 64; r += 4) {
-    const float u = tile[r][b];
-    const __half h = __float2half_rn(u);
-    const size_t o = (static_cast<size_t>(mat) * mp + ti * 64 + r) * np + tj * 64 + b;
-    hi[o] = h;
-    lo[o] = __float2half_rn((u - __half2float(h)) * kScaleLo);
+  const int wr = threadIdx.x >> 4, wc = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int r = wr; r < 64; r += 16) {
+    const float a = tile[r][wc], b = tile[r][wc + 1], c = tile[r][wc + 2], d = tile[r][wc + 3];
+    const uint32_t h0 = pack_half2(a, b), h1 = pack_half2(c, d);
+    const size_t o = (static_cast<size_t>(mat) * mp + ti * 64 + r) * np + tj * 64 + wc;
+    *reinterpret_cast<uint2*>(hi + o) = make_uint2(h0, h1);
+    *reinterpret_cast<uint32_t*>(lo + o) = pack_lo2(a, b, h0) | (pack_lo2(c, d, h1) << 16);
   }
-  griddep_launch_dependents();
 }
 
 // ---------------------------------------------------------------------------
@@ -180,14 +283,22 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsStacks st, const i
 // ---------------------------------------------------------------------------
 struct GemmArgs {
   int count;        // matrices
+  int group;        // matrices whose products follow one another
+  int steps;
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
-  float a, b, c;    // the step's coefficients
-  const __half* A;  // [count, mp, mp]
-  const __half* hi;  // X, [count, np]
-  const __half* lo;  // or nullptr
-  int store_lo;
+  float coeff[MOE_MAX_NS_STEPS][3];
+  __half* A;        // [count, mp, mp]
+  __half* B;
+  __half* hi[2];    // X, [count, mp, np], in turns
+  uint8_t* lo[2];
+  float* diag;      // [count, mp]: B's diagonal where it is kept apart
+  unsigned int* done;  // [count, 3 * steps] halves of tiles that are complete
   NsOutput out;
+};
+
+struct NsMaps {
+  CUtensorMap X[2], A, B;  // operands: 128 rows x two 64-column blocks
 };
 
 struct Ctl {
@@ -198,37 +309,95 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  int ready;                // tiles whose operands the producer has seen complete
+  int written[kEpiWarps];   // tiles whose stores an epilogue warp has issued
 };
 
-// One item of work: tile (ti, tj) of matrix mat.
-struct Item {
-  int mat, ti, tj;
-};
-
-template <bool kTriangle>
-MOE_DEV Item item_of(const GemmArgs& p, int idx) {
-  const int nt = (p.mp + kTile - 1) / kTile;
-  Item it;
-  if (!kTriangle) {
-    const int ntn = (p.np + kTile - 1) / kTile;
-    it.mat = idx / (nt * ntn);
-    const int r = idx - it.mat * nt * ntn;
-    it.ti = r / ntn;
-    it.tj = r - it.ti * ntn;
-  } else {
-    const int tri = nt * (nt + 1) / 2;
-    it.mat = idx / tri;
-    int r = idx - it.mat * tri;
-    it.ti = 0;
-    while (r > it.ti) r -= ++it.ti;
-    it.tj = r;
+// Walks the tiles of one pair in the common order: groups of matrices, in a
+// group product after product, in a product matrix after matrix.
+struct Walk {
+  int first, g0, prod;     // number of the product's first tile, group, product
+  int mat, ti, tj;         // the tile
+  MOE_DEV Walk() : first(0), g0(0), prod(0) {}
+  // Tiles of one matrix in product `prod`.
+  MOE_DEV static int tiles(const GemmArgs& p, int prod) {
+    const int nt = (p.mp + kTile - 1) / kTile;
+    return prod % 3 == kApply ? nt * ((p.np + kTile - 1) / kTile) : nt * (nt + 1) / 2;
   }
-  return it;
+  // Moves to tile `idx`; false past the last one.  idx never decreases.
+  MOE_DEV bool to(const GemmArgs& p, int idx) {
+    for (;;) {
+      if (g0 >= p.count) return false;
+      const int per = tiles(p, prod), here = min(p.group, p.count - g0) * per;
+      if (idx < first + here) {
+        int r = idx - first;
+        mat = g0 + r / per;
+        r %= per;
+        if (prod % 3 == kApply) {
+          const int ntn = (p.np + kTile - 1) / kTile;
+          ti = r / ntn;
+          tj = r - ti * ntn;
+        } else {
+          ti = 0;
+          while (r > ti) r -= ++ti;
+          tj = r;
+        }
+        return true;
+      }
+      first += here;
+      if (++prod == 3 * p.steps) {
+        prod = 0;
+        g0 += p.group;
+      }
+    }
+  }
+};
+
+// A wait's turn: false when it is to be given up, because another thread of
+// the CTA has or because it has lasted too long.
+MOE_DEV bool keep_waiting(uint32_t it, uint64_t& t0, volatile int* abort, unsigned int* dev_err) {
+  if ((it & 63u) != 63u) return true;
+  if (*abort) return false;
+  const uint64_t t = global_timer_ns();
+  if (t0 == 0) t0 = t;
+  if (t - t0 <= MOE_WAIT_TIMEOUT_NS) return true;
+  *abort = 1;
+  atomicOr(dev_err, MOE_DEVERR_TIMEOUT);
+  return false;
 }
 
-__host__ __device__ __forceinline__ int item_count(bool triangle, int count, int mp, int np) {
-  const int nt = (mp + kTile - 1) / kTile;
-  return count * (!triangle ? nt * ((np + kTile - 1) / kTile) : nt * (nt + 1) / 2);
+// Waits until the product before `prod` of matrix `mat` is complete, and
+// makes its results visible to this thread's loads and TMA operations.
+MOE_DEV bool wait_product(const GemmArgs& p, int prod, int mat, volatile int* abort, unsigned int* dev_err) {
+  if (prod == 0) return true;  // X_0 comes from an earlier kernel
+  const unsigned int* c = p.done + static_cast<size_t>(mat) * 3 * p.steps + prod - 1;
+  const unsigned int target = Walk::tiles(p, prod - 1) * 2;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+    if (v >= target) break;
+    if (!keep_waiting(it, t0, abort, dev_err)) return false;
+  }
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  return true;
+}
+
+// Counters in shared memory, written by one thread each.
+MOE_DEV void count_store(int* c, int v) {
+  asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(c)), "r"(v) : "memory");
+}
+
+// Waits until *c is above i; returns it, or -1 when the wait was given up.
+// What the writer has acquired or stored before, this thread may read.
+MOE_DEV int wait_count(const int* c, int i, volatile int* abort, unsigned int* dev_err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(c)) : "memory");
+    if (v > i) return v;
+    if (!keep_waiting(it, t0, abort, dev_err)) return -1;
+  }
 }
 
 MOE_DEV void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
@@ -240,77 +409,402 @@ MOE_DEV void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar
       : "memory");
 }
 
-MOE_DEV uint32_t pack_half2(float lo, float hi) {
-  __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // Instruction descriptor of tcgen05.mma.kind::f16: fp16 A (K-major) and B
 // (K-major or N-major), fp32 D.
 MOE_DEV uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn_major) {
   return (1u << 4) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// 32 x 32 fp16 box (lane = row) into the staging buffer, 64-byte swizzle:
-// 16-byte chunk c of row r at chunk c ^ ((r / 2) % 4).
-MOE_DEV void stage_rows(uint8_t* buf, const float (&v)[32]) {
-  const uint32_t lane = lane_id();
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(pack_half2(v[8 * c], v[8 * c + 1]), pack_half2(v[8 * c + 2], v[8 * c + 3]),
-                   pack_half2(v[8 * c + 4], v[8 * c + 5]), pack_half2(v[8 * c + 6], v[8 * c + 7]));
+// An epilogue warp's fp32 box in shared memory, 16 rows x 32 columns: 16-byte
+// chunk c of row r at chunk c ^ (r % 8) ^ 4 (r / 8).  Every access below is
+// free of bank conflicts.  TMEM gives a lane a whole row; memory wants
+// neighbouring lanes on neighbouring columns, so the box is turned: lane l
+// then holds, for i = 0 and 1, the 8 columns from 8 (l % 4) of row 8 i + l / 4
+// (elements 8 i .. 8 i + 7), and what the epilogue reads and writes goes 8
+// rows of 64 bytes at a time.  (With each lane on its own row, 32 cache lines
+// an access, the epilogue of X took 12 us a tile where the product takes 5.)
+//
+// Addresses are one XOR and a constant away from three per-lane bases.  The
+// empty asm keeps the compiler from holding all of them in registers around
+// the loop over tiles.
+MOE_DEV uint32_t here(uint32_t base) {
+  asm volatile("" : "+r"(base));
+  return base;
 }
 
-// The same box transposed: column j of the box becomes row j.
-MOE_DEV void stage_cols(uint8_t* buf, const float (&v)[32]) {
-  const uint32_t lane = lane_id();
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    *reinterpret_cast<__half*>(buf + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2) =
-        __float2half_rn(v[j]);
+MOE_DEV void st_shared4(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
-// 32 consecutive halves as floats, through L2.
-MOE_DEV void load_halves(const __half* p, float (&v)[32]) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
+MOE_DEV void ld_shared4(uint32_t a, float& x, float& y, float& z, float& w) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(a) : "memory");
+}
+
+// Rows 16 h .. 16 h + 15 of the 32 that the warp holds in TMEM's layout.
+MOE_DEV void box_put_half(uint32_t buf, const uint32_t (&v)[32], int h) {
+  const uint32_t l = lane_id();
+  if ((l >> 4) == h) {
+    const uint32_t r = l & 15, x = here(buf + r * 128 + (((r & 7) ^ ((r >> 3) << 2)) << 4));
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint4 u = __ldcg(q + c);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int c = 0; c < 8; ++c)
+      st_shared4(x ^ (c << 4), __uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]), __uint_as_float(v[4 * c + 2]),
+                 __uint_as_float(v[4 * c + 3]));
+  }
+}
+
+MOE_DEV uint32_t box_lane(uint32_t buf) {
+  const uint32_t l = lane_id();
+  return here(buf + (l >> 2) * 128 + (((2 * (l & 3)) ^ (l >> 2)) << 4));
+}
+
+MOE_DEV void box_get(uint32_t buf, float (&v)[16]) {
+  const uint32_t x = box_lane(buf);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      v[8 * c + 2 * k] = f.x;
-      v[8 * c + 2 * k + 1] = f.y;
+  for (int k = 0; k < 4; ++k)
+    ld_shared4((x ^ (((k & 1) ^ ((k >> 1) << 2)) << 4)) + (k >> 1) * 1024, v[4 * k], v[4 * k + 1], v[4 * k + 2],
+               v[4 * k + 3]);
+}
+
+MOE_DEV void box_put(uint32_t buf, const float (&v)[16]) {
+  const uint32_t x = box_lane(buf);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    st_shared4((x ^ (((k & 1) ^ ((k >> 1) << 2)) << 4)) + (k >> 1) * 1024, v[4 * k], v[4 * k + 1], v[4 * k + 2],
+               v[4 * k + 3]);
+}
+
+// The box transposed: lane l holds, for i = 0 and 1, the 8 rows from 8 (l % 2)
+// of column 16 i + l / 2.
+MOE_DEV void box_get_turned(uint32_t buf, float (&v)[16]) {
+  const uint32_t l = lane_id(), c = l >> 1;
+  const uint32_t x = here(buf + (l & 1) * 1024 + (((c >> 2) ^ (4 * (l & 1))) << 4) + (c & 3) * 4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(v[8 * i + k])
+                   : "r"((x ^ (((4 * i) ^ k) << 4)) + k * 128)
+                   : "memory");
+}
+
+// Eight values as fp16.
+MOE_DEV void store_halves8(__half* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
+// The 8 columns of the lane's rows 8 i + l / 4, i = 0 .. 3, of a box as packed
+// pairs, through L2.
+MOE_DEV void load_halves(const __half* p, size_t pitch, uint32_t (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + 8 * i * pitch));
+    v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+  }
+}
+
+// What an epilogue warp knows of its tile.
+struct EpiTile {
+  int mat, step, cur;
+  bool mirror;          // below the diagonal of a symmetric product
+  bool late;            // B's diagonal is kept apart
+  int row0, col0;       // the warp's first row and column
+  size_t at;            // this lane's first element, in the output
+  uint32_t taddr;       // its accumulator
+  uint32_t tfull, tphase, tempty;
+  uint32_t buf;         // the warp's box (shared memory)
+  volatile int* abort_flag;
+  unsigned int* dev_err;
+};
+
+// The accumulator is there; false when the wait was given up.
+MOE_DEV bool wait_acc(const EpiTile& t) {
+  const bool ok = mbar_wait_cluster(t.tfull, t.tphase, t.abort_flag, t.dev_err);
+  tc_fence_after_sync();
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// It has been read: the MMA issuer may use it again.  Relaxed, because the
+// values are in registers by then and nothing else is handed over: a release
+// waits for the stores before it (1500 cycles).
+MOE_DEV void release(const EpiTile& t) {
+  tc_fence_before_sync();
+  __syncwarp();
+  if (lane_id() == 0)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(t.tempty) : "memory");
+}
+
+// The four epilogues, on two boxes of 32 columns.  Each asks for what it reads
+// (A, or X's hi and lo) of the first before it waits for the accumulator and
+// of the second after the first; sixteen warps with little in flight each
+// hide the rest.  Little may spill here: shared memory leaves the L1 cache 28
+// KB, so spilled registers come back from L2.  (Eight warps that asked for
+// all of it at once: 0.9 KB a thread spilled, 2300 cycles a box.)  For the
+// same reason every load into registers is made without a condition:
+// registers written under one stay live around the loop over tiles.
+
+// A tile whose part for this warp lies outside the matrix.
+MOE_DEV bool epilogue_none(const EpiTile& t) {
+  const bool ok = wait_acc(t);
+  release(t);
+  return ok;
+}
+
+// Takes box b from TMEM; after the last one the accumulator is free.
+MOE_DEV void take(const EpiTile& t, int b, uint32_t (&acc)[32]) {
+  tmem_ld_32cols(t.taddr + b * kBox, acc);
+  tmem_ld_wait();
+  if (b == 1) release(t);
+}
+
+// Half a box into the lanes' 8-column pieces.
+MOE_DEV void turn(const EpiTile& t, const uint32_t (&acc)[32], int h, float (&v)[16]) {
+  __syncwarp();
+  box_put_half(t.buf, acc, h);
+  __syncwarp();
+  box_get(t.buf, v);
+}
+
+// Half a box of a symmetric product, from shared memory to its mirror place.
+MOE_DEV void store_mirror(__half* out, const GemmArgs& p, const EpiTile& t, int b, int h, float scale) {
+  const uint32_t l = lane_id();
+  float v[16];
+  box_get_turned(t.buf, v);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] *= scale;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    store_halves8(out + (static_cast<size_t>(t.mat) * p.mp + t.col0 + b * kBox + 16 * i + (l >> 1)) * p.mp + t.row0 +
+                      16 * h + 8 * (l & 1),
+                  v + 8 * i);
+}
+
+// A = X X^T.
+MOE_DEV bool epilogue_gram(const GemmArgs& p, const EpiTile& t) {
+  if (!wait_acc(t)) return false;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t acc[32];
+    take(t, b, acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[16];
+      turn(t, acc, h, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] *= 1.f / (kScaleX * kScaleX);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) store_halves8(p.A + t.at + b * kBox + (16 * h + 8 * i) * p.mp, v + 8 * i);
+      if (t.mirror) store_mirror(p.A, p, t, b, h, 1.f / (kScaleX * kScaleX));
     }
   }
+  return true;
 }
 
-// Element (row, col) of the stack's own matrix: the orthogonalised value o
-// is the result, or moves the weight.
-MOE_DEV void write_result(const NsOutput& o, const NsStack& s, size_t at, float v) {
-  if (o.kind == kNsPlain) {
-    static_cast<uint16_t*>(s.weight)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-  } else if (o.kind == kNsWeightBf16) {
-    uint16_t* w = static_cast<uint16_t*>(s.weight) + at;
-    *w = static_cast<uint16_t>(pack_bf16x2(fmaf(bf16_lo(*w), o.keep, -o.step * v), 0.f));
-  } else {
-    float* w = static_cast<float*>(s.weight) + at;
-    const float t = fmaf(*w, o.keep, -o.step * v);
-    *w = t;
-    if (s.weight_bf16 != nullptr) static_cast<uint16_t*>(s.weight_bf16)[at] = static_cast<uint16_t>(pack_bf16x2(t, 0.f));
+// B = b A + c A A.
+MOE_DEV bool epilogue_poly(const GemmArgs& p, const EpiTile& t) {
+  const uint32_t l = lane_id();
+  uint32_t pre[2][16];
+  load_halves(p.A + t.at, p.mp, pre[0]);
+  const float cb = p.coeff[t.step][1], cc = p.coeff[t.step][2];
+  if (!wait_acc(t)) return false;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t acc[32];
+    take(t, b, acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[16];
+      turn(t, acc, h, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 a = unpack_half2(pre[b][8 * h + j]);
+        v[2 * j] = fmaf(cc, v[2 * j], cb * a.x);
+        v[2 * j + 1] = fmaf(cc, v[2 * j + 1], cb * a.y);
+      }
+      // the lane's row 16 h + 8 i + l / 4 meets its columns where 2 h + i = l % 4
+      if (t.late && t.row0 == t.col0 + b * kBox) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if ((l & 3) == 2 * h + j / 8 && (l >> 2) == j % 8) {
+            p.diag[static_cast<size_t>(t.mat) * p.mp + t.row0 + 16 * h + j] = v[j];
+            v[j] = 0.f;
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) store_halves8(p.B + t.at + b * kBox + (16 * h + 8 * i) * p.mp, v + 8 * i);
+      if (t.mirror) {
+        __syncwarp();
+        box_put(t.buf, v);
+        __syncwarp();
+        store_mirror(p.B, p, t, b, h, 1.f);
+      }
+    }
+    if (b == 0) load_halves(p.A + t.at + kBox, p.mp, pre[1]);
+  }
+  return true;
+}
+
+// a plus, where it is kept apart, B's diagonal, for the lane's four rows.
+MOE_DEV void row_factors(const GemmArgs& p, const EpiTile& t, float (&ca)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ca[i] = p.coeff[t.step][0];
+    if (t.late) ca[i] += __ldcg(p.diag + static_cast<size_t>(t.mat) * p.mp + t.row0 + 8 * i + (lane_id() >> 2));
   }
 }
 
-// mapP: the left operand, mapQ: the right one, mapOut: the product's fp16
-// output (A, B or X's hi), mapLo: X's lo.
-template <Stage kStage>
+// X <- a X + B X.
+MOE_DEV bool epilogue_apply(const GemmArgs& p, const EpiTile& t) {
+  uint32_t hi[2][16], lo[2][8];
+  auto load = [&](int b) {
+    load_halves(p.hi[t.cur] + t.at + b * kBox, p.np, hi[b]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2 u = __ldcg(reinterpret_cast<const uint2*>(p.lo[t.cur] + t.at + b * kBox + 8 * i * p.np));
+      lo[b][2 * i] = u.x, lo[b][2 * i + 1] = u.y;
+    }
+  };
+  load(0);
+  float ca[4];
+  row_factors(p, t, ca);
+  if (!wait_acc(t)) return false;
+  const bool keep_lo = t.step + 2 < p.steps;  // the last step's X has none
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t acc[32];
+    take(t, b, acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[16];
+      turn(t, acc, h, v);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * h + i;  // row 8 r + l / 4
+        uint32_t w[4], n[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x[4];
+          unpack_hi_lo4(hi[b][4 * r + 2 * j], hi[b][4 * r + 2 * j + 1], lo[b][2 * r + j], x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = fmaf(ca[r], x[k], v[8 * i + 4 * j + k]);
+          w[2 * j] = pack_half2(x[0], x[1]);
+          w[2 * j + 1] = pack_half2(x[2], x[3]);
+          n[j] = pack_lo2(x[0], x[1], w[2 * j]) | (pack_lo2(x[2], x[3], w[2 * j + 1]) << 16);
+        }
+        const size_t at = t.at + b * kBox + 8 * r * p.np;
+        *reinterpret_cast<uint4*>(p.hi[t.cur ^ 1] + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (keep_lo) *reinterpret_cast<uint2*>(p.lo[t.cur ^ 1] + at) = make_uint2(n[0], n[1]);
+      }
+    }
+    if (b == 0) load(1);
+  }
+  return true;
+}
+
+// Eight consecutive bf16 weights (stop of them inside the row), packed.
+MOE_DEV void load_bf16(const void* base, size_t el, int stop, bool vec, uint32_t (&w)[4]) {
+  const uint16_t* p = static_cast<const uint16_t*>(base) + el;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = 0;
+  if (vec) {
+    if (stop > 0) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < stop) w[k / 2] |= static_cast<uint32_t>(__ldcs(p + k)) << (16 * (k & 1));
+  }
+}
+
+MOE_DEV void store_bf16(void* base, size_t el, int stop, bool vec, const float* v) {
+  uint16_t* p = static_cast<uint16_t*>(base) + el;
+  if (vec) {
+    if (stop > 0)
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < stop) p[k] = static_cast<uint16_t>(pack_bf16x2(v[k], 0.f));
+  }
+}
+
+// The last product: o is the result, or moves the weights, in runs of 8
+// elements of the stack's own rows.
+MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile& t) {
+  const uint32_t l = lane_id();
+  uint32_t hi[2][16];
+  load_halves(p.hi[t.cur] + t.at, p.np, hi[0]);
+  float ca[4];
+  row_factors(p, t, ca);
+  const NsStack& s = st.s[stack_of(st, t.mat)];
+  const size_t base = static_cast<size_t>(t.mat - s.first) * p.m * p.n;
+  const int rows = s.tall ? p.n : p.m, cols = s.tall ? p.m : p.n;  // the stack's own
+  const bool vec = cols % 8 == 0;                                  // runs start on 16 bytes and end inside
+  if (!wait_acc(t)) return false;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t acc[32];
+    take(t, b, acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the lane's two runs in the stack's own matrix
+      const int r0 = s.tall ? t.col0 + b * kBox + (l >> 1) : t.row0 + 16 * h + (l >> 2);
+      const int c0 = s.tall ? t.row0 + 16 * h + 8 * (l & 1) : t.col0 + b * kBox + 8 * (l & 3);
+      const int rstep = s.tall ? 16 : 8;
+      uint32_t w[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int stop = r0 + rstep * i < rows && p.out.kind == kNsWeightBf16 ? min(8, cols - c0) : 0;
+        load_bf16(s.weight, base + static_cast<size_t>(r0 + rstep * i) * cols + c0, stop, vec, w[i]);
+      }
+      float v[16];
+      turn(t, acc, h, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 x = unpack_half2(hi[b][8 * h + j]);
+        const float f = ca[2 * h + j / 4];
+        v[2 * j] = fmaf(f, x.x, v[2 * j]) * (1.f / kScaleX);
+        v[2 * j + 1] = fmaf(f, x.y, v[2 * j + 1]) * (1.f / kScaleX);
+      }
+      if (s.tall) {
+        __syncwarp();
+        box_put(t.buf, v);
+        __syncwarp();
+        box_get_turned(t.buf, v);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const size_t at = base + static_cast<size_t>(r0 + rstep * i) * cols + c0;
+        const int stop = r0 + rstep * i < rows ? min(8, cols - c0) : 0;
+        float* o = v + 8 * i;
+        if (p.out.kind == kNsWeightF32) {
+          float* d = static_cast<float*>(s.weight) + at;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < stop) d[k] = o[k] = fmaf(d[k], p.out.keep, -p.out.step * o[k]);
+          if (s.weight_bf16 != nullptr) store_bf16(s.weight_bf16, at, stop, vec, o);
+        } else {
+          if (p.out.kind == kNsWeightBf16) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = fmaf(k & 1 ? bf16_hi(w[i][k / 2]) : bf16_lo(w[i][k / 2]), p.out.keep, -p.out.step * o[k]);
+          }
+          store_bf16(s.weight, at, stop, vec, o);
+        }
+      }
+    }
+    if (b == 0) load_halves(p.hi[t.cur] + t.at + kBox, p.np, hi[1]);
+  }
+  return true;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    ns_gemm_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
-                   const __grid_constant__ CUtensorMap mapOut, const __grid_constant__ CUtensorMap mapLo,
-                   const __grid_constant__ GemmArgs p, const __grid_constant__ NsStacks st,
-                   unsigned int* const dev_err) {
+    ns_products_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ GemmArgs p,
+                       const __grid_constant__ NsStacks st, unsigned int* const dev_err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -320,14 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = static_cast<int>(cluster_id_x()), npairs = static_cast<int>(num_clusters_x());
-  constexpr bool kTriangle = kStage == kGram || kStage == kPoly;
-  const int K = kStage == kGram ? p.np : p.mp;
-  const int nkb = (K + kBK - 1) / kBK;
-  const int total = item_count(kTriangle, p.count, p.mp, p.np);
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&mapP);
-    tma_prefetch_desc(&mapQ);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl.full[i]), 1);
       mbar_init(smem_u32(&ctl.empty[i]), 1);
@@ -338,6 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
+    ctl.ready = 0;
+    for (int w = 0; w < kEpiWarps; ++w) ctl.written[w] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -345,8 +835,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
     tc_fence_before_sync();
   }
-  griddep_launch_dependents();
-  griddep_wait();  // the operands come from earlier kernels
   cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem_base = ctl.tmem_base;
@@ -356,11 +844,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== TMA producer (both CTAs) =====================
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_normal();
-      int stage = 0, issued = 0;
+      int stage = 0, issued = 0, i = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int idx = pair; idx < total && ok; idx += npairs) {
-        const Item it = item_of<kTriangle>(p, idx);
+      Walk t;
+      for (int idx = pair; ok && t.to(p, idx); idx += npairs) {
+        const int kind = t.prod % 3, cur = (t.prod / 3) & 1;
+        if (!wait_product(p, t.prod, t.mat, abort_flag, dev_err)) {
+          ok = false;
+          break;
+        }
+        count_store(&ctl.ready, ++i);
+        const CUtensorMap* mp = kind == kGram ? &maps.X[cur] : kind == kPoly ? &maps.A : &maps.B;
+        const CUtensorMap* mq = kind == kPoly ? &maps.A : &maps.X[cur];
+        const int nkb = ((kind == kGram ? p.np : p.mp) + kBK - 1) / kBK;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&ctl.empty[stage]), phase ^ 1u, abort_flag, dev_err)) {
             ok = false;
@@ -370,11 +867,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sp = smem_base + stage * kStageBytes, sq = sp + kOperandBytes;
           // both CTAs' boxes count in full, rows and k past the matrix are zeros
           if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), 2 * kStageBytes);
-          tma_load_4d_pair(sp, &mapP, bar, 0, it.ti * kTile + 128 * rank, kb * (kBK / 64), it.mat, policy);
-          if (!kTriangle)
-            tma_load_4d_pair(sq, &mapQ, bar, 0, kb * kBK, it.tj * (kTile / 64) + 2 * rank, it.mat, policy);
+          tma_load_4d_pair(sp, mp, bar, 0, t.ti * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
+          if (kind == kApply)
+            tma_load_4d_pair(sq, mq, bar, 0, kb * kBK, t.tj * (kTile / 64) + 2 * rank, t.mat, policy);
           else
-            tma_load_4d_pair(sq, &mapQ, bar, 0, it.tj * kTile + 128 * rank, kb * (kBK / 64), it.mat, policy);
+            tma_load_4d_pair(sq, mq, bar, 0, t.tj * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
           ++issued;
           if (++stage == kStages) {
             stage = 0;
@@ -384,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && leader) {
         // Let the copies already in flight land before the CTA exits.
-        for (int i = 0; i < kStages && i < issued; ++i) {
+        for (int k = 0; k < kStages && k < issued; ++k) {
           if (--stage < 0) {
             stage = kStages - 1;
             phase ^= 1u;
@@ -398,15 +895,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ===================== MMA issuer (leader only) =====================
     if (lane == 0 && leader) {
-      constexpr bool n_major = !kTriangle;
-      const uint32_t idesc = idesc_f16_f32(kTile, kTile, n_major ? 1u : 0u);
       int stage = 0, i = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int idx = pair; idx < total && ok; idx += npairs, ++i) {
+      Walk t;
+      for (int idx = pair; ok && t.to(p, idx); idx += npairs, ++i) {
         const int buf = i & 1;
         if (!mbar_wait_cluster(smem_u32(&ctl.tempty[buf]), ((i >> 1) & 1) ^ 1u, abort_flag, dev_err)) break;
         tc_fence_after_sync();
+        const bool n_major = t.prod % 3 == kApply;
+        const uint32_t idesc = idesc_f16_f32(kTile, kTile, n_major ? 1u : 0u);
+        const int K = t.prod % 3 == kGram ? p.np : p.mp;
+        const int nkb = (K + kBK - 1) / kBK;
         const uint32_t d = tmem_base + buf * kTile;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&ctl.full[stage]), phase, abort_flag, dev_err)) {
@@ -432,121 +932,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         umma_commit_pair(smem_u32(&ctl.tfull[buf]), 0x3);
       }
+      // All MMAs issued by this thread are complete once `drain` flips.
       umma_commit_pair(smem_u32(&ctl.drain), 0x1);
       volatile int local_abort = 0;
       mbar_wait_cluster(smem_u32(&ctl.drain), 0, &local_abort, dev_err);
     }
     __syncwarp();
+  } else if (warp == 2 + kEpiWarps) {
+    // ===================== completion (both CTAs) =====================
+    // Once the epilogue warps have issued a tile's stores, waits until these
+    // are in memory and counts the tile: 2000 to 5000 cycles that the
+    // epilogue warps spend on the next tile.
+    int i = 0, upto = 0;
+    Walk t;
+    for (int idx = pair; t.to(p, idx); idx += npairs, ++i) {
+      if (i >= upto) {  // all that every warp has issued by now, with one fence
+        int v = lane < kEpiWarps ? wait_count(&ctl.written[lane], i, abort_flag, dev_err) : 0x7fffffff;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (v < 0) break;
+        upto = v;
+        if (lane == 0) {
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+          __threadfence();
+        }
+      }
+      if (lane == 0 && t.prod + 1 < 3 * p.steps)
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + static_cast<size_t>(t.mat) * 3 * p.steps + t.prod)
+                     : "memory");
+    }
   } else {
     // ===================== epilogue (both CTAs) =====================
-    // Warp w: TMEM lanes 32 (w % 4) .. + 31 and half (w - 2) / 4 of the columns.
+    // Warp w: TMEM lanes 32 (w % 4) .. + 31 and columns 64 ((w - 2) / 4) ..
+    // + 63, in two boxes of 32 columns.
     const int q = warp & 3, part = (warp - 2) >> 2;
     const uint32_t tempty0 = map_to_cta(smem_u32(&ctl.tempty[0]), 0);
     const uint32_t tempty1 = map_to_cta(smem_u32(&ctl.tempty[1]), 0);
-    uint8_t* buf0 = smem + kStages * kStageBytes + (warp - 2) * kWarpStage;
-    uint8_t* buf1 = buf0 + kBoxBytes;
-    const int ncols = kTriangle ? p.mp : p.np;
-    // boxes read from TMEM at a time: all four where the epilogue holds
-    // little else (the accumulator is free again the sooner), else two
-    constexpr int kBurst = kStage == kGram ? 4 : 2;
+    const uint32_t box = smem_base + kStages * kStageBytes + (warp - 2) * kWarpStage;
     int i = 0;
-    for (int idx = pair; idx < total; idx += npairs, ++i) {
-      const Item it = item_of<kTriangle>(p, idx);
-      const int buf = i & 1;
-      const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[buf]), (i >> 1) & 1, abort_flag, dev_err);
+    Walk t;
+    for (int idx = pair; t.to(p, idx); idx += npairs, ++i) {
+      const int kind = t.prod % 3, step = t.prod / 3, buf = i & 1;
+      EpiTile e;
+      e.mat = t.mat, e.step = step, e.cur = step & 1;
+      e.mirror = t.ti != t.tj;
+      e.late = step + 2 >= p.steps;
+      e.row0 = t.ti * kTile + 128 * static_cast<int>(rank) + q * 32;
+      e.col0 = t.tj * kTile + part * 2 * kBox;
+      const int ncols = kind == kApply ? p.np : p.mp;
+      e.at = (static_cast<size_t>(t.mat) * p.mp + e.row0 + (lane >> 2)) * ncols + e.col0 + 8 * (lane & 3);
+      e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 2 * kBox;
+      e.tfull = smem_u32(&ctl.tfull[buf]);
+      e.tphase = (i >> 1) & 1;
+      e.tempty = buf ? tempty1 : tempty0;
+      e.buf = box;
+      e.abort_flag = abort_flag;
+      e.dev_err = dev_err;
+      bool got = true;
+      if (lane == 0) got = wait_count(&ctl.ready, i, abort_flag, dev_err) > 0;
       if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after_sync();
-      const int row0 = it.ti * kTile + 128 * static_cast<int>(rank) + q * 32;
-      const int col0 = it.tj * kTile + part * 128;
-      // padded sizes are multiples of 64: a box is inside or outside
-      const int nbox = row0 < p.mp && col0 < ncols ? min(4, (ncols - col0) / kBox) : 0;
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 128;
-      uint32_t acc[kBurst][32];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b % kBurst == 0) {
-#pragma unroll
-          for (int j = 0; j < kBurst; ++j)
-            if (b + j < nbox) tmem_ld_32cols(taddr + (b + j) * kBox, acc[j]);
-          if (b < nbox) tmem_ld_wait();
-          if (b + kBurst >= 4) {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
-          }
-        }
-        if (b >= nbox) continue;
-        const int col = col0 + b * kBox;
-        float v[32];
-        if constexpr (kStage == kGram) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc[b % kBurst][j]) * (kScaleA / (kScaleX * kScaleX));
-        } else if constexpr (kStage == kPoly) {
-          load_halves(p.A + (static_cast<size_t>(it.mat) * p.mp + row0 + lane) * p.mp + col, v);
-          const float c = p.c / kScaleA;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = fmaf(c, __uint_as_float(acc[b % kBurst][j]), p.b * v[j]);
-        } else {
-          const size_t at = (static_cast<size_t>(it.mat) * p.mp + row0 + lane) * p.np + col;
-          load_halves(p.hi + at, v);
-          if (p.lo != nullptr) {
-            float l[32];
-            load_halves(p.lo + at, l);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(1.f / kScaleLo, l[j], v[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = fmaf(p.a, v[j], __uint_as_float(acc[b % kBurst][j]) * (1.f / kScaleA));
-        }
-        bulk_wait_group_read0();  // lane 0's stores have read the buffers
-        __syncwarp();
-        if constexpr (kStage == kLast) {
-          // results, 32 consecutive elements of the stack's own rows at a time
-          const NsStack& s = st.s[stack_of(st, it.mat)];
-          const size_t base = static_cast<size_t>(it.mat - s.first) * p.m * p.n;
-          if (s.tall) {  // column j of the box is a run of row j: lanes are consecutive
-            if (row0 + lane < p.m) {
-#pragma unroll 4
-              for (int j = 0; j < 32; ++j)
-                if (col + j < p.n)
-                  write_result(p.out, s, base + static_cast<size_t>(col + j) * p.m + row0 + lane, v[j] * (1.f / kScaleX));
-            }
-          } else {  // turn the box so that lanes are columns
-            float* f = reinterpret_cast<float*>(buf0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[lane * 32 + (j ^ lane)] = v[j];
-            __syncwarp();
-            if (col + lane < p.n) {
-#pragma unroll 4
-              for (int r = 0; r < 32; ++r)
-                if (row0 + r < p.m)
-                  write_result(p.out, s, base + static_cast<size_t>(row0 + r) * p.n + col + lane,
-                               f[r * 32 + (lane ^ r)] * (1.f / kScaleX));
-            }
-            __syncwarp();
-          }
-        } else {
-          stage_rows(buf0, v);
-          const bool mirror = kTriangle && it.ti != it.tj;
-          if (mirror) stage_cols(buf1, v);
-          const bool low = kStage == kApply && p.store_lo;
-          if (low) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = (v[j] - __half2float(__float2half_rn(v[j]))) * kScaleLo;
-            stage_rows(buf1, v);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&mapOut, smem_u32(buf0), col, row0, it.mat);
-            if (mirror) tma_store_3d(&mapOut, smem_u32(buf1), row0, col, it.mat);
-            if (low) tma_store_3d(&mapLo, smem_u32(buf1), col, row0, it.mat);
-            bulk_commit_group();
-          }
-        }
-      }
+      // padded sizes are multiples of 64: the warp's part is inside or outside
+      if (e.row0 >= p.mp || e.col0 >= ncols)
+        got = epilogue_none(e);
+      else if (kind == kGram)
+        got = epilogue_gram(p, e);
+      else if (kind == kPoly)
+        got = epilogue_poly(p, e);
+      else if (step + 1 < p.steps)
+        got = epilogue_apply(p, e);
+      else
+        got = epilogue_last(p, st, e);
+      if (!got) break;
+      __syncwarp();
+      if (lane == 0) count_store(&ctl.written[warp - 2], i + 1);
     }
-    if (lane == 0) bulk_wait_group0();
     __syncwarp();
   }
   tc_fence_before_sync();
@@ -564,8 +1023,10 @@ inline size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255);
 inline int pad64(int v) { return (v + 63) / 64 * 64; }
 
 struct Buffers {
-  float* partial;
-  __half *hi[2], *lo[2], *A, *B;
+  float *partial, *diag;
+  unsigned int* done;
+  __half *hi[2], *A, *B;
+  uint8_t* lo[2];
   size_t bytes;
 };
 
@@ -577,10 +1038,12 @@ Buffers carve(void* base, int count, int mp, int np) {
     off += align_up(bytes);
     return base ? static_cast<char*>(base) + o : nullptr;
   };
-  const size_t x = static_cast<size_t>(count) * mp * np * 2, a = static_cast<size_t>(count) * mp * mp * 2;
+  const size_t x = static_cast<size_t>(count) * mp * np, a = static_cast<size_t>(count) * mp * mp * 2;
   w.partial = reinterpret_cast<float*>(take(static_cast<size_t>(count) * kNormChunks * 4));
-  for (int i = 0; i < 2; ++i) w.hi[i] = reinterpret_cast<__half*>(take(x));
-  for (int i = 0; i < 2; ++i) w.lo[i] = reinterpret_cast<__half*>(take(x));
+  w.done = reinterpret_cast<unsigned int*>(take(static_cast<size_t>(count) * 3 * MOE_MAX_NS_STEPS * 4));
+  w.diag = reinterpret_cast<float*>(take(static_cast<size_t>(count) * mp * 4));
+  for (int i = 0; i < 2; ++i) w.hi[i] = reinterpret_cast<__half*>(take(2 * x));
+  for (int i = 0; i < 2; ++i) w.lo[i] = reinterpret_cast<uint8_t*>(take(x));
   w.A = reinterpret_cast<__half*>(take(a));
   w.B = reinterpret_cast<__half*>(take(a));
   w.bytes = off;
@@ -610,13 +1073,9 @@ cudaError_t setup(PFN_cuTensorMapEncodeTiled_v12000* encode, int* pairs) {
     g_setup.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   if (g_setup.pairs[dev] == 0) {
-    const void* fns[] = {
-        reinterpret_cast<const void*>(ns_gemm_kernel<kGram>), reinterpret_cast<const void*>(ns_gemm_kernel<kPoly>),
-        reinterpret_cast<const void*>(ns_gemm_kernel<kApply>), reinterpret_cast<const void*>(ns_gemm_kernel<kLast>)};
-    for (const void* fn : fns) {
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-      if (e != cudaSuccess) return e;
-    }
+    const void* fn = reinterpret_cast<const void*>(ns_products_kernel);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
     int sms = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -632,7 +1091,7 @@ cudaError_t setup(PFN_cuTensorMapEncodeTiled_v12000* encode, int* pairs) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, fns[kGram], &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     g_setup.pairs[dev] = n;
@@ -659,40 +1118,18 @@ cudaError_t operand_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, c
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// [count, rows, cols] fp16 for stores of 32 x 32 boxes.
-cudaError_t store_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* p, int count, int rows,
-                      int cols) {
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows) * cols * 2};
-  cuuint32_t box[3] = {kBox, kBox, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-template <Stage kStage>
-cudaError_t launch_gemm(int pairs, const CUtensorMap& P, const CUtensorMap& Q, const CUtensorMap& out,
-                        const CUtensorMap& lo, const GemmArgs& a, const NsStacks& st, unsigned int* err,
-                        cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * std::min(pairs, item_count(kStage == kGram || kStage == kPoly, a.count, a.mp, a.np)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, ns_gemm_kernel<kStage>, P, Q, out, lo, a, st, err);
-  note_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
+template <typename GT, int VEC>
+cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, cudaStream_t s) {
+  const size_t elems = static_cast<size_t>(pr.m) * pr.n;
+  size_t chunk = (elems + kNormChunks - 1) / kNormChunks;
+  chunk = std::max<size_t>((chunk + 3) / 4 * 4, 8192);
+  const int chunks = static_cast<int>((elems + chunk - 1) / chunk);
+  cudaError_t e = launch_kernel(ns_norm_kernel<GT, VEC>, dim3(chunks, pr.count), dim3(kNormThreads), 0, s, false,
+                                pr.stacks, pr.momentum, pr.nesterov, elems, chunk, w.partial, w.done, 3 * pr.steps);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(ns_load_kernel<GT, VEC>, dim3((mp / 64) * (np / 64), pr.count), dim3(256), 0, s, true,
+                       pr.stacks, pr.momentum, pr.nesterov, pr.m, pr.n, mp, np, chunks, pr.eps,
+                       static_cast<const float*>(w.partial), w.hi[0], w.lo[0]);
 }
 
 }  // namespace
@@ -709,49 +1146,52 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   const int mp = pad64(pr.m), np = pad64(pr.n), count = pr.count;
   const Buffers w = carve(workspace, count, mp, np);
 
-  const size_t elems = static_cast<size_t>(pr.m) * pr.n;
-  size_t chunk = (elems + kNormChunks - 1) / kNormChunks;
-  if (chunk < 8192) chunk = 8192;
-  const int chunks = static_cast<int>((elems + chunk - 1) / chunk);
-  e = launch_kernel(ns_norm_kernel, dim3(chunks, count), dim3(kNormThreads), 0, s, false, pr.stacks, pr.grad_fp32,
-                    pr.momentum, pr.nesterov, elems, chunk, w.partial);
-  if (e != cudaSuccess) return e;
-  e = launch_kernel(ns_load_kernel, dim3((mp / 64) * (np / 64), count), dim3(256), 0, s, true, pr.stacks,
-                    pr.grad_fp32, pr.momentum, pr.nesterov, pr.m, pr.n, mp, np, chunks, pr.eps,
-                    static_cast<const float*>(w.partial), w.hi[0], w.lo[0]);
+  // four values at a time where rows (of either orientation) start on a multiple of four
+  const bool vec = pr.m % 4 == 0 && pr.n % 4 == 0;
+  if (pr.grad_fp32)
+    e = vec ? launch_first<float, 4>(pr, w, mp, np, s) : launch_first<float, 1>(pr, w, mp, np, s);
+  else
+    e = vec ? launch_first<uint16_t, 4>(pr, w, mp, np, s) : launch_first<uint16_t, 1>(pr, w, mp, np, s);
   if (e != cudaSuccess) return e;
 
-  CUtensorMap mX[2], sX[2], sLo[2], mA, sA, mB, sB;
-  for (int i = 0; i < 2; ++i) {
-    if ((e = operand_map(enc, &mX[i], w.hi[i], count, mp, np)) != cudaSuccess) return e;
-    if ((e = store_map(enc, &sX[i], w.hi[i], count, mp, np)) != cudaSuccess) return e;
-    if ((e = store_map(enc, &sLo[i], w.lo[i], count, mp, np)) != cudaSuccess) return e;
-  }
-  if ((e = operand_map(enc, &mA, w.A, count, mp, mp)) != cudaSuccess) return e;
-  if ((e = store_map(enc, &sA, w.A, count, mp, mp)) != cudaSuccess) return e;
-  if ((e = operand_map(enc, &mB, w.B, count, mp, mp)) != cudaSuccess) return e;
-  if ((e = store_map(enc, &sB, w.B, count, mp, mp)) != cudaSuccess) return e;
+  NsMaps maps;
+  for (int i = 0; i < 2; ++i)
+    if ((e = operand_map(enc, &maps.X[i], w.hi[i], count, mp, np)) != cudaSuccess) return e;
+  if ((e = operand_map(enc, &maps.A, w.A, count, mp, mp)) != cudaSuccess) return e;
+  if ((e = operand_map(enc, &maps.B, w.B, count, mp, mp)) != cudaSuccess) return e;
 
-  for (int k = 0; k < pr.steps; ++k) {
-    const int cur = k & 1;
-    GemmArgs a{};
-    a.count = count;
-    a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
-    a.a = pr.coeff[k][0], a.b = pr.coeff[k][1], a.c = pr.coeff[k][2];
-    a.A = w.A;
-    a.hi = w.hi[cur];
-    a.lo = w.lo[cur];
-    a.store_lo = 1;
-    a.out = pr.out;
-    if ((e = launch_gemm<kGram>(pairs, mX[cur], mX[cur], sA, sA, a, pr.stacks, err, s)) != cudaSuccess) return e;
-    if ((e = launch_gemm<kPoly>(pairs, mA, mA, sB, sB, a, pr.stacks, err, s)) != cudaSuccess) return e;
-    if (k + 1 < pr.steps)
-      e = launch_gemm<kApply>(pairs, mB, mX[cur], sX[cur ^ 1], sLo[cur ^ 1], a, pr.stacks, err, s);
-    else
-      e = launch_gemm<kLast>(pairs, mB, mX[cur], sX[cur], sX[cur], a, pr.stacks, err, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  GemmArgs a{};
+  a.count = count;
+  a.group = count;
+  a.steps = pr.steps;
+  a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
+  for (int k = 0; k < pr.steps; ++k)
+    for (int j = 0; j < 3; ++j) a.coeff[k][j] = pr.coeff[k][j];
+  a.A = w.A, a.B = w.B;
+  for (int i = 0; i < 2; ++i) a.hi[i] = w.hi[i], a.lo[i] = w.lo[i];
+  a.diag = w.diag;
+  a.done = w.done;
+  a.out = pr.out;
+  // more pairs than the widest product has tiles would find nothing to do
+  const long nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile;
+  const long most = count * std::max(nt * ntn, nt * (nt + 1) / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long>(pairs, most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, ns_products_kernel, maps, a, pr.stacks, err);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe
