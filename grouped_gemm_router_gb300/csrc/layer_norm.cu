@@ -14,6 +14,8 @@
 // rows in registers and writes one partial row, and a second kernel adds the
 // partial rows; there are no atomics, so the results do not change from run
 // to run.
+#include <algorithm>
+
 #include "moe_device.cuh"
 #include "moe_kernels.cuh"
 
@@ -23,6 +25,17 @@ namespace {
 
 constexpr int kLnThreads = 256;
 constexpr int kLnWarps = kLnThreads / 32;
+constexpr int kLnMaxStages = 6;                   // slots of the backward's ring
+constexpr size_t kLnHalfSm = 108 * 1024;          // shared memory of a block when two share an SM
+constexpr size_t kLnWholeSm = 216 * 1024;
+
+// One contiguous piece of global memory into shared memory; 16-byte aligned,
+// a multiple of 16 bytes.
+MOE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 // VEC consecutive elements as floats; p is aligned to VEC elements.
 template <int VEC>
@@ -129,6 +142,7 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_kernel(
         load_vec<VEC>(add + base + c, a);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[i][j] = as_stored(v[i][j] + a[j], x);
+        store_vec<VEC>(h + base + c, v[i]);  // at once: after the sums it took 75 us instead of 64 (fp32, D = 2048)
       }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += v[i][j];
@@ -141,7 +155,6 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_kernel(
   for (int i = 0; i < N; ++i) {
     const int c = (i * P + t) * VEC;
     if (live && c < D) {
-      if constexpr (ADD) store_vec<VEC>(h + base + c, v[i]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         v[i][j] -= mu;
@@ -173,14 +186,37 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_kernel(
   }
 }
 
+// The block's row groups have left their sums side by side, [kRows][2][D]:
+// adds them column by column into the block's partial row, or, when it is the
+// only block, into the results.
+template <int kRows>
+MOE_DEV void block_sums(const float* sums, int D, float* part, float* dweight, float* dbias) {
+  __syncthreads();
+  float* out = part + static_cast<size_t>(blockIdx.x) * 2 * D;
+  for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
+    float v = sums[c];
+#pragma unroll
+    for (int g = 1; g < kRows; ++g) v += sums[g * 2 * D + c];
+    if (gridDim.x > 1)
+      out[c] = v;
+    else if (c < D)
+      dweight[c] = v;
+    else if (dbias != nullptr)
+      dbias[c - D] = v;
+  }
+  griddep_launch_dependents();
+}
+
 // Backward: block k takes row groups k, k + gridDim.x, ...; part[k] = its
-// sums of dy n (first D) and dy (next D).
-template <typename XT, int P, int N, int VEC, bool STREAM>
+// sums of dy n (first D) and dy (next D).  This form, one element at a time,
+// is for rows that are no multiple of 16 bytes.
+template <typename XT, int P, int N, bool STREAM>
 __global__ void __launch_bounds__(kLnThreads) layer_norm_bwd_kernel(
     const uint16_t* __restrict__ dy, const XT* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ mean, const float* __restrict__ rstd, const XT* __restrict__ d_stream, int T, int D,
-    XT* __restrict__ dx, float* __restrict__ part) {
-  extern __shared__ float acc[];  // [2][D]
+    XT* __restrict__ dx, float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias) {
+  constexpr int VEC = 1;
+  extern __shared__ float sums[];  // [kRows][2][D]
   __shared__ float red[2 * kLnWarps];
   constexpr int kRows = kLnThreads / P;
   const int t = threadIdx.x % P, group = threadIdx.x / P;
@@ -238,50 +274,279 @@ __global__ void __launch_bounds__(kLnThreads) layer_norm_bwd_kernel(
       }
     }
   }
-  // the block's row groups add their columns one after the other
-  for (int g = 0; g < kRows; ++g) {
-    if (group == g) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = (i * P + t) * VEC;
-        if (c < D) {
+  for (int i = 0; i < N; ++i) {
+    const int c = i * P + t;
+    if (c < D) {
+      sums[(group * 2) * D + c] = dw[i][0];
+      sums[(group * 2 + 1) * D + c] = db[i][0];
+    }
+  }
+  block_sums<kRows>(sums, D, part, dweight, dbias);
+}
+
+// Rows that are multiples of 16 bytes come through a ring in shared memory:
+// each of `stages` slots holds the rows of one turn of the block (dy, x,
+// d_stream, one bulk copy each), which a warp of its own asks for a few turns
+// ahead, so that 100 to 200 KB are on the way on each SM without a register
+// held for them.  (Loads straight into registers left DRAM at 29%, a ring of
+// single rows filled by their own warps, with 1.5 KB copies, at 28%.)  A row
+// is read from its slot twice, for the sums and for dx, rather than kept.
+constexpr int kRingThreads = kLnThreads + 32;
+
+template <typename XT>
+__host__ __device__ constexpr int slot_bytes(int rows, int D, bool stream) {
+  return rows * D * (2 + static_cast<int>(sizeof(XT)) * (stream ? 2 : 1));
+}
+
+// All P threads of a row.
+template <int P>
+MOE_DEV void row_sync(int group) {
+  if constexpr (P == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(P) : "memory");
+}
+
+// Pairs of fp32 in one register pair: one instruction for two.
+typedef unsigned long long f2;
+MOE_DEV f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+MOE_DEV float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+MOE_DEV f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Two sums over the P threads of a row.
+template <int P>
+MOE_DEV void row_sum2(float& a, float& b, int group, float2* red) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            acc[c + j] = g == 0 ? dw[i][j] : acc[c + j] + dw[i][j];
-            acc[D + c + j] = g == 0 ? db[i][j] : acc[D + c + j] + db[i][j];
-          }
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (P > 32) {
+    constexpr int kPerRow = P / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
+    row_sync<P>(group);
+    const int first = warp / kPerRow * kPerRow;
+    a = red[first].x, b = red[first].y;
+#pragma unroll
+    for (int i = 1; i < kPerRow; ++i) a += red[first + i].x, b += red[first + i].y;
+  }
+}
+
+// Eight values of a slot (or of the weights) as four pairs.
+MOE_DEV void slot_vec(const float* p, f2 (&v)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = pack2(a.x, a.y), v[1] = pack2(a.z, a.w), v[2] = pack2(b.x, b.y), v[3] = pack2(b.z, b.w);
+}
+MOE_DEV void slot_vec(const uint16_t* p, f2 (&v)[4]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack2(bf16_lo(u[i]), bf16_hi(u[i]));
+}
+MOE_DEV void store_pairs(float* p, const f2 (&v)[4]) {
+  const float2 a = unpack2(v[0]), b = unpack2(v[1]), c = unpack2(v[2]), d = unpack2(v[3]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+}
+MOE_DEV void store_pairs(uint16_t* p, const f2 (&v)[4]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2(v[i]);
+    u[i] = pack_bf16x2(f.x, f.y);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+template <typename XT, int P, int N, bool STREAM>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
+    const uint16_t* __restrict__ dy, const XT* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const XT* __restrict__ d_stream, int T, int D,
+    int stages, XT* __restrict__ dx, float* __restrict__ part, float* __restrict__ dweight,
+    float* __restrict__ dbias, unsigned int* dev_err) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kLnMaxStages], empty[kLnMaxStages];
+  __shared__ float2 red[2][kLnWarps];
+  __shared__ int abort_flag;
+  constexpr int kRows = kLnThreads / P;
+  const int slot = slot_bytes<XT>(kRows, D, STREAM);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kLnWarps);
+    }
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  const int turns = (T + kRows - 1) / kRows;
+  f2 dw[N][4], db[N][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0ull;
+  const int t = threadIdx.x % P, group = threadIdx.x / P;
+  int st = 0;
+  uint32_t phase = 0;
+  if (threadIdx.x == kLnThreads) {
+    // ---- the warp that asks for rows (one lane) ----
+    int asked = 0;
+    bool ok = true;
+    for (int k = blockIdx.x; k < turns; k += gridDim.x) {
+      if (!(ok = mbar_wait(smem_u32(&empty[st]), phase ^ 1u, &abort_flag, dev_err))) break;
+      const int rows = min(kRows, T - k * kRows);
+      const size_t base = static_cast<size_t>(k) * kRows * D;
+      const uint32_t bar = smem_u32(&full[st]), dst = smem_u32(ring + st * slot);
+      mbar_arrive_expect_tx(bar, slot_bytes<XT>(rows, D, STREAM));
+      bulk_load(dst, dy + base, rows * D * 2, bar);
+      bulk_load(dst + kRows * D * 2, x + base, rows * D * sizeof(XT), bar);
+      if constexpr (STREAM)
+        bulk_load(dst + kRows * D * (2 + sizeof(XT)), d_stream + base, rows * D * sizeof(XT), bar);
+      ++asked;
+      if (++st == stages) st = 0, phase ^= 1u;
+    }
+    if (!ok) {  // copies may still be on their way into shared memory: another wait for each
+      for (int i = 0; i < stages && i < asked; ++i) {
+        if (--st < 0) st = stages - 1, phase ^= 1u;
+        volatile int local_abort = 0;
+        mbar_wait(smem_u32(&full[st]), phase, &local_abort, dev_err);
+      }
+    }
+  }
+  const float inv_d = 1.f / static_cast<float>(D);
+  int flip = 0;
+  // the rows' warps; each makes every turn of the block, also when a wait was
+  // given up (the error word says so), since a row's warps meet at barriers
+  for (int k = blockIdx.x; k < turns && threadIdx.x < kLnThreads; k += gridDim.x) {
+    const int row = k * kRows + group;
+    const bool live = row < T;
+    const float mu = live ? mean[row] : 0.f, r = live ? rstd[row] : 0.f;
+    mbar_wait(smem_u32(&full[st]), phase, &abort_flag, dev_err);
+    const uint16_t* sdy = reinterpret_cast<const uint16_t*>(ring + st * slot) + group * D;
+    const XT* sx = reinterpret_cast<const XT*>(ring + st * slot + kRows * D * 2) + group * D;
+    const XT* sg = sx + kRows * D;
+    // n = x r - mu r
+    const f2 rr = pack2(r, r), mr = pack2(-mu * r, -mu * r);
+    f2 q1 = 0ull, q2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * P + t) * 8;
+      if (live && c < D) {
+        f2 n[4], p[4], wv[4];
+        slot_vec(sx + c, n);
+        slot_vec(sdy + c, p);
+        slot_vec(w + c, wv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          n[j] = fma2(n[j], rr, mr);
+          dw[i][j] = fma2(p[j], n[j], dw[i][j]);
+          db[i][j] = add2(db[i][j], p[j]);
+          p[j] = mul2(p[j], wv[j]);
+          q1 = add2(q1, p[j]);
+          q2 = fma2(p[j], n[j], q2);
         }
       }
     }
-    __syncthreads();
+    float s1 = unpack2(q1).x + unpack2(q1).y, s2 = unpack2(q2).x + unpack2(q2).y;
+    row_sum2<P>(s1, s2, group, red[flip]);
+    flip ^= 1;
+    // dx = r dy w - r s1 / D - n r s2 / D, the last two as x k1 + k0
+    const float t2 = -r * s2 * inv_d;
+    const f2 k1 = pack2(t2 * r, t2 * r);
+    const float t0 = fmaf(-t2 * r, mu, -r * s1 * inv_d);
+    const f2 k0 = pack2(t0, t0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * P + t) * 8;
+      if (live && c < D) {
+        f2 n[4], p[4], wv[4];
+        slot_vec(sx + c, n);
+        slot_vec(sdy + c, p);
+        slot_vec(w + c, wv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = fma2(p[j], mul2(wv[j], rr), fma2(n[j], k1, k0));
+        if constexpr (STREAM) {
+          slot_vec(sg + c, n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = add2(p[j], n[j]);
+        }
+        store_pairs(dx + static_cast<size_t>(row) * D + c, p);
+      }
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&empty[st]));
+    if (++st == stages) st = 0, phase ^= 1u;
   }
-  float* out = part + static_cast<size_t>(blockIdx.x) * 2 * D;
-  for (int c = threadIdx.x; c < 2 * D; c += kLnThreads) out[c] = acc[c];
-  griddep_launch_dependents();
+  // every group's sums side by side, then added column by column
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);  // [kRows][2][D]
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = (i * P + t) * 8;
+    if (c < D && threadIdx.x < kLnThreads) {
+      store_pairs(sums + (group * 2) * D + c, dw[i]);
+      store_pairs(sums + (group * 2 + 1) * D + c, db[i]);
+    }
+  }
+  block_sums<kRows>(sums, D, part, dweight, dbias);
 }
 
 // out[c] = sum over the nblk partial rows, column c of [2 D]: 32 columns a
-// block, 8 strips of rows added in order.
-__global__ void __launch_bounds__(256) layer_norm_reduce_kernel(const float* __restrict__ part, int nblk, int D,
-                                                                float* __restrict__ dweight,
-                                                                float* __restrict__ dbias) {
-  __shared__ float strip[8][32];
+// block, kStrips strips of rows, each added in order and then together in order.
+constexpr int kStrips = 32;
+__global__ void __launch_bounds__(32 * kStrips) layer_norm_reduce_kernel(const float* __restrict__ part, int nblk,
+                                                                         int D, float* __restrict__ dweight,
+                                                                         float* __restrict__ dbias) {
+  __shared__ float strip[kStrips][33];
   griddep_wait();  // the partial rows come from the previous kernel
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  float v[(kLnMaxPartials + kStrips - 1) / kStrips];
   float s = 0.f;
-  if (c < 2 * D)
-    for (int i = k; i < nblk; i += 8) s += part[static_cast<size_t>(i) * 2 * D + c];
+#pragma unroll
+  for (int i = 0; i < (kLnMaxPartials + kStrips - 1) / kStrips; ++i) {
+    const int b = k + i * kStrips;
+    v[i] = c < 2 * D && b < nblk ? part[static_cast<size_t>(b) * 2 * D + c] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < (kLnMaxPartials + kStrips - 1) / kStrips; ++i) s += v[i];
   strip[k][lane] = s;
   __syncthreads();
-  if (k == 0 && c < 2 * D) {
-    s = strip[0][lane];
+  // warp k takes column k of the block: 32 strips in a tree of fixed shape
+  s = strip[lane][k];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += strip[i][lane];
-    if (c < D)
-      dweight[c] = s;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + k;
+  if (lane == 0 && col < 2 * D) {
+    if (col < D)
+      dweight[col] = s;
     else if (dbias != nullptr)
-      dbias[c - D] = s;
+      dbias[col - D] = s;
   }
 }
 
@@ -295,27 +560,49 @@ cudaError_t run_fwd(const LayerNormArgs& a, cudaStream_t s) {
                        static_cast<uint16_t*>(a.y), static_cast<XT*>(a.h), a.mean, a.rstd);
 }
 
+cudaError_t reduce_partials(const LayerNormBwdArgs& a, int nblk, cudaStream_t s) {
+  return launch_kernel(layer_norm_reduce_kernel, dim3((2 * a.D + 31) / 32), dim3(32 * kStrips), 0, s, true,
+                       static_cast<const float*>(a.part), nblk, a.D, a.dweight, a.dbias);
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
 template <typename XT, int P, int N, int VEC>
 cudaError_t run_bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
   constexpr int kRows = kLnThreads / P;
   const int sms = current_device_sms();
-  int nblk = (a.T + kRows - 1) / kRows;
-  if (nblk > 2 * sms) nblk = 2 * sms;
-  if (nblk > kLnMaxPartials) nblk = kLnMaxPartials;
-  auto kernel = a.d_stream ? layer_norm_bwd_kernel<XT, P, N, VEC, true> : layer_norm_bwd_kernel<XT, P, N, VEC, false>;
-  const size_t smem = static_cast<size_t>(2) * a.D * sizeof(float);
+  int nblk = std::min({(a.T + kRows - 1) / kRows, 2 * sms, kLnMaxPartials});
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  if (nblk > 0)  // no rows: the sums below are zeros
+  if (nblk == 0) return reduce_partials(a, 0, s);  // no rows: the sums are zeros
+  if constexpr (VEC == 1) {
+    auto kernel = a.d_stream ? layer_norm_bwd_kernel<XT, P, N, true> : layer_norm_bwd_kernel<XT, P, N, false>;
+    const size_t smem = static_cast<size_t>(kRows) * 2 * a.D * sizeof(float);
+    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
     e = launch_kernel(kernel, dim3(nblk), dim3(kLnThreads), smem, s, false, static_cast<const uint16_t*>(a.dy),
                       static_cast<const XT*>(a.x), a.weight, a.mean, a.rstd, static_cast<const XT*>(a.d_stream), a.T,
-                      a.D, static_cast<XT*>(a.dx), a.part);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(layer_norm_reduce_kernel, dim3((2 * a.D + 31) / 32), dim3(256), 0, s, true,
-                       static_cast<const float*>(a.part), nblk, a.D, a.dweight, a.dbias);
+                      a.D, static_cast<XT*>(a.dx), a.part, a.dweight, a.dbias);
+  } else {
+    // two blocks an SM with at least two slots each, else one
+    const size_t slots = slot_bytes<XT>(kRows, a.D, a.d_stream != nullptr);
+    const bool two = 2 * slots <= kLnHalfSm;
+    const int stages = static_cast<int>(std::min<size_t>(kLnMaxStages, (two ? kLnHalfSm : kLnWholeSm) / slots));
+    const size_t sums = static_cast<size_t>(kRows) * 2 * a.D * sizeof(float);
+    const size_t smem = std::max(stages * slots, sums);
+    if (!two) nblk = std::min(nblk, sms);
+    unsigned int* err = nullptr;
+    if ((e = device_error_address(&err)) != cudaSuccess) return e;
+    auto kernel =
+        a.d_stream ? layer_norm_bwd_ring_kernel<XT, P, N, true> : layer_norm_bwd_ring_kernel<XT, P, N, false>;
+    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
+    e = launch_kernel(kernel, dim3(nblk), dim3(kRingThreads), smem, s, false, static_cast<const uint16_t*>(a.dy),
+                      static_cast<const XT*>(a.x), a.weight, a.mean, a.rstd, static_cast<const XT*>(a.d_stream), a.T,
+                      a.D, stages, static_cast<XT*>(a.dx), a.part, a.dweight, a.dbias, err);
+  }
+  if (e != cudaSuccess || nblk == 1) return e;
+  return reduce_partials(a, nblk, s);
 }
 
 // P threads a row: 32 up to 1024 columns, then 64, 128, 256, so that a thread
