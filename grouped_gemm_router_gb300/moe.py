@@ -373,15 +373,34 @@ def moe_combine(y, weights, inv, ys=None, out=None):
 
 
 _STREAM_TYPES = {torch.bfloat16: N.MOE_BF16, torch.float32: N.MOE_FP32}
+_F32 = torch.float32
+_BF16 = torch.bfloat16
+_empty = torch.empty
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(t):
+    """The current stream of t's device, as the C ABI takes it (0.1 us where
+    torch.cuda.current_stream() takes 3: these calls are a few us each)."""
+    return _raw_stream(t.device.index)
+
+
+def _like(t, name, dtype, shape):
+    """As _need for a tensor that must be there, without the copies."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, dtype, shape)
 
 
 def _stream_type(x):
     """The C ABI's element type of a residual stream x."""
+    kind = _STREAM_TYPES.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [T, D]")
-    if x.dtype not in _STREAM_TYPES:
-        raise ValueError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    return _STREAM_TYPES[x.dtype]
+    if not x.is_cuda or not x.is_contiguous():
+        _need(x, "x", x.dtype)
+    return kind
 
 
 def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
@@ -391,24 +410,29 @@ def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
     rounded to x's type, and that is what is normalised; the dict then holds
     h too.  weight, bias: [D] fp32.  Any D up to 8192."""
     kind = _stream_type(x)
-    T, D = x.shape
-    _need(x, "x", x.dtype)
-    _need(weight, "weight", torch.float32, (D,))
-    _need(bias, "bias", torch.float32, (D,))
-    _need(add, "add", torch.bfloat16, (T, D))
-    _need(y, "y", torch.bfloat16, (T, D))
+    shape = x.shape
+    T, D = shape
+    _like(weight, "weight", _F32, (D,))
+    if bias is not None:
+        _like(bias, "bias", _F32, (D,))
     dev = x.device
     if y is None:
-        y = torch.empty(T, D, dtype=torch.bfloat16, device=dev)
-    out = dict(y=y, mean=torch.empty(T, dtype=torch.float32, device=dev),
-               rstd=torch.empty(T, dtype=torch.float32, device=dev))
+        y = _empty(shape, dtype=_BF16, device=dev)
+    else:
+        _like(y, "y", _BF16, shape)
+    mean = _empty(T, dtype=_F32, device=dev)
+    rstd = _empty(T, dtype=_F32, device=dev)
+    out = dict(y=y, mean=mean, rstd=rstd)
+    h = None
     if add is not None:
-        out["h"] = torch.empty_like(x)
+        _like(add, "add", _BF16, shape)
+        h = out["h"] = torch.empty_like(x)
     st = lib.moe_layer_norm_forward(x.data_ptr(), kind, None if add is None else add.data_ptr(), weight.data_ptr(),
                                     None if bias is None else bias.data_ptr(), eps, T, D, y.data_ptr(),
-                                    None if add is None else out["h"].data_ptr(), out["mean"].data_ptr(),
-                                    out["rstd"].data_ptr(), torch.cuda.current_stream().cuda_stream)
-    check(st, "moe_layer_norm_forward")
+                                    None if h is None else h.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                    _stream_of(x))
+    if st:
+        check(st, "moe_layer_norm_forward")
     return out
 
 
@@ -419,25 +443,29 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
     mean, rstd: the forward's; dy [T, D] bf16; d_stream [T, D] in x's type:
     the gradient that reaches these rows past the norm."""
     kind = _stream_type(x)
-    T, D = x.shape
-    _need(x, "x", x.dtype)
-    _need(dy, "dy", torch.bfloat16, (T, D))
-    _need(weight, "weight", torch.float32, (D,))
-    _need(mean, "mean", torch.float32, (T,))
-    _need(rstd, "rstd", torch.float32, (T,))
-    _need(d_stream, "d_stream", x.dtype, (T, D))
+    shape = x.shape
+    T, D = shape
+    _like(dy, "dy", _BF16, shape)
+    _like(weight, "weight", _F32, (D,))
+    _like(mean, "mean", _F32, (T,))
+    _like(rstd, "rstd", _F32, (T,))
+    if d_stream is not None:
+        _like(d_stream, "d_stream", x.dtype, shape)
     dev = x.device
-    out = dict(dx=torch.empty_like(x), dweight=torch.empty(D, dtype=torch.float32, device=dev))
+    dx = torch.empty_like(x)
+    dweight = _empty(D, dtype=_F32, device=dev)
+    out = dict(dx=dx, dweight=dweight)
+    dbias = None
     if bias:
-        out["dbias"] = torch.empty(D, dtype=torch.float32, device=dev)
-    nscratch = int(lib.moe_layer_norm_backward_scratch_size(T, D))
-    scratch = torch.empty(max(nscratch, 16), dtype=torch.uint8, device=dev)
+        dbias = out["dbias"] = _empty(D, dtype=_F32, device=dev)
+    nscratch = lib.moe_layer_norm_backward_scratch_size(T, D)
+    scratch = _empty(max(nscratch, 16), dtype=torch.uint8, device=dev)
     st = lib.moe_layer_norm_backward(dy.data_ptr(), x.data_ptr(), kind, weight.data_ptr(), mean.data_ptr(),
                                      rstd.data_ptr(), None if d_stream is None else d_stream.data_ptr(), T, D,
-                                     out["dx"].data_ptr(), out["dweight"].data_ptr(),
-                                     out["dbias"].data_ptr() if bias else None, scratch.data_ptr(), nscratch,
-                                     torch.cuda.current_stream().cuda_stream)
-    check(st, "moe_layer_norm_backward")
+                                     dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+                                     scratch.data_ptr(), nscratch, _stream_of(x))
+    if st:
+        check(st, "moe_layer_norm_backward")
     return out
 
 
@@ -485,7 +513,7 @@ def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, 
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=g.device)
     _need(workspace, "workspace", torch.uint8)
     st = lib.moe_newton_schulz(g.data_ptr(), kind, count, rows, cols, steps, c, eps, out.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
+                               workspace.data_ptr(), workspace.numel(), _stream_of(g))
     check(st, "moe_newton_schulz")
     return out
 
@@ -536,7 +564,7 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
     _need(workspace, "workspace", torch.uint8)
     if workspace.numel() < max(sizes):
         raise N.MoeError(N.MOE_ERR_WORKSPACE, "moe_muon_step")
-    stream = torch.cuda.current_stream().cuda_stream
+    stream = _stream_of(weights[0])
     for key, group in calls:
         p = N.MoeMuonParams(lr, momentum, weight_decay, 0.2 * key[1] ** 0.5 if scale is None else scale, eps,
                             int(bool(nesterov)), steps, ctypes.addressof(c))
