@@ -199,6 +199,9 @@ struct NsProblem {
 };
 size_t ns_workspace_bytes(int count, int m, int n);
 cudaError_t launch_newton_schulz(const NsProblem& p, void* workspace, cudaStream_t s);
+// All on chip, without a workspace (newton_schulz_small.cu).
+bool ns_small_fits(int m, int n);
+cudaError_t launch_ns_small(const NsProblem& p, cudaStream_t s);
 
 // 2-D bf16 TMA descriptor of a row-major [rows, cols] matrix with a
 // {box_cols, box_rows} box: 128-byte swizzle (64-byte for 32-column boxes),

@@ -1137,6 +1137,7 @@ cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, 
 size_t ns_workspace_bytes(int count, int m, int n) { return carve(nullptr, count, pad64(m), pad64(n)).bytes; }
 
 cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStream_t s) {
+  if (ns_small_fits(pr.m, pr.n)) return launch_ns_small(pr, s);
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   int pairs = 0;
   unsigned int* err = nullptr;

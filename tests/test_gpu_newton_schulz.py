@@ -59,7 +59,8 @@ def _check(got, ref, what):
 
 
 SIZES = [(1, 1, 1), (2, 1, 300), (3, 5, 7), (2, 17, 40), (1, 64, 64), (4, 128, 256), (2, 129, 255), (2, 300, 300),
-         (3, 1001, 363), (2, 200, 65), (1, 768, 1536), (2, 1536, 768), (1, 513, 2000), (1, 20, 8192), (70, 48, 96)]
+         (3, 1001, 363), (2, 200, 65), (1, 768, 1536), (2, 1536, 768), (1, 513, 2000), (1, 20, 8192), (70, 48, 96),
+         (3, 128, 257), (2, 100, 513), (2, 600, 96), (2, 128, 1024), (1, 2048, 128), (2, 33, 2001), (2, 128, 2049), (200, 64, 64)]
 
 
 @pytest.mark.parametrize("kind", ["full", "few tokens", "one strong", "dead features"])
