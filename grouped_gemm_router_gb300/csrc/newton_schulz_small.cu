@@ -41,7 +41,7 @@ constexpr int kBlockBytes = kRowsMax * 64 * 2;   // 128 rows x 64 columns of fp1
 constexpr int kXBytes = kSlice / 64 * kBlockBytes;
 constexpr int kABytes = 2 * kBlockBytes;
 constexpr int kPartBytes = kRowsMax * 128 * 4;
-constexpr int kPitch = kSlice + 1;               // stash: odd, so that rows and columns are free of bank conflicts
+constexpr int kPitch = kSlice + 4;               // stash: 16-byte pieces of 8 rows meet no bank conflict
 constexpr int kStashBytes = kRowsMax * kPitch * 4;
 constexpr int kSmemBytes = kXBytes + (kStashBytes > kABytes + kPartBytes ? kStashBytes : kABytes + kPartBytes) + 1024;
 constexpr uint32_t kTmemX = 0, kTmemA = 256, kTmemP = 384;
@@ -71,9 +71,6 @@ MOE_DEV int stack_of(const NsStacks& st, int mat) {
   while (s + 1 < st.n && mat >= st.s[s + 1].first) ++s;
   return s;
 }
-
-MOE_DEV float as_float(float v) { return v; }
-MOE_DEV float as_float(uint16_t v) { return bf16_lo(v); }
 
 MOE_DEV uint32_t pack_half2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
@@ -142,34 +139,164 @@ MOE_DEV void hand_to_mma() {
   tc_fence_after_sync();
 }
 
-// Visits the CTA's part of a matrix in memory order, kBatch elements a thread
-// at a time: load(k, element) for all of them, then use(k, row, column,
-// element) with the row and column of X.
-constexpr int kBatch = 16;
-template <typename Load, typename Use>
-MOE_DEV void visit(bool tall, int m, int n, int c0, int width, Load load, Use use) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = tall ? width : m, len = tall ? m : width;  // rows of memory, and how long
-  const int shift = len > 128 ? 3 : len > 64 ? 2 : len > 32 ? 1 : 0;  // 2^shift spans of 32 cover a row
-  const int total = rows << shift;
-  for (int s0 = warp; s0 < total; s0 += kWarps * kBatch) {
+// VEC consecutive elements.
+template <int VEC>
+MOE_DEV void load_run(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+    v[0] = *p;
+  }
+}
+template <int VEC>
+MOE_DEV void load_run(const uint16_t* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+  } else {
+    v[0] = bf16_lo(*p);
+  }
+}
+template <int VEC>
+MOE_DEV void store_run(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *p = v[0];
+}
+template <int VEC>
+MOE_DEV void store_run(uint16_t* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  else
+    *p = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f));
+}
+
+// The CTA's part of a matrix in memory order, runs of VEC elements, batch(VEC)
+// a thread at a time.  Four-element runs are for matrices that lie in memory as
+// X does; in a tall one a run would be a column of the stash, and single
+// elements meet fewer bank conflicts (4 lanes a bank).  In the stash the run
+// at memory row r, place x starts at element r * sr + x * sx.
+__host__ __device__ constexpr int batch(int vec) { return vec == 4 ? 4 : 16; }
+struct Part {
+  int rows, len, shift;  // memory rows, elements of one, 2^shift runs cover it
+  int sr, sx;
+  int first, pitch;      // element of the matrix where the part starts, and between rows
+};
+template <int VEC>
+MOE_DEV Part part_of(bool tall, int m, int n, int c0, int width) {
+  Part q;
+  q.rows = tall ? width : m;
+  q.len = tall ? m : width;
+  q.shift = 0;
+  while ((VEC << q.shift) < q.len) ++q.shift;
+  q.sr = tall ? 1 : kPitch;
+  q.sx = tall ? kPitch : 1;
+  q.first = tall ? c0 * m : c0;
+  q.pitch = tall ? m : n;
+  return q;
+}
+template <int VEC, typename Load, typename Use>
+MOE_DEV void visit(const Part& q, Load load, Use use) {
+  constexpr int kBatch = batch(VEC);
+  const int total = q.rows << q.shift, mask = (1 << q.shift) - 1;
+#pragma unroll 1
+  for (int s0 = threadIdx.x; s0 < total; s0 += kThreads * kBatch) {
+    // runs past the end (of a row, or of the part) repeat the part's first one
+    int at[kBatch], spot[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int s = s0 + k * kWarps, r = s >> shift, x = ((s - (r << shift)) << 5) + lane;
-      if (s < total && x < len)
-        load(k, tall ? static_cast<size_t>(c0 + r) * m + x : static_cast<size_t>(r) * n + c0 + x);
+      const int s = s0 + k * kThreads, r = s >> q.shift, x = (s & mask) * VEC;
+      const bool in = s < total && x < q.len;
+      at[k] = in ? q.first + r * q.pitch + x : q.first;
+      spot[k] = in ? r * q.sr + x * q.sx : -1;
+      load(k, at[k]);
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int s = s0 + k * kWarps, r = s >> shift, x = ((s - (r << shift)) << 5) + lane;
-      if (s < total && x < len)
-        use(k, tall ? x : r, tall ? r : x,
-            tall ? static_cast<size_t>(c0 + r) * m + x : static_cast<size_t>(r) * n + c0 + x);
-    }
+    for (int k = 0; k < kBatch; ++k)
+      if (spot[k] >= 0) use(k, spot[k], at[k]);
   }
 }
 
-template <typename GT>
+template <int VEC>
+MOE_DEV void stash_put(uint32_t stash, int spot, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stash + spot * 4), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+  else
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stash + spot * 4), "f"(v[0]) : "memory");
+}
+template <int VEC>
+MOE_DEV void stash_get(uint32_t stash, int spot, float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(stash + spot * 4)
+                 : "memory");
+  else
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(stash + spot * 4) : "memory");
+}
+
+// Momentum, and u into the stash; returns the thread's sum of squares.
+template <typename GT, int VEC>
+MOE_DEV float take_in(const SmallArgs& p, const NsStack& s, size_t base, const Part& q, uint32_t stash) {
+  const GT* g = static_cast<const GT*>(s.grad) + base;
+  float* mom = s.momentum ? s.momentum + base : nullptr;
+  constexpr int kBatch = batch(VEC);
+  float sq = 0.f, gv[kBatch][VEC], mv[kBatch][VEC];
+  visit<VEC>(
+      q,
+      [&](int k, int i) {
+        load_run<VEC>(g + i, gv[k]);
+        if (mom != nullptr) load_run<VEC>(mom + i, mv[k]);
+      },
+      [&](int k, int spot, int i) {
+        if (mom != nullptr) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            mv[k][j] = fmaf(p.mu, mv[k][j], gv[k][j]);
+            gv[k][j] = p.nesterov ? fmaf(p.mu, mv[k][j], gv[k][j]) : mv[k][j];
+          }
+          store_run<VEC>(mom + i, mv[k]);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sq = fmaf(gv[k][j], gv[k][j], sq);
+        stash_put<VEC>(stash, spot, gv[k]);
+      });
+  return sq;
+}
+
+// The result, or the weights it moves, from the stash.
+template <int VEC>
+MOE_DEV void give_out(const SmallArgs& p, const NsStack& s, size_t base, const Part& q, uint32_t stash) {
+  constexpr int kBatch = batch(VEC);
+  float w[kBatch][VEC];
+  uint16_t* const half = static_cast<uint16_t*>(p.out.kind == kNsWeightF32 ? s.weight_bf16 : s.weight) + base;
+  float* const full = static_cast<float*>(s.weight) + base;
+  const bool store_half = p.out.kind != kNsWeightF32 || s.weight_bf16 != nullptr;
+  visit<VEC>(
+      q,
+      [&](int k, int i) {
+        if (p.out.kind == kNsWeightBf16)
+          load_run<VEC>(half + i, w[k]);
+        else if (p.out.kind == kNsWeightF32)
+          load_run<VEC>(full + i, w[k]);
+      },
+      [&](int k, int spot, int i) {
+        float o[VEC];
+        stash_get<VEC>(stash, spot, o);
+        if (p.out.kind != kNsPlain) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) o[j] = fmaf(w[k][j], p.out.keep, -p.out.step * o[j]);
+        }
+        if (p.out.kind == kNsWeightF32) store_run<VEC>(full + i, o);
+        if (store_half) store_run<VEC>(half + i, o);
+      });
+}
+
+template <typename GT, int VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     ns_small_kernel(const __grid_constant__ SmallArgs p, const __grid_constant__ NsStacks st, unsigned int* const dev_err) {
   extern __shared__ uint8_t smem_raw[];
@@ -177,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t xs = smem_u32(smem), as = xs + kXBytes, part = as + kABytes;
-  float* stash = reinterpret_cast<float*>(smem + kXBytes);
+  const uint32_t stash = as;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3, cq = warp >> 2;
   const uint32_t row = 32 * q + lane;              // the thread's row of X, A and B
@@ -205,29 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 
   // ---- momentum, u into the stash, its sum of squares ----
-  const GT* g = static_cast<const GT*>(s.grad) + base;
-  float* mom = s.momentum ? s.momentum + base : nullptr;
-  float sq = 0.f;
-  {
-    GT gv[kBatch];
-    float mv[kBatch];
-    visit(
-        s.tall, p.m, p.n, c0, width,
-        [&](int k, size_t i) {
-          gv[k] = g[i];
-          if (mom != nullptr) mv[k] = mom[i];
-        },
-        [&](int k, int r, int c, size_t i) {
-          float u = as_float(gv[k]);
-          if (mom != nullptr) {
-            const float v = fmaf(p.mu, mv[k], u);
-            mom[i] = v;
-            u = p.nesterov ? fmaf(p.mu, v, u) : v;
-          }
-          sq = fmaf(u, u, sq);
-          stash[r * kPitch + c] = u;
-        });
-  }
+  const bool runs = VEC == 4 && !s.tall;
+  const Part mine = runs ? part_of<VEC>(false, p.m, p.n, c0, width) : part_of<1>(s.tall, p.m, p.n, c0, width);
+  float sq = runs ? take_in<GT, VEC>(p, s, base, mine, stash) : take_in<GT, 1>(p, s, base, mine, stash);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   if (lane == 0) ctl.red[warp] = sq;
@@ -252,9 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int h = 0; h < 2; ++h) {
       float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < 32; j += 4) {
         const int c = xcol + 32 * h + j;
-        v[j] = static_cast<int>(row) < p.m && c < width ? stash[row * kPitch + c] * inv : 0.f;
+        float x[4];
+        stash_get<4>(stash, row * kPitch + c, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j + k] = static_cast<int>(row) < p.m && c + k < width ? x[k] * inv : 0.f;
       }
       put_acc(tmem + kTmemX + xcol + 32 * h, v);
       put_halves(xs, row, xcol + 32 * h, v);
@@ -302,36 +412,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       put_halves(as, row, 32 * cq, a);
     } else {
       // partial sums into this CTA's memory (16-byte chunk c of row r at c ^
-      // (r % 8)), then each CTA adds a part of the rows and hands it to all
+      // (r % 8)), then each CTA adds a part of the rows and hands it to all:
+      // 9000 cycles with eight CTAs (10300 when the sums' owners were sent
+      // the parts instead of fetching them)
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         st_shared_u4(part + row * 512 + (((8 * cq + c) ^ (row & 7)) << 4), __float_as_uint(a[4 * c]),
                      __float_as_uint(a[4 * c + 1]), __float_as_uint(a[4 * c + 2]), __float_as_uint(a[4 * c + 3]));
       cluster_sync_all();
-      const int mine = kRowsMax / ranks;
-      for (int i = threadIdx.x; i < mine * 16; i += kThreads) {
-        const uint32_t r = rank * mine + (i >> 4), c8 = i & 15;
-        float v[8];
+      const uint32_t rows = kRowsMax / ranks;
+      for (uint32_t i = threadIdx.x; i < rows * 32; i += kThreads) {
+        const uint32_t r = rank * rows + (i >> 5), c4 = i & 31;
+        const uint32_t from = part + r * 512 + ((c4 ^ (r & 7)) << 4);
+        float x[kMaxCluster][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        for (uint32_t k = 0; k < ranks; ++k) {
-          const uint32_t from = map_to_cta(part + r * 512, k);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x, y, z, w;
+        for (uint32_t k = 0; k < kMaxCluster; ++k)
+          if (k < ranks)
             asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x), "=f"(y), "=f"(z), "=f"(w)
-                         : "r"(from + (((2 * c8 + h) ^ (r & 7)) << 4))
+                         : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]), "=f"(x[k][3])
+                         : "r"(map_to_cta(from, k)));
+#pragma unroll
+        for (uint32_t k = 1; k < kMaxCluster; ++k)
+          if (k < ranks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[0][j] += x[k][j];
+        const uint32_t h0 = pack_half2(x[0][0], x[0][1]), h1 = pack_half2(x[0][2], x[0][3]);
+        const uint32_t to = chunk_at(as, r, c4 >> 1) + (c4 & 1) * 8;
+#pragma unroll
+        for (uint32_t k = 0; k < kMaxCluster; ++k)
+          if (k < ranks)
+            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(map_to_cta(to, k)), "r"(h0), "r"(h1)
                          : "memory");
-            v[4 * h] += x, v[4 * h + 1] += y, v[4 * h + 2] += z, v[4 * h + 3] += w;
-          }
-        }
-        const uint32_t h0 = pack_half2(v[0], v[1]), h1 = pack_half2(v[2], v[3]), h2 = pack_half2(v[4], v[5]),
-                       h3 = pack_half2(v[6], v[7]);
-        for (uint32_t k = 0; k < ranks; ++k)
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_cta(chunk_at(as, r, c8), k)),
-                       "r"(h0), "r"(h1), "r"(h2), "r"(h3)
-                       : "memory");
       }
       asm volatile("fence.proxy.async;" ::: "memory");
       cluster_sync_all();
@@ -368,12 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v[32];
       get_acc(tmem + kTmemP + 32 * cq, v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        v[j] = fmaf(cc, v[j], cb * a[j]);
-        if (late && 32 * cq + j == static_cast<int>(row)) {
-          ctl.diag[row] = v[j];
-          v[j] = 0.f;
-        }
+      for (int j = 0; j < 32; ++j) v[j] = fmaf(cc, v[j], cb * a[j]);
+      if (late && cq == q) {  // the thread's diagonal element is among its columns
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == lane) {
+            ctl.diag[row] = v[j];
+            v[j] = 0.f;
+          }
       }
       put_halves(as, row, 32 * cq, v);
     }
@@ -411,7 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           put_halves(xs, row, xcol + 32 * h, v);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) stash[row * kPitch + xcol + 32 * h + j] = v[j] * (1.f / kScaleX);
+          for (int j = 0; j < 32; j += 4) {
+            const float x[4] = {v[j] * (1.f / kScaleX), v[j + 1] * (1.f / kScaleX), v[j + 2] * (1.f / kScaleX),
+                                v[j + 3] * (1.f / kScaleX)};
+            stash_put<4>(stash, row * kPitch + xcol + 32 * h + j, x);
+          }
         }
       }
     }
@@ -419,27 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---- the result, or the weights it moves ----
-  {
-    float w[kBatch];
-    visit(
-        s.tall, p.m, p.n, c0, width,
-        [&](int k, size_t i) {
-          if (p.out.kind == kNsWeightBf16)
-            w[k] = bf16_lo(static_cast<const uint16_t*>(s.weight)[base + i]);
-          else if (p.out.kind == kNsWeightF32)
-            w[k] = static_cast<const float*>(s.weight)[base + i];
-        },
-        [&](int k, int r, int c, size_t i) {
-          float o = stash[r * kPitch + c];
-          if (p.out.kind != kNsPlain) o = fmaf(w[k], p.out.keep, -p.out.step * o);
-          if (p.out.kind == kNsWeightF32) static_cast<float*>(s.weight)[base + i] = o;
-          const uint16_t h = static_cast<uint16_t>(pack_bf16x2(o, 0.f));
-          if (p.out.kind != kNsWeightF32)
-            static_cast<uint16_t*>(s.weight)[base + i] = h;
-          else if (s.weight_bf16 != nullptr)
-            static_cast<uint16_t*>(s.weight_bf16)[base + i] = h;
-        });
-  }
+  if (runs)
+    give_out<VEC>(p, s, base, mine, stash);
+  else
+    give_out<1>(p, s, base, mine, stash);
   // no CTA of the cluster leaves while another may read its memory
   tc_fence_before_sync();
   cluster_sync_all();
@@ -469,7 +569,10 @@ cudaError_t launch_ns_small(const NsProblem& pr, cudaStream_t s) {
   a.eps = pr.eps;
   a.nesterov = pr.nesterov;
   a.out = pr.out;
-  auto kernel = pr.grad_fp32 ? ns_small_kernel<float> : ns_small_kernel<uint16_t>;
+  // four elements at a time where rows (of either orientation) start on a multiple of four
+  const bool vec = pr.m % 4 == 0 && pr.n % 4 == 0;
+  auto kernel = pr.grad_fp32 ? (vec ? ns_small_kernel<float, 4> : ns_small_kernel<float, 1>)
+                             : (vec ? ns_small_kernel<uint16_t, 4> : ns_small_kernel<uint16_t, 1>);
   e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemBytes);
   if (e != cudaSuccess) return e;
