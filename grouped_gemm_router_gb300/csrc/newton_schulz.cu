@@ -13,13 +13,12 @@
 // fp32 sums.  fp16 and not bf16 because every operand has a known range
 // (singular values below about 1.3, so entries do too): scaled by a power of
 // two it holds 3 bits more at the same rate.  Two things are kept apart:
-//  * The term a X is not part of a product and keeps X to about 14 bits, as
-//    fp16 and what that leaves in e5m2 (hi + lo; not for the last step's
-//    X).  e5m2 is the upper byte of an fp16, so it needs no scale and is
-//    cheap to widen.  It matters where G has less than full rank (an expert
-//    with fewer tokens than rows): what rounding leaves outside the row space
-//    grows by a in every step, 485-fold in five with a = 3.4445, and nothing
-//    contracts it.  The products need no more bits there: A is small.
+//  * The term a X is not part of a product and keeps X to 16 bits (the upper
+//    three bytes of its fp32), beside the fp16 that the products read.  It
+//    matters where G has less than full rank (an expert with fewer tokens
+//    than rows): what rounding leaves outside the row space grows by a in
+//    every step, 485-fold in five with a = 3.4445, and nothing contracts it.
+//    The products need no more bits there: A is small.
 //  * In the last two steps B is close to -2.7 I and cancels most of a X, so
 //    the rounding of its diagonal would be the largest error left.  There the
 //    diagonal goes from product to product in fp32 and the stored B has
@@ -27,11 +26,18 @@
 //    the row space into two differently rounded halves.)
 // Simulated 2-norm errors, of which the bf16 rounding of the result is
 // 1.66e-3: full rank 1.8e-3 to 2.1e-3 (2.3e-3 to 2.6e-3 without the fp32
-// diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 without lo; with bf16 operands
-// 0.9e-1 to 2e-1).
+// diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 with a X in fp16; with bf16
+// operands 0.9e-1 to 2e-1).
 //
-// A and B are symmetric: only the tiles on and below the diagonal are
-// computed, and each is stored twice, once transposed.
+// A and B are symmetric: only the tiles on and below the diagonal are computed
+// and stored.  Where a product needs one from above, it loads the tile from
+// below as the transposed (M- or N-major) operand, which costs nothing.
+//
+// What the epilogues read themselves (A in B's, X in X's) is kept a second
+// time in the order in which they hold it: for each warp and 32 x 32 box,
+// 16-byte pieces of 32 lanes side by side.  So those accesses are whole lines
+// and need no turning in shared memory, whose bandwidth the products use.
+// The operands' copies leave by TMA.
 //
 // All products of all steps are one persistent launch over 256 x 256 tiles,
 // run by CTA pairs (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM,
@@ -49,7 +55,6 @@
 //   warps 2-17  epilogue
 //   warp 18     counts the tiles whose results are in memory
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -71,7 +76,9 @@ constexpr int kStages = 3;
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 96 + 32 * kEpiWarps;
 constexpr int kBox = 32;                       // columns an epilogue warp takes from TMEM at a time
-constexpr int kWarpStage = 16 * kBox * 4;      // its fp32 box in shared memory: half of those rows
+constexpr int kWarpStage = kBox * kBox * 2;    // its box in shared memory, fp16 (or 16 rows in fp32)
+constexpr int kBoxX = 6 * 512;                 // its box of X: 24 words a lane
+constexpr int kBoxA = 4 * 512;                 // its box of A: 16 words a lane
 constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kWarpStage + 1024;
 constexpr uint32_t kTmemCols = 512;
 
@@ -183,23 +190,29 @@ MOE_DEV uint32_t pack_half2(float lo, float hi) {
 
 MOE_DEV float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-MOE_DEV float half_minus(uint32_t h, float c) {  // the low half of h, minus c, in fp32
-  float d;
-  asm("sub.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(static_cast<uint16_t>(h)), "f"(c));
-  return d;
+// Four floats' upper three bytes in three words, and back (the byte that is
+// gone is filled with its neighbour, so that nothing is biased; zero,
+// infinities and NaN stay what they are).
+MOE_DEV void pack24(const float* v, uint32_t (&w)[3]) {
+  const uint32_t a = __float_as_uint(v[0]), b = __float_as_uint(v[1]), c = __float_as_uint(v[2]),
+                 d = __float_as_uint(v[3]);
+  w[0] = __byte_perm(a, b, 0x5321);
+  w[1] = __byte_perm(b, c, 0x6532);
+  w[2] = __byte_perm(c, d, 0x7653);
+}
+MOE_DEV void unpack24(uint32_t w0, uint32_t w1, uint32_t w2, float (&v)[4]) {
+  v[0] = __uint_as_float(__byte_perm(w0, 0, 0x2100));
+  v[1] = __uint_as_float(__byte_perm(w0, w1, 0x5433));
+  v[2] = __uint_as_float(__byte_perm(w1, w2, 0x4322));
+  v[3] = __uint_as_float(__byte_perm(w2, 0, 0x3211));
 }
 
-// lo is kept with its sign turned, as hi - x: that is one instruction, and so
-// is x = hi - lo.
-MOE_DEV uint32_t pack_lo2(float a, float b, uint32_t h) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(half_minus(h, a), half_minus(h >> 16, b)), __NV_SATFINITE, __NV_E5M2);
-}
-
-// Four values from two packed pairs of hi and four bytes of lo.
-MOE_DEV void unpack_hi_lo4(uint32_t h01, uint32_t h23, uint32_t lo, float (&x)[4]) {
-  const float2 l01 = unpack_half2(__byte_perm(lo, 0, 0x1404)), l23 = unpack_half2(__byte_perm(lo, 0, 0x3424));
-  x[0] = half_minus(h01, l01.x), x[1] = half_minus(h01 >> 16, l01.y);
-  x[2] = half_minus(h23, l23.x), x[3] = half_minus(h23 >> 16, l23.y);
+// Boxes of one matrix in X's private copy come tile by tile, in a tile CTA by
+// CTA, warp by warp (column part, lane quarter), two boxes each: the number of
+// the box that holds row i, column j.
+MOE_DEV size_t x_box(int mat, int nt, int ntn, int i, int j) {
+  const size_t tile = (static_cast<size_t>(mat) * nt + (i >> 8)) * ntn + (j >> 8);
+  return ((tile * 2 + ((i >> 7) & 1)) * kEpiWarps + ((j >> 6) & 3) * 4 + ((i >> 5) & 3)) * 2 + ((j >> 5) & 1);
 }
 
 // X_0 in 64 x 64 tiles (zeros past the matrix), transposed for a tall one.
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
                                                       const int nesterov, const int m, const int n, const int mp,
                                                       const int np, const int chunks, const float eps,
                                                       const float* __restrict__ partial, __half* __restrict__ hi,
-                                                      uint8_t* __restrict__ lo) {
+                                                      uint8_t* __restrict__ x) {
   __shared__ float tile[64][65];
   __shared__ float red[8];
   griddep_wait();  // the partial sums and the momentum come from the previous kernel
@@ -271,11 +284,27 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
 #pragma unroll
   for (int r = wr; r < 64; r += 16) {
     const float a = tile[r][wc], b = tile[r][wc + 1], c = tile[r][wc + 2], d = tile[r][wc + 3];
-    const uint32_t h0 = pack_half2(a, b), h1 = pack_half2(c, d);
     const size_t o = (static_cast<size_t>(mat) * mp + ti * 64 + r) * np + tj * 64 + wc;
-    *reinterpret_cast<uint2*>(hi + o) = make_uint2(h0, h1);
-    *reinterpret_cast<uint32_t*>(lo + o) = pack_lo2(a, b, h0) | (pack_lo2(c, d, h1) << 16);
+    *reinterpret_cast<uint2*>(hi + o) = make_uint2(pack_half2(a, b), pack_half2(c, d));
   }
+  // the private copy: four boxes, two warps each, a lane a row of 16 columns
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int br = (w >> 1 & 1) * 32, bc = (w >> 2) * 32, half = w & 1;
+  uint32_t word[12];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = tile[br + lane][bc + 16 * half + 4 * k + j];
+    uint32_t three[3];
+    pack24(v, three);
+    word[3 * k] = three[0], word[3 * k + 1] = three[1], word[3 * k + 2] = three[2];
+  }
+  uint8_t* box = x + x_box(mat, (mp + kTile - 1) / kTile, (np + kTile - 1) / kTile, ti * 64 + br, tj * 64 + bc) * kBoxX;
+#pragma unroll
+  for (int c = 0; c < 3; ++c)
+    *reinterpret_cast<uint4*>(box + (3 * half + c) * 512 + lane * 16) =
+        make_uint4(word[4 * c], word[4 * c + 1], word[4 * c + 2], word[4 * c + 3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -288,17 +317,16 @@ struct GemmArgs {
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
   float coeff[MOE_MAX_NS_STEPS][3];
-  __half* A;        // [count, mp, mp]
-  __half* B;
-  __half* hi[2];    // X, [count, mp, np], in turns
-  uint8_t* lo[2];
+  uint8_t* x;       // X's private copy (x_box), and A's (boxes as in EpiTile)
+  uint8_t* a;
   float* diag;      // [count, mp]: B's diagonal where it is kept apart
   unsigned int* done;  // [count, 3 * steps] halves of tiles that are complete
   NsOutput out;
 };
 
 struct NsMaps {
-  CUtensorMap X[2], A, B;  // operands: 128 rows x two 64-column blocks
+  CUtensorMap X[2], A, B;           // operands: 128 rows x two 64-column blocks
+  CUtensorMap boxX[2], boxA, boxB;  // the same arrays in 32 x 32 boxes
 };
 
 struct Ctl {
@@ -409,20 +437,22 @@ MOE_DEV void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar
       : "memory");
 }
 
-// Instruction descriptor of tcgen05.mma.kind::f16: fp16 A (K-major) and B
-// (K-major or N-major), fp32 D.
-MOE_DEV uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn_major) {
-  return (1u << 4) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// Instruction descriptor of tcgen05.mma.kind::f16: fp16 A and B, each K-major
+// or not, fp32 D.
+MOE_DEV uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn_major, uint32_t b_mn_major) {
+  return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// An epilogue warp's fp32 box in shared memory, 16 rows x 32 columns: 16-byte
-// chunk c of row r at chunk c ^ (r % 8) ^ 4 (r / 8).  Every access below is
-// free of bank conflicts.  TMEM gives a lane a whole row; memory wants
-// neighbouring lanes on neighbouring columns, so the box is turned: lane l
-// then holds, for i = 0 and 1, the 8 columns from 8 (l % 4) of row 8 i + l / 4
-// (elements 8 i .. 8 i + 7), and what the epilogue reads and writes goes 8
-// rows of 64 bytes at a time.  (With each lane on its own row, 32 cache lines
-// an access, the epilogue of X took 12 us a tile where the product takes 5.)
+// Whether k block kb of the row tile t of a symmetric operand lies above the
+// diagonal, where only its mirror image is stored.
+MOE_DEV bool above(int kb, int t) { return kb / (kTile / kBK) > t; }
+
+// The results (and the weights they move) lie in rows of the stack's own
+// matrices, so there the box is turned: half of it at a time, 16 rows x 32
+// columns in fp32, 16-byte chunk c of row r at chunk c ^ (r % 8) ^ 4 (r / 8),
+// free of bank conflicts.  TMEM gives a lane a whole row; after the turn lane
+// l holds, for i = 0 and 1, the 8 columns from 8 (l % 4) of row 8 i + l / 4
+// (elements 8 i .. 8 i + 7).
 //
 // Addresses are one XOR and a constant away from three per-lane bases.  The
 // empty asm keeps the compiler from holding all of them in registers around
@@ -488,29 +518,12 @@ MOE_DEV void box_get_turned(uint32_t buf, float (&v)[16]) {
                    : "memory");
 }
 
-// Eight values as fp16.
-MOE_DEV void store_halves8(__half* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
-}
-
-// The 8 columns of the lane's rows 8 i + l / 4, i = 0 .. 3, of a box as packed
-// pairs, through L2.
-MOE_DEV void load_halves(const __half* p, size_t pitch, uint32_t (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + 8 * i * pitch));
-    v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-  }
-}
-
 // What an epilogue warp knows of its tile.
 struct EpiTile {
   int mat, step, cur;
-  bool mirror;          // below the diagonal of a symmetric product
   bool late;            // B's diagonal is kept apart
   int row0, col0;       // the warp's first row and column
-  size_t at;            // this lane's first element, in the output
+  uint8_t* own;         // the lane's piece of the first box in X's or A's private copy
   uint32_t taddr;       // its accumulator
   uint32_t tfull, tphase, tempty;
   uint32_t buf;         // the warp's box (shared memory)
@@ -535,14 +548,12 @@ MOE_DEV void release(const EpiTile& t) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(t.tempty) : "memory");
 }
 
-// The four epilogues, on two boxes of 32 columns.  Each asks for what it reads
-// (A, or X's hi and lo) of the first before it waits for the accumulator and
-// of the second after the first; sixteen warps with little in flight each
-// hide the rest.  Little may spill here: shared memory leaves the L1 cache 28
-// KB, so spilled registers come back from L2.  (Eight warps that asked for
-// all of it at once: 0.9 KB a thread spilled, 2300 cycles a box.)  For the
-// same reason every load into registers is made without a condition:
-// registers written under one stay live around the loop over tiles.
+// The four epilogues, on two boxes of 32 columns, a lane a row.  Each asks for
+// what it reads (A, or X) of the first box before it waits for the accumulator
+// and of the second before it works on the first.  Little may spill here:
+// shared memory leaves the L1 cache 28 KB, so spilled registers come back from
+// L2.  For the same reason every load into registers is made without a
+// condition: registers written under one stay live around the loop over tiles.
 
 // A tile whose part for this warp lies outside the matrix.
 MOE_DEV bool epilogue_none(const EpiTile& t) {
@@ -558,146 +569,137 @@ MOE_DEV void take(const EpiTile& t, int b, uint32_t (&acc)[32]) {
   if (b == 1) release(t);
 }
 
-// Half a box into the lanes' 8-column pieces.
-MOE_DEV void turn(const EpiTile& t, const uint32_t (&acc)[32], int h, float (&v)[16]) {
-  __syncwarp();
-  box_put_half(t.buf, acc, h);
-  __syncwarp();
-  box_get(t.buf, v);
+// A lane's 4 N words of a private box, 16 bytes from each run of 512, through L2.
+template <int N>
+MOE_DEV void load_own(const uint8_t* p, uint32_t (&w)[4 * N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + c * 512));
+    w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
+  }
 }
 
-// Half a box of a symmetric product, from shared memory to its mirror place.
-MOE_DEV void store_mirror(__half* out, const GemmArgs& p, const EpiTile& t, int b, int h, float scale) {
+// The box as fp16 to its place in an operand: through the warp's buffer
+// (64-byte swizzle: 16-byte chunk c of row r at c ^ ((r / 2) % 4)) and TMA.
+MOE_DEV void store_box(const CUtensorMap* map, const EpiTile& t, int b, const uint32_t (&h)[16]) {
   const uint32_t l = lane_id();
-  float v[16];
-  box_get_turned(t.buf, v);
+  if (l == 0) bulk_wait_group_read0();  // the store before has read the buffer
+  __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] *= scale;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    store_halves8(out + (static_cast<size_t>(t.mat) * p.mp + t.col0 + b * kBox + 16 * i + (l >> 1)) * p.mp + t.row0 +
-                      16 * h + 8 * (l & 1),
-                  v + 8 * i);
+  for (int c = 0; c < 4; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t.buf + l * 64 + ((c ^ ((l >> 1) & 3)) << 4)),
+                 "r"(h[4 * c]), "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
+                 : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (l == 0) {
+    tma_store_3d(map, t.buf, t.col0 + b * kBox, t.row0, t.mat);
+    bulk_commit_group();
+  }
 }
 
 // A = X X^T.
-MOE_DEV bool epilogue_gram(const GemmArgs& p, const EpiTile& t) {
+MOE_DEV bool epilogue_gram(const NsMaps& maps, const EpiTile& t) {
   if (!wait_acc(t)) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    uint32_t acc[32];
+    uint32_t acc[32], h[16];
     take(t, b, acc);
+    constexpr float f = 1.f / (kScaleX * kScaleX);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[16];
-      turn(t, acc, h, v);
+    for (int j = 0; j < 16; ++j)
+      h[j] = pack_half2(__uint_as_float(acc[2 * j]) * f, __uint_as_float(acc[2 * j + 1]) * f);
+    store_box(&maps.boxA, t, b, h);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] *= 1.f / (kScaleX * kScaleX);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) store_halves8(p.A + t.at + b * kBox + (16 * h + 8 * i) * p.mp, v + 8 * i);
-      if (t.mirror) store_mirror(p.A, p, t, b, h, 1.f / (kScaleX * kScaleX));
-    }
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(t.own + b * kBoxA + c * 512) =
+          make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
   }
   return true;
 }
 
 // B = b A + c A A.
-MOE_DEV bool epilogue_poly(const GemmArgs& p, const EpiTile& t) {
+MOE_DEV bool epilogue_poly(const NsMaps& maps, const GemmArgs& p, const EpiTile& t) {
   const uint32_t l = lane_id();
-  uint32_t pre[2][16];
-  load_halves(p.A + t.at, p.mp, pre[0]);
+  uint32_t a[2][16];
+  load_own<4>(t.own, a[0]);
   const float cb = p.coeff[t.step][1], cc = p.coeff[t.step][2];
   if (!wait_acc(t)) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    uint32_t acc[32];
+    uint32_t acc[32], h[16];
     take(t, b, acc);
+    if (b == 0) load_own<4>(t.own + kBoxA, a[1]);
+    const bool diagonal = t.late && t.row0 == t.col0 + b * kBox;
+    float mine = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[16];
-      turn(t, acc, h, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 a = unpack_half2(pre[b][8 * h + j]);
-        v[2 * j] = fmaf(cc, v[2 * j], cb * a.x);
-        v[2 * j + 1] = fmaf(cc, v[2 * j + 1], cb * a.y);
+    for (int j = 0; j < 16; ++j) {
+      const float2 x = unpack_half2(a[b][j]);
+      float u = fmaf(cc, __uint_as_float(acc[2 * j]), cb * x.x);
+      float v = fmaf(cc, __uint_as_float(acc[2 * j + 1]), cb * x.y);
+      if (diagonal) {
+        if (l == 2 * j) mine = u, u = 0.f;
+        if (l == 2 * j + 1) mine = v, v = 0.f;
       }
-      // the lane's row 16 h + 8 i + l / 4 meets its columns where 2 h + i = l % 4
-      if (t.late && t.row0 == t.col0 + b * kBox) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if ((l & 3) == 2 * h + j / 8 && (l >> 2) == j % 8) {
-            p.diag[static_cast<size_t>(t.mat) * p.mp + t.row0 + 16 * h + j] = v[j];
-            v[j] = 0.f;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) store_halves8(p.B + t.at + b * kBox + (16 * h + 8 * i) * p.mp, v + 8 * i);
-      if (t.mirror) {
-        __syncwarp();
-        box_put(t.buf, v);
-        __syncwarp();
-        store_mirror(p.B, p, t, b, h, 1.f);
-      }
+      h[j] = pack_half2(u, v);
     }
-    if (b == 0) load_halves(p.A + t.at + kBox, p.mp, pre[1]);
+    if (diagonal) p.diag[static_cast<size_t>(t.mat) * p.mp + t.row0 + l] = mine;
+    store_box(&maps.boxB, t, b, h);
   }
   return true;
 }
 
-// a plus, where it is kept apart, B's diagonal, for the lane's four rows.
-MOE_DEV void row_factors(const GemmArgs& p, const EpiTile& t, float (&ca)[4]) {
+// a plus, where it is kept apart, B's diagonal, for the lane's row.
+MOE_DEV float row_factor(const GemmArgs& p, const EpiTile& t) {
+  const float d = __ldcg(p.diag + static_cast<size_t>(t.mat) * p.mp + t.row0 + lane_id());
+  return p.coeff[t.step][0] + (t.late ? d : 0.f);
+}
+
+// acc <- f X + acc: the lane's row of the next X.
+MOE_DEV void add_linear(float f, const uint32_t (&x)[24], uint32_t (&acc)[32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ca[i] = p.coeff[t.step][0];
-    if (t.late) ca[i] += __ldcg(p.diag + static_cast<size_t>(t.mat) * p.mp + t.row0 + 8 * i + (lane_id() >> 2));
+  for (int k = 0; k < 8; ++k) {
+    float v[4];
+    unpack24(x[3 * k], x[3 * k + 1], x[3 * k + 2], v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[4 * k + j] = __float_as_uint(fmaf(f, v[j], __uint_as_float(acc[4 * k + j])));
   }
 }
 
 // X <- a X + B X.
-MOE_DEV bool epilogue_apply(const GemmArgs& p, const EpiTile& t) {
-  uint32_t hi[2][16], lo[2][8];
-  auto load = [&](int b) {
-    load_halves(p.hi[t.cur] + t.at + b * kBox, p.np, hi[b]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2 u = __ldcg(reinterpret_cast<const uint2*>(p.lo[t.cur] + t.at + b * kBox + 8 * i * p.np));
-      lo[b][2 * i] = u.x, lo[b][2 * i + 1] = u.y;
-    }
-  };
-  load(0);
-  float ca[4];
-  row_factors(p, t, ca);
+MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, const EpiTile& t) {
+  uint32_t x[2][24];
+  load_own<6>(t.own, x[0]);
+  const float f = row_factor(p, t);
   if (!wait_acc(t)) return false;
-  const bool keep_lo = t.step + 2 < p.steps;  // the last step's X has none
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     uint32_t acc[32];
     take(t, b, acc);
+    add_linear(f, x[b], acc);
+    if (b == 0) load_own<6>(t.own + kBoxX, x[1]);
+    uint32_t h[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[16];
-      turn(t, acc, h, v);
+    for (int j = 0; j < 16; ++j) h[j] = pack_half2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1]));
+    store_box(&maps.boxX[t.cur ^ 1], t, b, h);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * h + i;  // row 8 r + l / 4
-        uint32_t w[4], n[2];
+    for (int c = 0; c < 2; ++c) {
+      uint32_t w[12];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x[4];
-          unpack_hi_lo4(hi[b][4 * r + 2 * j], hi[b][4 * r + 2 * j + 1], lo[b][2 * r + j], x);
+      for (int k = 0; k < 4; ++k) {
+        float v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = fmaf(ca[r], x[k], v[8 * i + 4 * j + k]);
-          w[2 * j] = pack_half2(x[0], x[1]);
-          w[2 * j + 1] = pack_half2(x[2], x[3]);
-          n[j] = pack_lo2(x[0], x[1], w[2 * j]) | (pack_lo2(x[2], x[3], w[2 * j + 1]) << 16);
-        }
-        const size_t at = t.at + b * kBox + 8 * r * p.np;
-        *reinterpret_cast<uint4*>(p.hi[t.cur ^ 1] + at) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (keep_lo) *reinterpret_cast<uint2*>(p.lo[t.cur ^ 1] + at) = make_uint2(n[0], n[1]);
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(acc[16 * c + 4 * k + j]);
+        uint32_t three[3];
+        pack24(v, three);
+        w[3 * k] = three[0], w[3 * k + 1] = three[1], w[3 * k + 2] = three[2];
       }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(t.own + b * kBoxX + (3 * c + k) * 512) =
+            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
-    if (b == 0) load(1);
   }
   return true;
 }
@@ -736,10 +738,9 @@ MOE_DEV void store_bf16(void* base, size_t el, int stop, bool vec, const float* 
 // elements of the stack's own rows.
 MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile& t) {
   const uint32_t l = lane_id();
-  uint32_t hi[2][16];
-  load_halves(p.hi[t.cur] + t.at, p.np, hi[0]);
-  float ca[4];
-  row_factors(p, t, ca);
+  uint32_t x[2][24];
+  load_own<6>(t.own, x[0]);
+  const float f = row_factor(p, t);
   const NsStack& s = st.s[stack_of(st, t.mat)];
   const size_t base = static_cast<size_t>(t.mat - s.first) * p.m * p.n;
   const int rows = s.tall ? p.n : p.m, cols = s.tall ? p.m : p.n;  // the stack's own
@@ -749,6 +750,8 @@ MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile&
   for (int b = 0; b < 2; ++b) {
     uint32_t acc[32];
     take(t, b, acc);
+    add_linear(f, x[b], acc);
+    if (b == 0) load_own<6>(t.own + kBoxX, x[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // the lane's two runs in the stack's own matrix
@@ -762,14 +765,12 @@ MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile&
         load_bf16(s.weight, base + static_cast<size_t>(r0 + rstep * i) * cols + c0, stop, vec, w[i]);
       }
       float v[16];
-      turn(t, acc, h, v);
+      __syncwarp();
+      box_put_half(t.buf, acc, h);
+      __syncwarp();
+      box_get(t.buf, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 x = unpack_half2(hi[b][8 * h + j]);
-        const float f = ca[2 * h + j / 4];
-        v[2 * j] = fmaf(f, x.x, v[2 * j]) * (1.f / kScaleX);
-        v[2 * j + 1] = fmaf(f, x.y, v[2 * j + 1]) * (1.f / kScaleX);
-      }
+      for (int j = 0; j < 16; ++j) v[j] *= 1.f / kScaleX;
       if (s.tall) {
         __syncwarp();
         box_put(t.buf, v);
@@ -797,7 +798,6 @@ MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile&
         }
       }
     }
-    if (b == 0) load_halves(p.hi[t.cur] + t.at + kBox, p.np, hi[1]);
   }
   return true;
 }
@@ -867,8 +867,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sp = smem_base + stage * kStageBytes, sq = sp + kOperandBytes;
           // both CTAs' boxes count in full, rows and k past the matrix are zeros
           if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), 2 * kStageBytes);
-          tma_load_4d_pair(sp, mp, bar, 0, t.ti * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
-          if (kind == kApply)
+          // 128 rows of the operand and 128 k, or the mirror image of that
+          if (kind != kGram && above(kb, t.ti))
+            tma_load_4d_pair(sp, mp, bar, 0, kb * kBK, t.ti * (kTile / 64) + 2 * rank, t.mat, policy);
+          else
+            tma_load_4d_pair(sp, mp, bar, 0, t.ti * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
+          if (kind == kApply || (kind == kPoly && above(kb, t.tj)))
             tma_load_4d_pair(sq, mq, bar, 0, kb * kBK, t.tj * (kTile / 64) + 2 * rank, t.mat, policy);
           else
             tma_load_4d_pair(sq, mq, bar, 0, t.tj * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
@@ -903,9 +907,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = i & 1;
         if (!mbar_wait_cluster(smem_u32(&ctl.tempty[buf]), ((i >> 1) & 1) ^ 1u, abort_flag, dev_err)) break;
         tc_fence_after_sync();
-        const bool n_major = t.prod % 3 == kApply;
-        const uint32_t idesc = idesc_f16_f32(kTile, kTile, n_major ? 1u : 0u);
-        const int K = t.prod % 3 == kGram ? p.np : p.mp;
+        const int kind = t.prod % 3;
+        const int K = kind == kGram ? p.np : p.mp;
         const int nkb = (K + kBK - 1) / kBK;
         const uint32_t d = tmem_base + buf * kTile;
         for (int kb = 0; kb < nkb; ++kb) {
@@ -915,10 +918,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after_sync();
           const uint32_t sp = smem_base + stage * kStageBytes, sq = sp + kOperandBytes;
+          const bool m_major = kind != kGram && above(kb, t.ti);
+          const bool n_major = kind == kApply || (kind == kPoly && above(kb, t.tj));
+          const uint32_t idesc = idesc_f16_f32(kTile, kTile, m_major, n_major);
           const int slices = K - kb * kBK >= kBK ? kBK / 16 : 4;  // K is a multiple of 64
           for (int kk = 0; kk < slices; ++kk) {
             const uint32_t off = (kk >> 2) * kAtomBytes + (kk & 3) * 32;
-            const uint64_t pd = smem_desc_sw128(sp + off, 16, 1024);
+            const uint64_t pd = m_major ? smem_desc_sw128(sp + kk * 2048, kAtomBytes, 1024)
+                                        : smem_desc_sw128(sp + off, 16, 1024);
             const uint64_t qd = n_major ? smem_desc_sw128(sq + kk * 2048, kAtomBytes, 1024)
                                         : smem_desc_sw128(sq + off, 16, 1024);
             umma_bf16_pair(d, pd, qd, idesc, (kb | kk) != 0 ? 1u : 0u);
@@ -975,12 +982,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kind = t.prod % 3, step = t.prod / 3, buf = i & 1;
       EpiTile e;
       e.mat = t.mat, e.step = step, e.cur = step & 1;
-      e.mirror = t.ti != t.tj;
       e.late = step + 2 >= p.steps;
       e.row0 = t.ti * kTile + 128 * static_cast<int>(rank) + q * 32;
       e.col0 = t.tj * kTile + part * 2 * kBox;
       const int ncols = kind == kApply ? p.np : p.mp;
-      e.at = (static_cast<size_t>(t.mat) * p.mp + e.row0 + (lane >> 2)) * ncols + e.col0 + 8 * (lane & 3);
+      const int nt = (p.mp + kTile - 1) / kTile, ntn = (p.np + kTile - 1) / kTile;
+      const size_t tile = kind == kApply ? (static_cast<size_t>(t.mat) * nt + t.ti) * ntn + t.tj
+                                         : static_cast<size_t>(t.mat) * (nt * (nt + 1) / 2) + t.ti * (t.ti + 1) / 2 + t.tj;
+      e.own = (kind == kApply ? p.x : p.a) + lane * 16 +
+              ((tile * 2 + rank) * kEpiWarps + part * 4 + q) * 2 * (kind == kApply ? kBoxX : kBoxA);
       e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 2 * kBox;
       e.tfull = smem_u32(&ctl.tfull[buf]);
       e.tphase = (i >> 1) & 1;
@@ -995,15 +1005,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e.row0 >= p.mp || e.col0 >= ncols)
         got = epilogue_none(e);
       else if (kind == kGram)
-        got = epilogue_gram(p, e);
+        got = epilogue_gram(maps, e);
       else if (kind == kPoly)
-        got = epilogue_poly(p, e);
+        got = epilogue_poly(maps, p, e);
       else if (step + 1 < p.steps)
-        got = epilogue_apply(p, e);
+        got = epilogue_apply(maps, p, e);
       else
         got = epilogue_last(p, st, e);
       if (!got) break;
       __syncwarp();
+      if (lane == 0) bulk_wait_group0();  // TMA stores are complete for their own thread only
       if (lane == 0) count_store(&ctl.written[warp - 2], i + 1);
     }
     __syncwarp();
@@ -1026,7 +1037,7 @@ struct Buffers {
   float *partial, *diag;
   unsigned int* done;
   __half *hi[2], *A, *B;
-  uint8_t* lo[2];
+  uint8_t *x, *a;
   size_t bytes;
 };
 
@@ -1043,7 +1054,9 @@ Buffers carve(void* base, int count, int mp, int np) {
   w.done = reinterpret_cast<unsigned int*>(take(static_cast<size_t>(count) * 3 * MOE_MAX_NS_STEPS * 4));
   w.diag = reinterpret_cast<float*>(take(static_cast<size_t>(count) * mp * 4));
   for (int i = 0; i < 2; ++i) w.hi[i] = reinterpret_cast<__half*>(take(2 * x));
-  for (int i = 0; i < 2; ++i) w.lo[i] = reinterpret_cast<uint8_t*>(take(x));
+  const size_t nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile, boxes = 2 * kEpiWarps * 2;
+  w.x = reinterpret_cast<uint8_t*>(take(count * nt * ntn * boxes * kBoxX));
+  w.a = reinterpret_cast<uint8_t*>(take(count * (nt * (nt + 1) / 2) * boxes * kBoxA));
   w.A = reinterpret_cast<__half*>(take(a));
   w.B = reinterpret_cast<__half*>(take(a));
   w.bytes = off;
@@ -1118,6 +1131,19 @@ cudaError_t operand_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, c
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// [count, rows, cols] fp16 in 32 x 32 boxes with the 64-byte swizzle.
+cudaError_t box_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* p, int count, int rows,
+                    int cols) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows) * cols * 2};
+  cuuint32_t box[3] = {kBox, kBox, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename GT, int VEC>
 cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, cudaStream_t s) {
   const size_t elems = static_cast<size_t>(pr.m) * pr.n;
@@ -1129,7 +1155,7 @@ cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, 
   if (e != cudaSuccess) return e;
   return launch_kernel(ns_load_kernel<GT, VEC>, dim3((mp / 64) * (np / 64), pr.count), dim3(256), 0, s, true,
                        pr.stacks, pr.momentum, pr.nesterov, pr.m, pr.n, mp, np, chunks, pr.eps,
-                       static_cast<const float*>(w.partial), w.hi[0], w.lo[0]);
+                       static_cast<const float*>(w.partial), w.hi[0], w.x);
 }
 
 }  // namespace
@@ -1157,7 +1183,11 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
 
   NsMaps maps;
   for (int i = 0; i < 2; ++i)
-    if ((e = operand_map(enc, &maps.X[i], w.hi[i], count, mp, np)) != cudaSuccess) return e;
+    if ((e = operand_map(enc, &maps.X[i], w.hi[i], count, mp, np)) != cudaSuccess ||
+        (e = box_map(enc, &maps.boxX[i], w.hi[i], count, mp, np)) != cudaSuccess)
+      return e;
+  if ((e = box_map(enc, &maps.boxA, w.A, count, mp, mp)) != cudaSuccess) return e;
+  if ((e = box_map(enc, &maps.boxB, w.B, count, mp, mp)) != cudaSuccess) return e;
   if ((e = operand_map(enc, &maps.A, w.A, count, mp, mp)) != cudaSuccess) return e;
   if ((e = operand_map(enc, &maps.B, w.B, count, mp, mp)) != cudaSuccess) return e;
 
@@ -1168,8 +1198,7 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   for (int k = 0; k < pr.steps; ++k)
     for (int j = 0; j < 3; ++j) a.coeff[k][j] = pr.coeff[k][j];
-  a.A = w.A, a.B = w.B;
-  for (int i = 0; i < 2; ++i) a.hi[i] = w.hi[i], a.lo[i] = w.lo[i];
+  a.x = w.x, a.a = w.a;
   a.diag = w.diag;
   a.done = w.done;
   a.out = pr.out;
