@@ -13,12 +13,13 @@
 // fp32 sums.  fp16 and not bf16 because every operand has a known range
 // (singular values below about 1.3, so entries do too): scaled by a power of
 // two it holds 3 bits more at the same rate.  Two things are kept apart:
-//  * The term a X is not part of a product and keeps X to 16 bits (the upper
-//    three bytes of its fp32), beside the fp16 that the products read.  It
-//    matters where G has less than full rank (an expert with fewer tokens
-//    than rows): what rounding leaves outside the row space grows by a in
-//    every step, 485-fold in five with a = 3.4445, and nothing contracts it.
-//    The products need no more bits there: A is small.
+//  * The term a X is not part of a product and keeps X to about 14 bits, as
+//    fp16 and what that leaves in e5m2 (hi + lo; not for the last step's
+//    X).  e5m2 is the upper byte of an fp16, so it needs no scale and is
+//    cheap to widen.  It matters where G has less than full rank (an expert
+//    with fewer tokens than rows): what rounding leaves outside the row space
+//    grows by a in every step, 485-fold in five with a = 3.4445, and nothing
+//    contracts it.  The products need no more bits there: A is small.
 //  * In the last two steps B is close to -2.7 I and cancels most of a X, so
 //    the rounding of its diagonal would be the largest error left.  There the
 //    diagonal goes from product to product in fp32 and the stored B has
@@ -26,18 +27,18 @@
 //    the row space into two differently rounded halves.)
 // Simulated 2-norm errors, of which the bf16 rounding of the result is
 // 1.66e-3: full rank 1.8e-3 to 2.1e-3 (2.3e-3 to 2.6e-3 without the fp32
-// diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 with a X in fp16; with bf16
-// operands 0.9e-1 to 2e-1).
+// diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 without lo; with bf16 operands
+// 0.9e-1 to 2e-1).
 //
 // A and B are symmetric: only the tiles on and below the diagonal are computed
 // and stored.  Where a product needs one from above, it loads the tile from
 // below as the transposed (M- or N-major) operand, which costs nothing.
 //
-// What the epilogues read themselves (A in B's, X in X's) is kept a second
-// time in the order in which they hold it: for each warp and 32 x 32 box,
-// 16-byte pieces of 32 lanes side by side.  So those accesses are whole lines
-// and need no turning in shared memory, whose bandwidth the products use.
-// The operands' copies leave by TMA.
+// What only the epilogues read (lo, and a copy of A) is kept in the order in
+// which they hold it: for each warp and 32 x 32 box, 16-byte pieces of 32
+// lanes side by side.  So those accesses are whole lines and need no turning
+// in shared memory, whose bandwidth the products use.  The operands, hi among
+// them, come and go by TMA.
 //
 // All products of all steps are one persistent launch over 256 x 256 tiles,
 // run by CTA pairs (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM,
@@ -55,6 +56,7 @@
 //   warps 2-17  epilogue
 //   warp 18     counts the tiles whose results are in memory
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -77,7 +79,7 @@ constexpr int kEpiWarps = 16;
 constexpr int kThreads = 96 + 32 * kEpiWarps;
 constexpr int kBox = 32;                       // columns an epilogue warp takes from TMEM at a time
 constexpr int kWarpStage = kBox * kBox * 2;    // its box in shared memory, fp16 (or 16 rows in fp32)
-constexpr int kBoxX = 6 * 512;                 // its box of X: 24 words a lane
+constexpr int kBoxX = 2 * 512;                 // its box of lo: 8 words a lane
 constexpr int kBoxA = 4 * 512;                 // its box of A: 16 words a lane
 constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kWarpStage + 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -190,24 +192,26 @@ MOE_DEV uint32_t pack_half2(float lo, float hi) {
 
 MOE_DEV float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-// Four floats' upper three bytes in three words, and back (the byte that is
-// gone is filled with its neighbour, so that nothing is biased; zero,
-// infinities and NaN stay what they are).
-MOE_DEV void pack24(const float* v, uint32_t (&w)[3]) {
-  const uint32_t a = __float_as_uint(v[0]), b = __float_as_uint(v[1]), c = __float_as_uint(v[2]),
-                 d = __float_as_uint(v[3]);
-  w[0] = __byte_perm(a, b, 0x5321);
-  w[1] = __byte_perm(b, c, 0x6532);
-  w[2] = __byte_perm(c, d, 0x7653);
-}
-MOE_DEV void unpack24(uint32_t w0, uint32_t w1, uint32_t w2, float (&v)[4]) {
-  v[0] = __uint_as_float(__byte_perm(w0, 0, 0x2100));
-  v[1] = __uint_as_float(__byte_perm(w0, w1, 0x5433));
-  v[2] = __uint_as_float(__byte_perm(w1, w2, 0x4322));
-  v[3] = __uint_as_float(__byte_perm(w2, 0, 0x3211));
+MOE_DEV float half_minus(uint32_t h, float c) {  // the low half of h, minus c, in fp32
+  float d;
+  asm("sub.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(static_cast<uint16_t>(h)), "f"(c));
+  return d;
 }
 
-// Boxes of one matrix in X's private copy come tile by tile, in a tile CTA by
+// lo is kept with its sign turned, as hi - x: that is one instruction, and so
+// is x = hi - lo.
+MOE_DEV uint32_t pack_lo2(float a, float b, uint32_t h) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(half_minus(h, a), half_minus(h >> 16, b)), __NV_SATFINITE, __NV_E5M2);
+}
+
+// Four values from two packed pairs of hi and four bytes of lo.
+MOE_DEV void unpack_hi_lo4(uint32_t h01, uint32_t h23, uint32_t lo, float (&x)[4]) {
+  const float2 l01 = unpack_half2(__byte_perm(lo, 0, 0x1404)), l23 = unpack_half2(__byte_perm(lo, 0, 0x3424));
+  x[0] = half_minus(h01, l01.x), x[1] = half_minus(h01 >> 16, l01.y);
+  x[2] = half_minus(h23, l23.x), x[3] = half_minus(h23 >> 16, l23.y);
+}
+
+// Boxes of one matrix's lo come tile by tile, in a tile CTA by
 // CTA, warp by warp (column part, lane quarter), two boxes each: the number of
 // the box that holds row i, column j.
 MOE_DEV size_t x_box(int mat, int nt, int ntn, int i, int j) {
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
                                                       const int nesterov, const int m, const int n, const int mp,
                                                       const int np, const int chunks, const float eps,
                                                       const float* __restrict__ partial, __half* __restrict__ hi,
-                                                      uint8_t* __restrict__ x) {
+                                                      uint8_t* __restrict__ lo) {
   __shared__ float tile[64][65];
   __shared__ float red[8];
   griddep_wait();  // the partial sums and the momentum come from the previous kernel
@@ -287,24 +291,17 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
     const size_t o = (static_cast<size_t>(mat) * mp + ti * 64 + r) * np + tj * 64 + wc;
     *reinterpret_cast<uint2*>(hi + o) = make_uint2(pack_half2(a, b), pack_half2(c, d));
   }
-  // the private copy: four boxes, two warps each, a lane a row of 16 columns
+  // lo: four boxes, two warps each, a lane a row of 16 columns
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int br = (w >> 1 & 1) * 32, bc = (w >> 2) * 32, half = w & 1;
-  uint32_t word[12];
+  uint32_t word[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = tile[br + lane][bc + 16 * half + 4 * k + j];
-    uint32_t three[3];
-    pack24(v, three);
-    word[3 * k] = three[0], word[3 * k + 1] = three[1], word[3 * k + 2] = three[2];
+    const float* v = &tile[br + lane][bc + 16 * half + 4 * k];
+    word[k] = pack_lo2(v[0], v[1], pack_half2(v[0], v[1])) | (pack_lo2(v[2], v[3], pack_half2(v[2], v[3])) << 16);
   }
-  uint8_t* box = x + x_box(mat, (mp + kTile - 1) / kTile, (np + kTile - 1) / kTile, ti * 64 + br, tj * 64 + bc) * kBoxX;
-#pragma unroll
-  for (int c = 0; c < 3; ++c)
-    *reinterpret_cast<uint4*>(box + (3 * half + c) * 512 + lane * 16) =
-        make_uint4(word[4 * c], word[4 * c + 1], word[4 * c + 2], word[4 * c + 3]);
+  uint8_t* box = lo + x_box(mat, (mp + kTile - 1) / kTile, (np + kTile - 1) / kTile, ti * 64 + br, tj * 64 + bc) * kBoxX;
+  *reinterpret_cast<uint4*>(box + half * 512 + lane * 16) = make_uint4(word[0], word[1], word[2], word[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -317,8 +314,9 @@ struct GemmArgs {
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
   float coeff[MOE_MAX_NS_STEPS][3];
-  uint8_t* x;       // X's private copy (x_box), and A's (boxes as in EpiTile)
-  uint8_t* a;
+  const __half* hi[2];  // X, [count, mp, np], in turns
+  uint8_t* lo;      // what hi leaves of X, in boxes (x_box)
+  uint8_t* a;       // the epilogues' copy of A, in boxes
   float* diag;      // [count, mp]: B's diagonal where it is kept apart
   unsigned int* done;  // [count, 3 * steps] halves of tiles that are complete
   NsOutput out;
@@ -335,6 +333,7 @@ struct Ctl {
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
+  uint64_t box[kEpiWarps];
   uint32_t tmem_base;
   int abort;
   int ready;                // tiles whose operands the producer has seen complete
@@ -437,6 +436,15 @@ MOE_DEV void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar
       : "memory");
 }
 
+// A box into this CTA's own shared memory.
+MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
 // Instruction descriptor of tcgen05.mma.kind::f16: fp16 A and B, each K-major
 // or not, fp32 D.
 MOE_DEV uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn_major, uint32_t b_mn_major) {
@@ -523,10 +531,11 @@ struct EpiTile {
   int mat, step, cur;
   bool late;            // B's diagonal is kept apart
   int row0, col0;       // the warp's first row and column
-  uint8_t* own;         // the lane's piece of the first box in X's or A's private copy
+  uint8_t* own;         // the lane's piece of the first box of lo, or of A's copy
   uint32_t taddr;       // its accumulator
   uint32_t tfull, tphase, tempty;
   uint32_t buf;         // the warp's box (shared memory)
+  uint32_t bar, bar_phase;  // and the barrier of loads into it
   volatile int* abort_flag;
   unsigned int* dev_err;
 };
@@ -655,50 +664,72 @@ MOE_DEV float row_factor(const GemmArgs& p, const EpiTile& t) {
   return p.coeff[t.step][0] + (t.late ? d : 0.f);
 }
 
-// acc <- f X + acc: the lane's row of the next X.
-MOE_DEV void add_linear(float f, const uint32_t (&x)[24], uint32_t (&acc)[32]) {
+// The lane's 32 columns of hi, straight from its row.
+MOE_DEV void load_row(const __half* p, uint32_t (&h)[16]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float v[4];
-    unpack24(x[3 * k], x[3 * k + 1], x[3 * k + 2], v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc[4 * k + j] = __float_as_uint(fmaf(f, v[j], __uint_as_float(acc[4 * k + j])));
+  for (int c = 0; c < 4; ++c) {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p) + c);
+    h[4 * c] = u.x, h[4 * c + 1] = u.y, h[4 * c + 2] = u.z, h[4 * c + 3] = u.w;
   }
 }
 
-// X <- a X + B X.
-MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, const EpiTile& t) {
-  uint32_t x[2][24];
-  load_own<6>(t.own, x[0]);
+MOE_DEV const __half* row_of(const GemmArgs& p, const EpiTile& t) {
+  return p.hi[t.cur] + (static_cast<size_t>(t.mat) * p.mp + t.row0 + lane_id()) * p.np + t.col0;
+}
+
+// X <- a X + B X.  hi of the first box comes by TMA into the buffer that the
+// box leaves from, hi of the second straight into registers (there is no
+// shared memory for a second buffer); both are in L2, as operands.
+MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, EpiTile& t) {
+  const uint32_t l = lane_id();
+  uint32_t hi[16], lo[2][8];
+  if (l == 0) {
+    mbar_arrive_expect_tx(t.bar, kWarpStage);
+    tma_load_3d(t.buf, &maps.boxX[t.cur], t.bar, t.col0, t.row0, t.mat);
+  }
+  load_own<2>(t.own, lo[0]);
+  load_own<2>(t.own + kBoxX, lo[1]);
+  load_row(row_of(p, t) + kBox, hi);
   const float f = row_factor(p, t);
-  if (!wait_acc(t)) return false;
+  const bool ok = wait_acc(t);
+  // also when given up: the copy lands before the CTA exits
+  volatile int local_abort = 0;
+  mbar_wait(t.bar, t.bar_phase, &local_abort, t.dev_err);
+  t.bar_phase ^= 1u;
+  if (!ok) return false;
+  const bool keep_lo = t.step + 2 < p.steps;  // the last step's X has none
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    uint32_t acc[32];
+    uint32_t acc[32], h[16];
     take(t, b, acc);
-    add_linear(f, x[b], acc);
-    if (b == 0) load_own<6>(t.own + kBoxX, x[1]);
-    uint32_t h[16];
+    if (b == 0) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = pack_half2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1]));
+      for (int c = 0; c < 4; ++c)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(h[4 * c]), "=r"(h[4 * c + 1]), "=r"(h[4 * c + 2]), "=r"(h[4 * c + 3])
+                     : "r"(t.buf + l * 64 + ((c ^ ((l >> 1) & 3)) << 4))
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) h[j] = hi[j];
+    }
+    uint32_t n[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x[4];
+      unpack_hi_lo4(h[2 * k], h[2 * k + 1], lo[b][k], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = fmaf(f, x[j], __uint_as_float(acc[4 * k + j]));
+      h[2 * k] = pack_half2(x[0], x[1]);
+      h[2 * k + 1] = pack_half2(x[2], x[3]);
+      n[k] = pack_lo2(x[0], x[1], h[2 * k]) | (pack_lo2(x[2], x[3], h[2 * k + 1]) << 16);
+    }
     store_box(&maps.boxX[t.cur ^ 1], t, b, h);
+    if (keep_lo) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t w[12];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(acc[16 * c + 4 * k + j]);
-        uint32_t three[3];
-        pack24(v, three);
-        w[3 * k] = three[0], w[3 * k + 1] = three[1], w[3 * k + 2] = three[2];
-      }
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(t.own + b * kBoxX + (3 * c + k) * 512) =
-            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint4*>(t.own + b * kBoxX + c * 512) =
+            make_uint4(n[4 * c], n[4 * c + 1], n[4 * c + 2], n[4 * c + 3]);
     }
   }
   return true;
@@ -738,8 +769,8 @@ MOE_DEV void store_bf16(void* base, size_t el, int stop, bool vec, const float* 
 // elements of the stack's own rows.
 MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile& t) {
   const uint32_t l = lane_id();
-  uint32_t x[2][24];
-  load_own<6>(t.own, x[0]);
+  uint32_t hi[2][16];
+  load_row(row_of(p, t), hi[0]);
   const float f = row_factor(p, t);
   const NsStack& s = st.s[stack_of(st, t.mat)];
   const size_t base = static_cast<size_t>(t.mat - s.first) * p.m * p.n;
@@ -750,8 +781,13 @@ MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile&
   for (int b = 0; b < 2; ++b) {
     uint32_t acc[32];
     take(t, b, acc);
-    add_linear(f, x[b], acc);
-    if (b == 0) load_own<6>(t.own + kBoxX, x[1]);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 x = unpack_half2(hi[b][j]);
+      acc[2 * j] = __float_as_uint(fmaf(f, x.x, __uint_as_float(acc[2 * j])));
+      acc[2 * j + 1] = __float_as_uint(fmaf(f, x.y, __uint_as_float(acc[2 * j + 1])));
+    }
+    if (b == 0) load_row(row_of(p, t) + kBox, hi[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // the lane's two runs in the stack's own matrix
@@ -827,7 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
     ctl.ready = 0;
-    for (int w = 0; w < kEpiWarps; ++w) ctl.written[w] = 0;
+    for (int w = 0; w < kEpiWarps; ++w) {
+      ctl.written[w] = 0;
+      mbar_init(smem_u32(&ctl.box[w]), 1);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -977,6 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty1 = map_to_cta(smem_u32(&ctl.tempty[1]), 0);
     const uint32_t box = smem_base + kStages * kStageBytes + (warp - 2) * kWarpStage;
     int i = 0;
+    uint32_t bar_phase = 0;
     Walk t;
     for (int idx = pair; t.to(p, idx); idx += npairs, ++i) {
       const int kind = t.prod % 3, step = t.prod / 3, buf = i & 1;
@@ -989,13 +1029,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = (p.mp + kTile - 1) / kTile, ntn = (p.np + kTile - 1) / kTile;
       const size_t tile = kind == kApply ? (static_cast<size_t>(t.mat) * nt + t.ti) * ntn + t.tj
                                          : static_cast<size_t>(t.mat) * (nt * (nt + 1) / 2) + t.ti * (t.ti + 1) / 2 + t.tj;
-      e.own = (kind == kApply ? p.x : p.a) + lane * 16 +
+      e.own = (kind == kApply ? p.lo : p.a) + lane * 16 +
               ((tile * 2 + rank) * kEpiWarps + part * 4 + q) * 2 * (kind == kApply ? kBoxX : kBoxA);
       e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 2 * kBox;
       e.tfull = smem_u32(&ctl.tfull[buf]);
       e.tphase = (i >> 1) & 1;
       e.tempty = buf ? tempty1 : tempty0;
       e.buf = box;
+      e.bar = smem_u32(&ctl.box[warp - 2]), e.bar_phase = bar_phase;
       e.abort_flag = abort_flag;
       e.dev_err = dev_err;
       bool got = true;
@@ -1012,6 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         got = epilogue_apply(maps, p, e);
       else
         got = epilogue_last(p, st, e);
+      bar_phase = e.bar_phase;
       if (!got) break;
       __syncwarp();
       if (lane == 0) bulk_wait_group0();  // TMA stores are complete for their own thread only
@@ -1037,7 +1079,7 @@ struct Buffers {
   float *partial, *diag;
   unsigned int* done;
   __half *hi[2], *A, *B;
-  uint8_t *x, *a;
+  uint8_t *lo, *a;
   size_t bytes;
 };
 
@@ -1055,7 +1097,7 @@ Buffers carve(void* base, int count, int mp, int np) {
   w.diag = reinterpret_cast<float*>(take(static_cast<size_t>(count) * mp * 4));
   for (int i = 0; i < 2; ++i) w.hi[i] = reinterpret_cast<__half*>(take(2 * x));
   const size_t nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile, boxes = 2 * kEpiWarps * 2;
-  w.x = reinterpret_cast<uint8_t*>(take(count * nt * ntn * boxes * kBoxX));
+  w.lo = reinterpret_cast<uint8_t*>(take(count * nt * ntn * boxes * kBoxX));
   w.a = reinterpret_cast<uint8_t*>(take(count * (nt * (nt + 1) / 2) * boxes * kBoxA));
   w.A = reinterpret_cast<__half*>(take(a));
   w.B = reinterpret_cast<__half*>(take(a));
@@ -1155,7 +1197,7 @@ cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, 
   if (e != cudaSuccess) return e;
   return launch_kernel(ns_load_kernel<GT, VEC>, dim3((mp / 64) * (np / 64), pr.count), dim3(256), 0, s, true,
                        pr.stacks, pr.momentum, pr.nesterov, pr.m, pr.n, mp, np, chunks, pr.eps,
-                       static_cast<const float*>(w.partial), w.hi[0], w.x);
+                       static_cast<const float*>(w.partial), w.hi[0], w.lo);
 }
 
 }  // namespace
@@ -1198,7 +1240,8 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   for (int k = 0; k < pr.steps; ++k)
     for (int j = 0; j < 3; ++j) a.coeff[k][j] = pr.coeff[k][j];
-  a.x = w.x, a.a = w.a;
+  for (int i = 0; i < 2; ++i) a.hi[i] = w.hi[i];
+  a.lo = w.lo, a.a = w.a;
   a.diag = w.diag;
   a.done = w.done;
   a.out = pr.out;
