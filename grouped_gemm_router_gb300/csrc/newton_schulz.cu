@@ -35,7 +35,7 @@
 // below as the transposed (M- or N-major) operand, which costs nothing.
 //
 // What only the epilogues read (lo, and a copy of A) is kept in the order in
-// which they hold it: for each warp and 32 x 32 box, 16-byte pieces of 32
+// which they hold it: for each warp and 32 x 32 box, 32-byte pieces of 32
 // lanes side by side.  So those accesses are whole lines and need no turning
 // in shared memory, whose bandwidth the products use.  The operands, hi among
 // them, come and go by TMA.
@@ -55,6 +55,8 @@
 //   warp 1      TMEM allocator; MMA issuer (one lane, leader only)
 //   warps 2-17  epilogue
 //   warp 18     counts the tiles whose results are in memory
+//   warp 19     finds the CTA's next tiles, waits for what they depend on and
+//               posts them for the others, a few ahead
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -76,7 +78,7 @@ constexpr int kOperandBytes = 2 * kAtomBytes;  // one operand's half of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 3;
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 96 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kBox = 32;                       // columns an epilogue warp takes from TMEM at a time
 constexpr int kWarpStage = kBox * kBox * 2;    // its box in shared memory, fp16 (or 16 rows in fp32)
 constexpr int kBoxX = 2 * 512;                 // its box of lo: 8 words a lane
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
     word[k] = pack_lo2(v[0], v[1], pack_half2(v[0], v[1])) | (pack_lo2(v[2], v[3], pack_half2(v[2], v[3])) << 16);
   }
   uint8_t* box = lo + x_box(mat, (mp + kTile - 1) / kTile, (np + kTile - 1) / kTile, ti * 64 + br, tj * 64 + bc) * kBoxX;
-  *reinterpret_cast<uint4*>(box + half * 512 + lane * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+  *reinterpret_cast<uint4*>(box + lane * 32 + half * 16) = make_uint4(word[0], word[1], word[2], word[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -309,7 +311,6 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
 // ---------------------------------------------------------------------------
 struct GemmArgs {
   int count;        // matrices
-  int group;        // matrices whose products follow one another
   int steps;
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
@@ -327,6 +328,14 @@ struct NsMaps {
   CUtensorMap boxX[2], boxA, boxB;  // the same arrays in 32 x 32 boxes
 };
 
+// A tile as it is posted: the product (-1: there are no more), matrix, place,
+// and its number in the arrays of private boxes.
+struct Tile {
+  int prod, mat, ti, tj;
+  unsigned int number;
+};
+constexpr int kPosted = 8;  // tiles posted at a time
+
 struct Ctl {
   uint64_t full[kStages];
   uint64_t empty[kStages];
@@ -336,16 +345,20 @@ struct Ctl {
   uint64_t box[kEpiWarps];
   uint32_t tmem_base;
   int abort;
-  int ready;                // tiles whose operands the producer has seen complete
+  int ready;                // tiles posted: what they read is complete
   int written[kEpiWarps];   // tiles whose stores an epilogue warp has issued
+  int counted;              // tiles that all warps are done with
+  Tile tile[kPosted];
 };
 
-// Walks the tiles of one pair in the common order: groups of matrices, in a
-// group product after product, in a product matrix after matrix.
+// Walks the tiles of one pair in the common order: product after product, in a
+// product matrix after matrix.  (Groups of matrices that fit the L2 cache one
+// after the other, or parts a product apart, were slower: 12 of 24 matrices of
+// 768 x 1536 at a time 620 us, in three parts 738, all at once 555.)
 struct Walk {
-  int first, g0, prod;     // number of the product's first tile, group, product
-  int mat, ti, tj;         // the tile
-  MOE_DEV Walk() : first(0), g0(0), prod(0) {}
+  int first, prod;     // number of the product's first tile, product
+  int mat, ti, tj;     // the tile
+  MOE_DEV Walk() : first(0), prod(0) {}
   // Tiles of one matrix in product `prod`.
   MOE_DEV static int tiles(const GemmArgs& p, int prod) {
     const int nt = (p.mp + kTile - 1) / kTile;
@@ -353,12 +366,11 @@ struct Walk {
   }
   // Moves to tile `idx`; false past the last one.  idx never decreases.
   MOE_DEV bool to(const GemmArgs& p, int idx) {
-    for (;;) {
-      if (g0 >= p.count) return false;
-      const int per = tiles(p, prod), here = min(p.group, p.count - g0) * per;
+    for (; prod < 3 * p.steps; ++prod) {
+      const int per = tiles(p, prod), here = p.count * per;
       if (idx < first + here) {
         int r = idx - first;
-        mat = g0 + r / per;
+        mat = r / per;
         r %= per;
         if (prod % 3 == kApply) {
           const int ntn = (p.np + kTile - 1) / kTile;
@@ -372,11 +384,8 @@ struct Walk {
         return true;
       }
       first += here;
-      if (++prod == 3 * p.steps) {
-        prod = 0;
-        g0 += p.group;
-      }
     }
+    return false;
   }
 };
 
@@ -425,6 +434,14 @@ MOE_DEV int wait_count(const int* c, int i, volatile int* abort, unsigned int* d
     if (v > i) return v;
     if (!keep_waiting(it, t0, abort, dev_err)) return -1;
   }
+}
+
+// Tile number i of this CTA, once it is posted; false past the last one (or
+// when the wait was given up).
+MOE_DEV bool next_tile(const Ctl& ctl, int i, Tile& t, volatile int* abort, unsigned int* dev_err) {
+  if (wait_count(&ctl.ready, i, abort, dev_err) < 0) return false;
+  t = ctl.tile[i % kPosted];
+  return t.prod >= 0;
 }
 
 MOE_DEV void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
@@ -578,14 +595,18 @@ MOE_DEV void take(const EpiTile& t, int b, uint32_t (&acc)[32]) {
   if (b == 1) release(t);
 }
 
-// A lane's 4 N words of a private box, 16 bytes from each run of 512, through L2.
-template <int N>
-MOE_DEV void load_own(const uint8_t* p, uint32_t (&w)[4 * N]) {
-#pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + c * 512));
-    w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
-  }
+// 32 bytes, a whole sector, as the last to write them left them in L2.  (With
+// 16-byte loads of a lane's own row each sector is fetched twice.)
+MOE_DEV void load_sector(const void* p, uint32_t* v) {
+  asm volatile("ld.relaxed.gpu.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p)
+               : "memory");
+}
+MOE_DEV void store_sector(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // The box as fp16 to its place in an operand: through the warp's buffer
@@ -619,10 +640,8 @@ MOE_DEV bool epilogue_gram(const NsMaps& maps, const EpiTile& t) {
     for (int j = 0; j < 16; ++j)
       h[j] = pack_half2(__uint_as_float(acc[2 * j]) * f, __uint_as_float(acc[2 * j + 1]) * f);
     store_box(&maps.boxA, t, b, h);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(t.own + b * kBoxA + c * 512) =
-          make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+    store_sector(t.own + b * kBoxA, h);
+    store_sector(t.own + b * kBoxA + 1024, h + 8);
   }
   return true;
 }
@@ -631,14 +650,18 @@ MOE_DEV bool epilogue_gram(const NsMaps& maps, const EpiTile& t) {
 MOE_DEV bool epilogue_poly(const NsMaps& maps, const GemmArgs& p, const EpiTile& t) {
   const uint32_t l = lane_id();
   uint32_t a[2][16];
-  load_own<4>(t.own, a[0]);
+  load_sector(t.own, a[0]);
+  load_sector(t.own + 1024, a[0] + 8);
   const float cb = p.coeff[t.step][1], cc = p.coeff[t.step][2];
   if (!wait_acc(t)) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     uint32_t acc[32], h[16];
     take(t, b, acc);
-    if (b == 0) load_own<4>(t.own + kBoxA, a[1]);
+    if (b == 0) {
+      load_sector(t.own + kBoxA, a[1]);
+      load_sector(t.own + kBoxA + 1024, a[1] + 8);
+    }
     const bool diagonal = t.late && t.row0 == t.col0 + b * kBox;
     float mine = 0.f;
 #pragma unroll
@@ -666,53 +689,56 @@ MOE_DEV float row_factor(const GemmArgs& p, const EpiTile& t) {
 
 // The lane's 32 columns of hi, straight from its row.
 MOE_DEV void load_row(const __half* p, uint32_t (&h)[16]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p) + c);
-    h[4 * c] = u.x, h[4 * c + 1] = u.y, h[4 * c + 2] = u.z, h[4 * c + 3] = u.w;
-  }
+  load_sector(p, h);
+  load_sector(p + 16, h + 8);
 }
 
 MOE_DEV const __half* row_of(const GemmArgs& p, const EpiTile& t) {
   return p.hi[t.cur] + (static_cast<size_t>(t.mat) * p.mp + t.row0 + lane_id()) * p.np + t.col0;
 }
 
-// X <- a X + B X.  hi of the first box comes by TMA into the buffer that the
-// box leaves from, hi of the second straight into registers (there is no
-// shared memory for a second buffer); both are in L2, as operands.
-MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, EpiTile& t) {
-  const uint32_t l = lane_id();
-  uint32_t hi[16], lo[2][8];
-  if (l == 0) {
+// hi of the first box comes by TMA into the warp's buffer, hi of the second
+// straight into registers (there is no shared memory for a second buffer);
+// both are in L2, as operands.
+MOE_DEV void ask_hi(const NsMaps& maps, const GemmArgs& p, const EpiTile& t, uint32_t (&second)[16]) {
+  if (lane_id() == 0) {
     mbar_arrive_expect_tx(t.bar, kWarpStage);
     tma_load_3d(t.buf, &maps.boxX[t.cur], t.bar, t.col0, t.row0, t.mat);
   }
-  load_own<2>(t.own, lo[0]);
-  load_own<2>(t.own + kBoxX, lo[1]);
-  load_row(row_of(p, t) + kBox, hi);
-  const float f = row_factor(p, t);
+  load_row(row_of(p, t) + kBox, second);
+}
+
+// The accumulator and the first box; false when the wait was given up (the
+// copy has landed then too).
+MOE_DEV bool wait_acc_hi(EpiTile& t, uint32_t (&first)[16]) {
+  const uint32_t l = lane_id();
   const bool ok = wait_acc(t);
-  // also when given up: the copy lands before the CTA exits
   volatile int local_abort = 0;
   mbar_wait(t.bar, t.bar_phase, &local_abort, t.dev_err);
   t.bar_phase ^= 1u;
-  if (!ok) return false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(first[4 * c]), "=r"(first[4 * c + 1]), "=r"(first[4 * c + 2]), "=r"(first[4 * c + 3])
+                 : "r"(t.buf + l * 64 + ((c ^ ((l >> 1) & 3)) << 4))
+                 : "memory");
+  return ok;
+}
+
+// X <- a X + B X.
+MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, EpiTile& t) {
+  uint32_t hi[2][16], lo[2][8];
+  ask_hi(maps, p, t, hi[1]);
+  load_sector(t.own, lo[0]);
+  load_sector(t.own + kBoxX, lo[1]);
+  const float f = row_factor(p, t);
+  if (!wait_acc_hi(t, hi[0])) return false;
   const bool keep_lo = t.step + 2 < p.steps;  // the last step's X has none
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    uint32_t acc[32], h[16];
+    uint32_t acc[32];
     take(t, b, acc);
-    if (b == 0) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(h[4 * c]), "=r"(h[4 * c + 1]), "=r"(h[4 * c + 2]), "=r"(h[4 * c + 3])
-                     : "r"(t.buf + l * 64 + ((c ^ ((l >> 1) & 3)) << 4))
-                     : "memory");
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) h[j] = hi[j];
-    }
+    uint32_t(&h)[16] = hi[b];
     uint32_t n[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -725,12 +751,7 @@ MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, EpiTile& t) {
       n[k] = pack_lo2(x[0], x[1], h[2 * k]) | (pack_lo2(x[2], x[3], h[2 * k + 1]) << 16);
     }
     store_box(&maps.boxX[t.cur ^ 1], t, b, h);
-    if (keep_lo) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<uint4*>(t.own + b * kBoxX + c * 512) =
-            make_uint4(n[4 * c], n[4 * c + 1], n[4 * c + 2], n[4 * c + 3]);
-    }
+    if (keep_lo) store_sector(t.own + b * kBoxX, n);
   }
   return true;
 }
@@ -767,16 +788,16 @@ MOE_DEV void store_bf16(void* base, size_t el, int stop, bool vec, const float* 
 
 // The last product: o is the result, or moves the weights, in runs of 8
 // elements of the stack's own rows.
-MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile& t) {
+MOE_DEV bool epilogue_last(const NsMaps& maps, const GemmArgs& p, const NsStacks& st, EpiTile& t) {
   const uint32_t l = lane_id();
   uint32_t hi[2][16];
-  load_row(row_of(p, t), hi[0]);
+  ask_hi(maps, p, t, hi[1]);
   const float f = row_factor(p, t);
   const NsStack& s = st.s[stack_of(st, t.mat)];
   const size_t base = static_cast<size_t>(t.mat - s.first) * p.m * p.n;
   const int rows = s.tall ? p.n : p.m, cols = s.tall ? p.m : p.n;  // the stack's own
   const bool vec = cols % 8 == 0;                                  // runs start on 16 bytes and end inside
-  if (!wait_acc(t)) return false;
+  if (!wait_acc_hi(t, hi[0])) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     uint32_t acc[32];
@@ -787,7 +808,6 @@ MOE_DEV bool epilogue_last(const GemmArgs& p, const NsStacks& st, const EpiTile&
       acc[2 * j] = __float_as_uint(fmaf(f, x.x, __uint_as_float(acc[2 * j])));
       acc[2 * j + 1] = __float_as_uint(fmaf(f, x.y, __uint_as_float(acc[2 * j + 1])));
     }
-    if (b == 0) load_row(row_of(p, t) + kBox, hi[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // the lane's two runs in the stack's own matrix
@@ -863,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
     ctl.ready = 0;
+    ctl.counted = 0;
     for (int w = 0; w < kEpiWarps; ++w) {
       ctl.written[w] = 0;
       mbar_init(smem_u32(&ctl.box[w]), 1);
@@ -883,17 +904,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== TMA producer (both CTAs) =====================
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_normal();
-      int stage = 0, issued = 0, i = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Walk t;
-      for (int idx = pair; ok && t.to(p, idx); idx += npairs) {
+      Tile t;
+      for (int i = 0; ok && next_tile(ctl, i, t, abort_flag, dev_err); ++i) {
         const int kind = t.prod % 3, cur = (t.prod / 3) & 1;
-        if (!wait_product(p, t.prod, t.mat, abort_flag, dev_err)) {
-          ok = false;
-          break;
-        }
-        count_store(&ctl.ready, ++i);
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         const CUtensorMap* mp = kind == kGram ? &maps.X[cur] : kind == kPoly ? &maps.A : &maps.B;
         const CUtensorMap* mq = kind == kPoly ? &maps.A : &maps.X[cur];
         const int nkb = ((kind == kGram ? p.np : p.mp) + kBK - 1) / kBK;
@@ -922,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok && leader) {
+      if (*abort_flag && leader) {
         // Let the copies already in flight land before the CTA exits.
         for (int k = 0; k < kStages && k < issued; ++k) {
           if (--stage < 0) {
@@ -938,11 +955,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ===================== MMA issuer (leader only) =====================
     if (lane == 0 && leader) {
-      int stage = 0, i = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Walk t;
-      for (int idx = pair; ok && t.to(p, idx); idx += npairs, ++i) {
+      Tile t;
+      for (int i = 0; ok && next_tile(ctl, i, t, abort_flag, dev_err); ++i) {
         const int buf = i & 1;
         if (!mbar_wait_cluster(smem_u32(&ctl.tempty[buf]), ((i >> 1) & 1) ^ 1u, abort_flag, dev_err)) break;
         tc_fence_after_sync();
@@ -989,9 +1006,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Once the epilogue warps have issued a tile's stores, waits until these
     // are in memory and counts the tile: 2000 to 5000 cycles that the
     // epilogue warps spend on the next tile.
-    int i = 0, upto = 0;
-    Walk t;
-    for (int idx = pair; t.to(p, idx); idx += npairs, ++i) {
+    int upto = 0;
+    Tile t;
+    for (int i = 0; next_tile(ctl, i, t, abort_flag, dev_err); ++i) {
       if (i >= upto) {  // all that every warp has issued by now, with one fence
         int v = lane < kEpiWarps ? wait_count(&ctl.written[lane], i, abort_flag, dev_err) : 0x7fffffff;
 #pragma unroll
@@ -1003,10 +1020,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
         }
       }
-      if (lane == 0 && t.prod + 1 < 3 * p.steps)
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + static_cast<size_t>(t.mat) * 3 * p.steps + t.prod)
-                     : "memory");
+      if (lane == 0) {
+        if (t.prod + 1 < 3 * p.steps)
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + static_cast<size_t>(t.mat) * 3 * p.steps + t.prod)
+                       : "memory");
+        count_store(&ctl.counted, i + 1);
+      }
+      __syncwarp();
     }
+  } else if (warp == 3 + kEpiWarps) {
+    // ===================== next tiles (both CTAs) =====================
+    // The CTA's tiles in order, each posted when the product that it reads is
+    // complete, at most kPosted ahead of the last one that is done with.  The
+    // others would each spend 500 to 1500 cycles a tile on finding it and on
+    // the round trip to the counter, the producer in the middle of its loads.
+    if (lane == 0) {
+      Walk w;
+      int i = 0;
+      bool ok = true;
+      for (int idx = pair; ok && w.to(p, idx); idx += npairs, ++i) {
+        ok = wait_count(&ctl.counted, i - kPosted, abort_flag, dev_err) >= 0 &&
+             wait_product(p, w.prod, w.mat, abort_flag, dev_err);
+        if (!ok) break;
+        const int nt = (p.mp + kTile - 1) / kTile, ntn = (p.np + kTile - 1) / kTile;
+        const unsigned int number = w.prod % 3 == kApply ? (static_cast<unsigned int>(w.mat) * nt + w.ti) * ntn + w.tj
+                                                         : static_cast<unsigned int>(w.mat) * (nt * (nt + 1) / 2) +
+                                                               w.ti * (w.ti + 1) / 2 + w.tj;
+        ctl.tile[i % kPosted] = Tile{w.prod, w.mat, w.ti, w.tj, number};
+        count_store(&ctl.ready, i + 1);
+      }
+      if (ok && wait_count(&ctl.counted, i - kPosted, abort_flag, dev_err) >= 0) {
+        ctl.tile[i % kPosted].prod = -1;
+        count_store(&ctl.ready, i + 1);
+      }
+    }
+    __syncwarp();
   } else {
     // ===================== epilogue (both CTAs) =====================
     // Warp w: TMEM lanes 32 (w % 4) .. + 31 and columns 64 ((w - 2) / 4) ..
@@ -1015,10 +1063,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = map_to_cta(smem_u32(&ctl.tempty[0]), 0);
     const uint32_t tempty1 = map_to_cta(smem_u32(&ctl.tempty[1]), 0);
     const uint32_t box = smem_base + kStages * kStageBytes + (warp - 2) * kWarpStage;
-    int i = 0;
     uint32_t bar_phase = 0;
-    Walk t;
-    for (int idx = pair; t.to(p, idx); idx += npairs, ++i) {
+    Tile t;
+    for (int i = 0;; ++i) {
+      bool got = next_tile(ctl, i, t, abort_flag, dev_err);
+      if (!__all_sync(0xffffffffu, got)) break;
       const int kind = t.prod % 3, step = t.prod / 3, buf = i & 1;
       EpiTile e;
       e.mat = t.mat, e.step = step, e.cur = step & 1;
@@ -1026,11 +1075,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       e.row0 = t.ti * kTile + 128 * static_cast<int>(rank) + q * 32;
       e.col0 = t.tj * kTile + part * 2 * kBox;
       const int ncols = kind == kApply ? p.np : p.mp;
-      const int nt = (p.mp + kTile - 1) / kTile, ntn = (p.np + kTile - 1) / kTile;
-      const size_t tile = kind == kApply ? (static_cast<size_t>(t.mat) * nt + t.ti) * ntn + t.tj
-                                         : static_cast<size_t>(t.mat) * (nt * (nt + 1) / 2) + t.ti * (t.ti + 1) / 2 + t.tj;
-      e.own = (kind == kApply ? p.lo : p.a) + lane * 16 +
-              ((tile * 2 + rank) * kEpiWarps + part * 4 + q) * 2 * (kind == kApply ? kBoxX : kBoxA);
+      e.own = (kind == kApply ? p.lo : p.a) + lane * 32 +
+              ((static_cast<size_t>(t.number) * 2 + rank) * kEpiWarps + part * 4 + q) * 2 * (kind == kApply ? kBoxX : kBoxA);
       e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 2 * kBox;
       e.tfull = smem_u32(&ctl.tfull[buf]);
       e.tphase = (i >> 1) & 1;
@@ -1039,9 +1085,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       e.bar = smem_u32(&ctl.box[warp - 2]), e.bar_phase = bar_phase;
       e.abort_flag = abort_flag;
       e.dev_err = dev_err;
-      bool got = true;
-      if (lane == 0) got = wait_count(&ctl.ready, i, abort_flag, dev_err) > 0;
-      if (!__all_sync(0xffffffffu, got)) break;
       // padded sizes are multiples of 64: the warp's part is inside or outside
       if (e.row0 >= p.mp || e.col0 >= ncols)
         got = epilogue_none(e);
@@ -1052,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (step + 1 < p.steps)
         got = epilogue_apply(maps, p, e);
       else
-        got = epilogue_last(p, st, e);
+        got = epilogue_last(maps, p, st, e);
       bar_phase = e.bar_phase;
       if (!got) break;
       __syncwarp();
@@ -1186,6 +1229,9 @@ cudaError_t box_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Norms, then X_0.  (In batches of what the L2 cache holds of g and m, so that
+// the second pass finds them there: 584 us for a step of 24 matrices of 768 x
+// 1536 instead of 578.)
 template <typename GT, int VEC>
 cudaError_t launch_first(const NsProblem& pr, const Buffers& w, int mp, int np, cudaStream_t s) {
   const size_t elems = static_cast<size_t>(pr.m) * pr.n;
@@ -1235,7 +1281,6 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
 
   GemmArgs a{};
   a.count = count;
-  a.group = count;
   a.steps = pr.steps;
   a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   for (int k = 0; k < pr.steps; ++k)
