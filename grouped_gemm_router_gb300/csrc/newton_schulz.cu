@@ -978,13 +978,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool n_major = kind == kApply || (kind == kPoly && above(kb, t.tj));
           const uint32_t idesc = idesc_f16_f32(kTile, kTile, m_major, n_major);
           const int slices = K - kb * kBK >= kBK ? kBK / 16 : 4;  // K is a multiple of 64
-          for (int kk = 0; kk < slices; ++kk) {
-            const uint32_t off = (kk >> 2) * kAtomBytes + (kk & 3) * 32;
-            const uint64_t pd = m_major ? smem_desc_sw128(sp + kk * 2048, kAtomBytes, 1024)
-                                        : smem_desc_sw128(sp + off, 16, 1024);
-            const uint64_t qd = n_major ? smem_desc_sw128(sq + kk * 2048, kAtomBytes, 1024)
-                                        : smem_desc_sw128(sq + off, 16, 1024);
-            umma_bf16_pair(d, pd, qd, idesc, (kb | kk) != 0 ? 1u : 0u);
+          // 16-byte steps from one 16-deep slice to the next: K-major 32 bytes
+          // in an atom, then the next atom; else 16 k rows
+          const uint64_t pd = smem_desc_sw128(sp, m_major ? kAtomBytes : 16, 1024);
+          const uint64_t qd = smem_desc_sw128(sq, n_major ? kAtomBytes : 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            if (kk >= slices) break;
+            const uint32_t k_step = (kk >> 2) * (kAtomBytes / 16) + (kk & 3) * 2, mn_step = kk * (2048 / 16);
+            umma_bf16_pair(d, pd + (m_major ? mn_step : k_step), qd + (n_major ? mn_step : k_step), idesc,
+                           (kb | kk) != 0 ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&ctl.empty[stage]), 0x3);
           if (++stage == kStages) {
