@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
 // ---------------------------------------------------------------------------
 struct GemmArgs {
   int count;        // matrices
+  int group;        // of them, that are worked on at a time
   int steps;
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
@@ -351,14 +352,12 @@ struct Ctl {
   Tile tile[kPosted];
 };
 
-// Walks the tiles of one pair in the common order: product after product, in a
-// product matrix after matrix.  (Groups of matrices that fit the L2 cache one
-// after the other, or parts a product apart, were slower: 12 of 24 matrices of
-// 768 x 1536 at a time 620 us, in three parts 738, all at once 555.)
+// Walks the tiles of one pair in the common order: group of matrices after
+// group, in a group product after product, in a product matrix after matrix.
 struct Walk {
-  int first, prod;     // number of the product's first tile, product
-  int mat, ti, tj;     // the tile
-  MOE_DEV Walk() : first(0), prod(0) {}
+  int first, g0, prod;     // number of the product's first tile, group, product
+  int mat, ti, tj;         // the tile
+  MOE_DEV Walk() : first(0), g0(0), prod(0) {}
   // Tiles of one matrix in product `prod`.
   MOE_DEV static int tiles(const GemmArgs& p, int prod) {
     const int nt = (p.mp + kTile - 1) / kTile;
@@ -366,25 +365,26 @@ struct Walk {
   }
   // Moves to tile `idx`; false past the last one.  idx never decreases.
   MOE_DEV bool to(const GemmArgs& p, int idx) {
-    for (; prod < 3 * p.steps; ++prod) {
-      const int per = tiles(p, prod), here = p.count * per;
-      if (idx < first + here) {
-        int r = idx - first;
-        mat = r / per;
-        r %= per;
-        if (prod % 3 == kApply) {
-          const int ntn = (p.np + kTile - 1) / kTile;
-          ti = r / ntn;
-          tj = r - ti * ntn;
-        } else {
-          ti = 0;
-          while (r > ti) r -= ++ti;
-          tj = r;
+    for (; g0 < p.count; g0 += p.group, prod = 0)
+      for (; prod < 3 * p.steps; ++prod) {
+        const int per = tiles(p, prod), here = min(p.group, p.count - g0) * per;
+        if (idx < first + here) {
+          int r = idx - first;
+          mat = g0 + r / per;
+          r %= per;
+          if (prod % 3 == kApply) {
+            const int ntn = (p.np + kTile - 1) / kTile;
+            ti = r / ntn;
+            tj = r - ti * ntn;
+          } else {
+            ti = 0;
+            while (r > ti) r -= ++ti;
+            tj = r;
+          }
+          return true;
         }
-        return true;
+        first += here;
       }
-      first += here;
-    }
     return false;
   }
 };
@@ -1282,8 +1282,17 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   if ((e = operand_map(enc, &maps.A, w.A, count, mp, mp)) != cudaSuccess) return e;
   if ((e = operand_map(enc, &maps.B, w.B, count, mp, mp)) != cudaSuccess) return e;
 
+  const long nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile;
   GemmArgs a{};
   a.count = count;
+  // Groups whose smallest product has two tiles for each pair, so that the way
+  // from one product to the next is covered, and no more, so that X may still
+  // be in L2 for its second reading: 12 matrices of 2048 x 8192 four at a time
+  // 5.36 ms, all at once 5.68, two at a time 5.66.  For 192 of 768 x 1536 any
+  // size from 24 on is the same.
+  const int tri = static_cast<int>(nt * (nt + 1) / 2);
+  const int groups = std::max(1, count / std::max(1, 2 * pairs / tri));
+  a.group = (count + groups - 1) / groups;
   a.steps = pr.steps;
   a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   for (int k = 0; k < pr.steps; ++k)
@@ -1294,7 +1303,6 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   a.done = w.done;
   a.out = pr.out;
   // more pairs than the widest product has tiles would find nothing to do
-  const long nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile;
   const long most = count * std::max(nt * ntn, nt * (nt + 1) / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long>(pairs, most)));
