@@ -213,12 +213,9 @@ MOE_DEV void unpack_hi_lo4(uint32_t h01, uint32_t h23, uint32_t lo, float (&x)[4
   x[2] = half_minus(h23, l23.x), x[3] = half_minus(h23 >> 16, l23.y);
 }
 
-// Boxes of one matrix's lo come tile by tile, in a tile CTA by
-// CTA, warp by warp (column part, lane quarter), two boxes each: the number of
-// the box that holds row i, column j.
-MOE_DEV size_t x_box(int mat, int nt, int ntn, int i, int j) {
-  const size_t tile = (static_cast<size_t>(mat) * nt + (i >> 8)) * ntn + (j >> 8);
-  return ((tile * 2 + ((i >> 7) & 1)) * kEpiWarps + ((j >> 6) & 3) * 4 + ((i >> 5) & 3)) * 2 + ((j >> 5) & 1);
+// The number of the 32 x 32 box at (i, j) of matrix mat; rows and cols padded.
+MOE_DEV size_t box_number(int mat, int rows, int cols, int i, int j) {
+  return (static_cast<size_t>(mat) * (rows / kBox) + i / kBox) * (cols / kBox) + j / kBox;
 }
 
 // X_0 in 64 x 64 tiles (zeros past the matrix), transposed for a tall one.
@@ -302,7 +299,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Ns
     const float* v = &tile[br + lane][bc + 16 * half + 4 * k];
     word[k] = pack_lo2(v[0], v[1], pack_half2(v[0], v[1])) | (pack_lo2(v[2], v[3], pack_half2(v[2], v[3])) << 16);
   }
-  uint8_t* box = lo + x_box(mat, (mp + kTile - 1) / kTile, (np + kTile - 1) / kTile, ti * 64 + br, tj * 64 + bc) * kBoxX;
+  uint8_t* box = lo + box_number(mat, mp, np, ti * 64 + br, tj * 64 + bc) * kBoxX;
   *reinterpret_cast<uint4*>(box + lane * 32 + half * 16) = make_uint4(word[0], word[1], word[2], word[3]);
 }
 
@@ -315,12 +312,14 @@ struct GemmArgs {
   int steps;
   int mp, np;       // padded sizes (multiples of 64)
   int m, n;         // sizes
+  int tn;           // columns of a tile: 256, or 128
+  int direct;       // each epilogue warp counts its part of a tile itself
   float coeff[MOE_MAX_NS_STEPS][3];
   const __half* hi[2];  // X, [count, mp, np], in turns
-  uint8_t* lo;      // what hi leaves of X, in boxes (x_box)
+  uint8_t* lo;      // what hi leaves of X, in boxes
   uint8_t* a;       // the epilogues' copy of A, in boxes
   float* diag;      // [count, mp]: B's diagonal where it is kept apart
-  unsigned int* done;  // [count, 3 * steps] halves of tiles that are complete
+  unsigned int* done;  // [count, 3 * steps] CTAs' (or warps') parts of tiles that are complete
   NsOutput out;
 };
 
@@ -329,11 +328,9 @@ struct NsMaps {
   CUtensorMap boxX[2], boxA, boxB;  // the same arrays in 32 x 32 boxes
 };
 
-// A tile as it is posted: the product (-1: there are no more), matrix, place,
-// and its number in the arrays of private boxes.
+// A tile as it is posted: the product (-1: there are no more), matrix, place.
 struct Tile {
   int prod, mat, ti, tj;
-  unsigned int number;
 };
 constexpr int kPosted = 8;  // tiles posted at a time
 
@@ -358,10 +355,17 @@ struct Walk {
   int first, g0, prod;     // number of the product's first tile, group, product
   int mat, ti, tj;         // the tile
   MOE_DEV Walk() : first(0), g0(0), prod(0) {}
+  // Tiles in row ti of a matrix in product `prod`: a symmetric one's up to the
+  // 256 columns that hold the diagonal.
+  __host__ MOE_DEV static int row_tiles(const GemmArgs& p, int prod, int ti) {
+    const int all = ((prod % 3 == kApply ? p.np : p.mp) + p.tn - 1) / p.tn;
+    return prod % 3 == kApply ? all : min(all, (ti + 1) * (kTile / p.tn));
+  }
   // Tiles of one matrix in product `prod`.
-  MOE_DEV static int tiles(const GemmArgs& p, int prod) {
+  __host__ MOE_DEV static int tiles(const GemmArgs& p, int prod) {
     const int nt = (p.mp + kTile - 1) / kTile;
-    return prod % 3 == kApply ? nt * ((p.np + kTile - 1) / kTile) : nt * (nt + 1) / 2;
+    if (prod % 3 == kApply) return nt * row_tiles(p, prod, 0);
+    return nt * (nt - 1) / 2 * (kTile / p.tn) + row_tiles(p, prod, nt - 1);  // all rows but the last are whole
   }
   // Moves to tile `idx`; false past the last one.  idx never decreases.
   MOE_DEV bool to(const GemmArgs& p, int idx) {
@@ -372,15 +376,8 @@ struct Walk {
           int r = idx - first;
           mat = g0 + r / per;
           r %= per;
-          if (prod % 3 == kApply) {
-            const int ntn = (p.np + kTile - 1) / kTile;
-            ti = r / ntn;
-            tj = r - ti * ntn;
-          } else {
-            ti = 0;
-            while (r > ti) r -= ++ti;
-            tj = r;
-          }
+          for (ti = 0; r >= row_tiles(p, prod, ti); ++ti) r -= row_tiles(p, prod, ti);
+          tj = r;
           return true;
         }
         first += here;
@@ -407,7 +404,7 @@ MOE_DEV bool keep_waiting(uint32_t it, uint64_t& t0, volatile int* abort, unsign
 MOE_DEV bool wait_product(const GemmArgs& p, int prod, int mat, volatile int* abort, unsigned int* dev_err) {
   if (prod == 0) return true;  // X_0 comes from an earlier kernel
   const unsigned int* c = p.done + static_cast<size_t>(mat) * 3 * p.steps + prod - 1;
-  const unsigned int target = Walk::tiles(p, prod - 1) * 2;
+  const unsigned int target = Walk::tiles(p, prod - 1) * 2 * (p.direct ? kEpiWarps : 1);
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
     unsigned int v;
@@ -417,6 +414,13 @@ MOE_DEV bool wait_product(const GemmArgs& p, int prod, int mat, volatile int* ab
   }
   asm volatile("fence.proxy.async.global;" ::: "memory");
   return true;
+}
+
+// Counts a part of tile t as complete, after all that this thread has seen
+// written.
+MOE_DEV void count_done(const GemmArgs& p, const Tile& t) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + static_cast<size_t>(t.mat) * 3 * p.steps + t.prod)
+               : "memory");
 }
 
 // Counters in shared memory, written by one thread each.
@@ -548,6 +552,7 @@ struct EpiTile {
   int mat, step, cur;
   bool late;            // B's diagonal is kept apart
   int row0, col0;       // the warp's first row and column
+  int boxes;            // of 32 columns: 2, or 1 in a narrow tile
   uint8_t* own;         // the lane's piece of the first box of lo, or of A's copy
   uint32_t taddr;       // its accumulator
   uint32_t tfull, tphase, tempty;
@@ -574,12 +579,15 @@ MOE_DEV void release(const EpiTile& t) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(t.tempty) : "memory");
 }
 
-// The four epilogues, on two boxes of 32 columns, a lane a row.  Each asks for
+// The four epilogues, on two boxes of 32 columns (or one), a lane a row.  Each asks for
 // what it reads (A, or X) of the first box before it waits for the accumulator
 // and of the second before it works on the first.  Little may spill here:
 // shared memory leaves the L1 cache 28 KB, so spilled registers come back from
 // L2.  For the same reason every load into registers is made without a
 // condition: registers written under one stay live around the loop over tiles.
+
+// The second box, for loads that are made whether or not there is one.
+MOE_DEV int second(const EpiTile& t) { return t.boxes - 1; }
 
 // A tile whose part for this warp lies outside the matrix.
 MOE_DEV bool epilogue_none(const EpiTile& t) {
@@ -592,7 +600,7 @@ MOE_DEV bool epilogue_none(const EpiTile& t) {
 MOE_DEV void take(const EpiTile& t, int b, uint32_t (&acc)[32]) {
   tmem_ld_32cols(t.taddr + b * kBox, acc);
   tmem_ld_wait();
-  if (b == 1) release(t);
+  if (b + 1 == t.boxes) release(t);
 }
 
 // 32 bytes, a whole sector, as the last to write them left them in L2.  (With
@@ -633,6 +641,7 @@ MOE_DEV bool epilogue_gram(const NsMaps& maps, const EpiTile& t) {
   if (!wait_acc(t)) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
+    if (b >= t.boxes) break;
     uint32_t acc[32], h[16];
     take(t, b, acc);
     constexpr float f = 1.f / (kScaleX * kScaleX);
@@ -656,11 +665,12 @@ MOE_DEV bool epilogue_poly(const NsMaps& maps, const GemmArgs& p, const EpiTile&
   if (!wait_acc(t)) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
+    if (b >= t.boxes) break;
     uint32_t acc[32], h[16];
     take(t, b, acc);
     if (b == 0) {
-      load_sector(t.own + kBoxA, a[1]);
-      load_sector(t.own + kBoxA + 1024, a[1] + 8);
+      load_sector(t.own + second(t) * kBoxA, a[1]);
+      load_sector(t.own + second(t) * kBoxA + 1024, a[1] + 8);
     }
     const bool diagonal = t.late && t.row0 == t.col0 + b * kBox;
     float mine = 0.f;
@@ -700,12 +710,12 @@ MOE_DEV const __half* row_of(const GemmArgs& p, const EpiTile& t) {
 // hi of the first box comes by TMA into the warp's buffer, hi of the second
 // straight into registers (there is no shared memory for a second buffer);
 // both are in L2, as operands.
-MOE_DEV void ask_hi(const NsMaps& maps, const GemmArgs& p, const EpiTile& t, uint32_t (&second)[16]) {
+MOE_DEV void ask_hi(const NsMaps& maps, const GemmArgs& p, const EpiTile& t, uint32_t (&other)[16]) {
   if (lane_id() == 0) {
     mbar_arrive_expect_tx(t.bar, kWarpStage);
     tma_load_3d(t.buf, &maps.boxX[t.cur], t.bar, t.col0, t.row0, t.mat);
   }
-  load_row(row_of(p, t) + kBox, second);
+  load_row(row_of(p, t) + second(t) * kBox, other);
 }
 
 // The accumulator and the first box; false when the wait was given up (the
@@ -730,12 +740,13 @@ MOE_DEV bool epilogue_apply(const NsMaps& maps, const GemmArgs& p, EpiTile& t) {
   uint32_t hi[2][16], lo[2][8];
   ask_hi(maps, p, t, hi[1]);
   load_sector(t.own, lo[0]);
-  load_sector(t.own + kBoxX, lo[1]);
+  load_sector(t.own + second(t) * kBoxX, lo[1]);
   const float f = row_factor(p, t);
   if (!wait_acc_hi(t, hi[0])) return false;
   const bool keep_lo = t.step + 2 < p.steps;  // the last step's X has none
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
+    if (b >= t.boxes) break;
     uint32_t acc[32];
     take(t, b, acc);
     uint32_t(&h)[16] = hi[b];
@@ -800,6 +811,7 @@ MOE_DEV bool epilogue_last(const NsMaps& maps, const GemmArgs& p, const NsStacks
   if (!wait_acc_hi(t, hi[0])) return false;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
+    if (b >= t.boxes) break;
     uint32_t acc[32];
     take(t, b, acc);
 #pragma unroll
@@ -928,10 +940,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d_pair(sp, mp, bar, 0, kb * kBK, t.ti * (kTile / 64) + 2 * rank, t.mat, policy);
           else
             tma_load_4d_pair(sp, mp, bar, 0, t.ti * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
-          if (kind == kApply || (kind == kPoly && above(kb, t.tj)))
-            tma_load_4d_pair(sq, mq, bar, 0, kb * kBK, t.tj * (kTile / 64) + 2 * rank, t.mat, policy);
+          if (kind == kApply || (kind == kPoly && above(kb, t.tj * p.tn / kTile)))
+            tma_load_4d_pair(sq, mq, bar, 0, kb * kBK, (t.tj * p.tn + p.tn / 2 * rank) / 64, t.mat, policy);
           else
-            tma_load_4d_pair(sq, mq, bar, 0, t.tj * kTile + 128 * rank, kb * (kBK / 64), t.mat, policy);
+            tma_load_4d_pair(sq, mq, bar, 0, t.tj * p.tn + p.tn / 2 * rank, kb * (kBK / 64), t.mat, policy);
           ++issued;
           if (++stage == kStages) {
             stage = 0;
@@ -975,8 +987,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           const uint32_t sp = smem_base + stage * kStageBytes, sq = sp + kOperandBytes;
           const bool m_major = kind != kGram && above(kb, t.ti);
-          const bool n_major = kind == kApply || (kind == kPoly && above(kb, t.tj));
-          const uint32_t idesc = idesc_f16_f32(kTile, kTile, m_major, n_major);
+          const bool n_major = kind == kApply || (kind == kPoly && above(kb, t.tj * p.tn / kTile));
+          const uint32_t idesc = idesc_f16_f32(kTile, p.tn, m_major, n_major);
           const int slices = K - kb * kBK >= kBK ? kBK / 16 : 4;  // K is a multiple of 64
           // 16-byte steps from one 16-deep slice to the next: K-major 32 bytes
           // in an atom, then the next atom; else 16 k rows
@@ -1008,7 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== completion (both CTAs) =====================
     // Once the epilogue warps have issued a tile's stores, waits until these
     // are in memory and counts the tile: 2000 to 5000 cycles that the
-    // epilogue warps spend on the next tile.
+    // epilogue warps spend on the next tile.  Where there is no next tile to
+    // speak of they count their own parts, which is sooner (3 x 1001 x 363:
+    // 177 -> 163 us; a step of 24 matrices of 768 x 1536: 490 -> 512 us).
     int upto = 0;
     Tile t;
     for (int i = 0; next_tile(ctl, i, t, abort_flag, dev_err); ++i) {
@@ -1018,15 +1032,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
         if (v < 0) break;
         upto = v;
-        if (lane == 0) {
+        if (lane == 0 && !p.direct) {
           asm volatile("fence.proxy.async.global;" ::: "memory");
           __threadfence();
         }
       }
       if (lane == 0) {
-        if (t.prod + 1 < 3 * p.steps)
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + static_cast<size_t>(t.mat) * 3 * p.steps + t.prod)
-                       : "memory");
+        if (!p.direct && t.prod + 1 < 3 * p.steps) count_done(p, t);
         count_store(&ctl.counted, i + 1);
       }
       __syncwarp();
@@ -1045,11 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_count(&ctl.counted, i - kPosted, abort_flag, dev_err) >= 0 &&
              wait_product(p, w.prod, w.mat, abort_flag, dev_err);
         if (!ok) break;
-        const int nt = (p.mp + kTile - 1) / kTile, ntn = (p.np + kTile - 1) / kTile;
-        const unsigned int number = w.prod % 3 == kApply ? (static_cast<unsigned int>(w.mat) * nt + w.ti) * ntn + w.tj
-                                                         : static_cast<unsigned int>(w.mat) * (nt * (nt + 1) / 2) +
-                                                               w.ti * (w.ti + 1) / 2 + w.tj;
-        ctl.tile[i % kPosted] = Tile{w.prod, w.mat, w.ti, w.tj, number};
+        ctl.tile[i % kPosted] = Tile{w.prod, w.mat, w.ti, w.tj};
         count_store(&ctl.ready, i + 1);
       }
       if (ok && wait_count(&ctl.counted, i - kPosted, abort_flag, dev_err) >= 0) {
@@ -1076,11 +1084,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       e.mat = t.mat, e.step = step, e.cur = step & 1;
       e.late = step + 2 >= p.steps;
       e.row0 = t.ti * kTile + 128 * static_cast<int>(rank) + q * 32;
-      e.col0 = t.tj * kTile + part * 2 * kBox;
+      e.col0 = t.tj * p.tn + part * (p.tn / 4);
+      e.boxes = p.tn / 128;
       const int ncols = kind == kApply ? p.np : p.mp;
       e.own = (kind == kApply ? p.lo : p.a) + lane * 32 +
-              ((static_cast<size_t>(t.number) * 2 + rank) * kEpiWarps + part * 4 + q) * 2 * (kind == kApply ? kBoxX : kBoxA);
-      e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * 2 * kBox;
+              box_number(t.mat, p.mp, ncols, e.row0, e.col0) * (kind == kApply ? kBoxX : kBoxA);
+      e.taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile + part * (p.tn / 4);
       e.tfull = smem_u32(&ctl.tfull[buf]);
       e.tphase = (i >> 1) & 1;
       e.tempty = buf ? tempty1 : tempty0;
@@ -1102,7 +1111,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_phase = e.bar_phase;
       if (!got) break;
       __syncwarp();
-      if (lane == 0) bulk_wait_group0();  // TMA stores are complete for their own thread only
+      if (lane == 0) {
+        bulk_wait_group0();  // TMA stores are complete for their own thread only
+        if (p.direct && t.prod + 1 < 3 * p.steps) {
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+          count_done(p, t);
+        }
+      }
       if (lane == 0) count_store(&ctl.written[warp - 2], i + 1);
     }
     __syncwarp();
@@ -1142,9 +1157,8 @@ Buffers carve(void* base, int count, int mp, int np) {
   w.done = reinterpret_cast<unsigned int*>(take(static_cast<size_t>(count) * 3 * MOE_MAX_NS_STEPS * 4));
   w.diag = reinterpret_cast<float*>(take(static_cast<size_t>(count) * mp * 4));
   for (int i = 0; i < 2; ++i) w.hi[i] = reinterpret_cast<__half*>(take(2 * x));
-  const size_t nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile, boxes = 2 * kEpiWarps * 2;
-  w.lo = reinterpret_cast<uint8_t*>(take(count * nt * ntn * boxes * kBoxX));
-  w.a = reinterpret_cast<uint8_t*>(take(count * (nt * (nt + 1) / 2) * boxes * kBoxA));
+  w.lo = reinterpret_cast<uint8_t*>(take(x));
+  w.a = reinterpret_cast<uint8_t*>(take(a));
   w.A = reinterpret_cast<__half*>(take(a));
   w.B = reinterpret_cast<__half*>(take(a));
   w.bytes = off;
@@ -1282,19 +1296,22 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   if ((e = operand_map(enc, &maps.A, w.A, count, mp, mp)) != cudaSuccess) return e;
   if ((e = operand_map(enc, &maps.B, w.B, count, mp, mp)) != cudaSuccess) return e;
 
-  const long nt = (mp + kTile - 1) / kTile, ntn = (np + kTile - 1) / kTile;
   GemmArgs a{};
+  a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
+  a.steps = pr.steps;
+  // Narrow tiles while one wave of them holds the widest product: what counts
+  // then is how long a tile takes (3 x 1001 x 363: 163 -> 133 us).
+  a.tn = 128;
+  if (static_cast<long>(count) * Walk::tiles(a, kApply) > pairs) a.tn = kTile;
+  a.direct = static_cast<long>(count) * Walk::tiles(a, kGram) <= pairs;
   a.count = count;
   // Groups whose smallest product has two tiles for each pair, so that the way
   // from one product to the next is covered, and no more, so that X may still
   // be in L2 for its second reading: 12 matrices of 2048 x 8192 four at a time
   // 5.36 ms, all at once 5.68, two at a time 5.66.  For 192 of 768 x 1536 any
   // size from 24 on is the same.
-  const int tri = static_cast<int>(nt * (nt + 1) / 2);
-  const int groups = std::max(1, count / std::max(1, 2 * pairs / tri));
+  const int groups = std::max(1, count / std::max(1, 2 * pairs / Walk::tiles(a, kGram)));
   a.group = (count + groups - 1) / groups;
-  a.steps = pr.steps;
-  a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   for (int k = 0; k < pr.steps; ++k)
     for (int j = 0; j < 3; ++j) a.coeff[k][j] = pr.coeff[k][j];
   for (int i = 0; i < 2; ++i) a.hi[i] = w.hi[i];
@@ -1303,7 +1320,7 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   a.done = w.done;
   a.out = pr.out;
   // more pairs than the widest product has tiles would find nothing to do
-  const long most = count * std::max(nt * ntn, nt * (nt + 1) / 2);
+  const long most = static_cast<long>(count) * std::max(Walk::tiles(a, kApply), Walk::tiles(a, kGram));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long>(pairs, most)));
   cfg.blockDim = dim3(kThreads);
