@@ -1,4 +1,5 @@
-"""GB300-native (sm_103a) forward pass of the mixture-of-experts SwiGLU FFN.
+"""GB300-native (sm_103a) mixture-of-experts SwiGLU FFN, forward and backward,
+with the layer norm and the Muon step that train it.
 
 The compute path is libmoeffn.so (hand-written CUDA kernels behind a C ABI,
 declared in include/moe_ffn.h); `grouped_gemm_router_gb300.moe` is its thin

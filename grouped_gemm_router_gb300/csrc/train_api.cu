@@ -1,6 +1,6 @@
 // C ABI of the operators around the layer in a training step: argument
 // validation of the layer norm and Newton-Schulz entry points.  The arithmetic
-// is in layer_norm.cu and newton_schulz.cu.
+// is in layer_norm.cu, newton_schulz.cu and newton_schulz_small.cu.
 #include <cmath>
 
 #include <algorithm>

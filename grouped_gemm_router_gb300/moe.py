@@ -1,4 +1,5 @@
-"""PyTorch-facing entry points of the MoE SwiGLU FFN forward pass.
+"""PyTorch-facing entry points of the MoE SwiGLU FFN forward and backward passes,
+and of layer norm, Newton-Schulz orthogonalisation and the Muon step beside them.
 
 These functions only allocate outputs with torch, check shapes/dtypes, and
 call the C ABI of libmoeffn.so on the current CUDA stream.  Tensor layouts:

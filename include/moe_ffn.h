@@ -1,6 +1,7 @@
 /*
  * moe_ffn.h -- C ABI of the GB300 (sm_103a) mixture-of-experts SwiGLU FFN
- * forward pass.
+ * forward and backward passes, and of the operators around the layer in a
+ * training step: layer norm, Newton-Schulz orthogonalisation, Muon step.
  *
  * The layer (per token t of x [T, D]):
  *   logits = x[t] . Wg (+ router_bias)                 router GEMM
@@ -314,7 +315,9 @@ size_t moe_newton_schulz_workspace_size(int32_t count, int32_t rows, int32_t col
  *   grad [count, rows, cols] of type grad_type; out [count, rows, cols] bf16;
  *   coefficients: steps x 3 floats in host memory, read before the call
  *   returns.  The products take fp16 operands and fp32 sums, the linear term
- *   keeps X to 22 bits.  The coefficients have to keep the singular values of
+ *   keeps X to about 14 bits (to fp32 where the short side is at most 128 and
+ *   the long one at most 2048; such matrices stay on chip and leave the
+ *   workspace untouched).  The coefficients have to keep the singular values of
  *   X below 5 (those in common use keep them below 1.3).  A matrix with an
  *   element that is no finite number, or with a sum of squares past fp32,
  *   becomes NaN; the others of the stack do not.
