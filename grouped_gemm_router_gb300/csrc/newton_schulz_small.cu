@@ -551,6 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+// Over the whole range this is faster than the tiled kernel, five steps from
+// fp32: 1 of 128 x 128 24 us (tiled 77), 2048 of 128 x 256 422 (1634), 16 of
+// 128 x 2048 100 (145), 256 of them 893 (990), 64 of 8 x 2048 216 (238).
 bool ns_small_fits(int m, int n) { return m <= kRowsMax && n <= kSlice * kMaxCluster; }
 
 cudaError_t launch_ns_small(const NsProblem& pr, cudaStream_t s) {
