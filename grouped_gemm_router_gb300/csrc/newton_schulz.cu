@@ -40,7 +40,8 @@
 // in shared memory, whose bandwidth the products use.  The operands, hi among
 // them, come and go by TMA.
 //
-// All products of all steps are one persistent launch over 256 x 256 tiles,
+// All products of all steps are one persistent launch over 256 x 256 tiles
+// (256 x 128 where there are few),
 // run by CTA pairs (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM,
 // operands by TMA with the 128-byte swizzle).  The tiles of all (product,
 // matrix) are numbered product by product and pair p takes tiles p, p +
@@ -1306,10 +1307,13 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   GemmArgs a{};
   a.mp = mp, a.np = np, a.m = pr.m, a.n = pr.n;
   a.steps = pr.steps;
-  // Narrow tiles while one wave of them holds the widest product: what counts
-  // then is how long a tile takes (3 x 1001 x 363: 163 -> 133 us).
+  // Narrow tiles while one wave of them holds the widest product, two with a
+  // short k: what counts then is how long a tile takes, and not that operands
+  // are loaded twice as often.  3 x 1001 x 363: 163 -> 133 us; 12 x 256 x 1024
+  // 132 -> 119, 3 x 512 x 2048 167 -> 151, 4 x 768 x 1536 (1.9 waves) 181 both
+  // ways; but 30 x 256 x 1024 (3.2) 153 -> 160, 1 x 2048 x 2048 (1.7) 248 -> 288.
   a.tn = 128;
-  if (static_cast<long>(count) * Walk::tiles(a, kApply) > pairs) a.tn = kTile;
+  if (static_cast<long>(count) * Walk::tiles(a, kApply) > (mp <= 3 * kTile ? 2 : 1) * pairs) a.tn = kTile;
   a.direct = static_cast<long>(count) * Walk::tiles(a, kGram) <= pairs;
   a.count = count;
   // Groups whose smallest product has two tiles for each pair, so that the way

@@ -206,3 +206,17 @@ def test_many_and_large_matrices(moe):
     assert moe.device_error() == 0
     assert torch.equal(o[0], o[-1]) and torch.equal(o[-1], moe.newton_schulz(one)[0])
     assert not o[1:-1].any()
+
+
+@pytest.mark.parametrize("kind", ["full", "few tokens"])
+@pytest.mark.parametrize("B,rows,cols", [(9, 129, 300), (16, 256, 1024), (38, 256, 512), (60, 250, 250), (70, 129, 131),
+                                         (5, 700, 513), (4, 768, 1536), (1, 1024, 1024)])
+def test_tile_widths(moe, B, rows, cols, kind):
+    """One to two waves of narrow tiles, with each way of counting them, and
+    the sizes just past them."""
+    g = _grad(B, rows, cols, kind, 29)
+    o = moe.newton_schulz(g)
+    torch.cuda.synchronize()
+    assert moe.device_error() == 0
+    for e in range(B):
+        _check(f64(o[e]), newton_schulz(f64(g[e]), [C] * 5, 1e-7), (kind, e))
