@@ -805,6 +805,27 @@ MOE_DEV void store_bf16(void* base, size_t el, int stop, bool vec, const float* 
   }
 }
 
+// Moves eight consecutive fp32 weights (stop of them inside the row) by o and
+// leaves them in o.  (One by one, a step of 24 matrices of 768 x 1536 takes 583
+// us instead of 529; 493 with bf16 weights, which are 113 MB less to move.)
+MOE_DEV void move_f32(float* d, int stop, bool vec, const NsOutput& out, float* o) {
+  if (vec) {
+    if (stop > 0) {
+      float4* q = reinterpret_cast<float4*>(d);
+      const float4 a = __ldcs(q), b = __ldcs(q + 1);
+      const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = fmaf(old[k], out.keep, -out.step * o[k]);
+      q[0] = make_float4(o[0], o[1], o[2], o[3]);
+      q[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < stop) d[k] = o[k] = fmaf(d[k], out.keep, -out.step * o[k]);
+  }
+}
+
 // The last product: o is the result, or moves the weights, in runs of 8
 // elements of the stack's own rows.
 MOE_DEV bool epilogue_last(const NsMaps& maps, const GemmArgs& p, const NsStacks& st, EpiTile& t) {
@@ -859,10 +880,7 @@ MOE_DEV bool epilogue_last(const NsMaps& maps, const GemmArgs& p, const NsStacks
         const int stop = r0 + rstep * i < rows ? min(8, cols - c0) : 0;
         float* o = v + 8 * i;
         if (p.out.kind == kNsWeightF32) {
-          float* d = static_cast<float*>(s.weight) + at;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < stop) d[k] = o[k] = fmaf(d[k], p.out.keep, -p.out.step * o[k]);
+          move_f32(static_cast<float*>(s.weight) + at, stop, vec, p.out, o);
           if (s.weight_bf16 != nullptr) store_bf16(s.weight_bf16, at, stop, vec, o);
         } else {
           if (p.out.kind == kNsWeightBf16) {
