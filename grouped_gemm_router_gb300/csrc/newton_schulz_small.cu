@@ -27,21 +27,17 @@
 
 #include "moe_device.cuh"
 #include "moe_kernels.cuh"
+#include "newton_schulz_parts.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kRowsMax = 128;
-constexpr int kSlice = 256;                      // most columns of a CTA
-constexpr int kMaxCluster = 8;
-constexpr int kThreads = 512;                    // 16 warps: 4 lane quarters x 4 column quarters
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlockBytes = kRowsMax * 64 * 2;   // 128 rows x 64 columns of fp16
 constexpr int kXBytes = kSlice / 64 * kBlockBytes;
 constexpr int kABytes = 2 * kBlockBytes;
 constexpr int kPartBytes = kRowsMax * 128 * 4;
-constexpr int kPitch = kSlice + 4;               // stash: 16-byte pieces of 8 rows meet no bank conflict
 constexpr int kStashBytes = kRowsMax * kPitch * 4;
 constexpr int kSmemBytes = kXBytes + (kStashBytes > kABytes + kPartBytes ? kStashBytes : kABytes + kPartBytes) + 1024;
 constexpr uint32_t kTmemX = 0, kTmemA = 256, kTmemP = 384;
@@ -173,44 +169,17 @@ MOE_DEV void store_run(uint16_t* p, const float (&v)[VEC]) {
     *p = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f));
 }
 
-// The CTA's part of a matrix in memory order, runs of VEC elements, batch(VEC)
-// a thread at a time.  Four-element runs are for matrices that lie in memory as
-// X does; in a tall one a run would be a column of the stash, and single
-// elements meet fewer bank conflicts (4 lanes a bank).  In the stash the run
-// at memory row r, place x starts at element r * sr + x * sx.
-__host__ __device__ constexpr int batch(int vec) { return vec == 4 ? 4 : 16; }
-struct Part {
-  int rows, len, shift;  // memory rows, elements of one, 2^shift runs cover it
-  int sr, sx;
-  int first, pitch;      // element of the matrix where the part starts, and between rows
-};
-template <int VEC>
-MOE_DEV Part part_of(bool tall, int m, int n, int c0, int width) {
-  Part q;
-  q.rows = tall ? width : m;
-  q.len = tall ? m : width;
-  q.shift = 0;
-  while ((VEC << q.shift) < q.len) ++q.shift;
-  q.sr = tall ? 1 : kPitch;
-  q.sx = tall ? kPitch : 1;
-  q.first = tall ? c0 * m : c0;
-  q.pitch = tall ? m : n;
-  return q;
-}
+// Visits the part's runs, batch(VEC) a thread at a time.
 template <int VEC, typename Load, typename Use>
 MOE_DEV void visit(const Part& q, Load load, Use use) {
   constexpr int kBatch = batch(VEC);
-  const int total = q.rows << q.shift, mask = (1 << q.shift) - 1;
+  const int total = run_count(q);
 #pragma unroll 1
   for (int s0 = threadIdx.x; s0 < total; s0 += kThreads * kBatch) {
-    // runs past the end (of a row, or of the part) repeat the part's first one
     int at[kBatch], spot[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int s = s0 + k * kThreads, r = s >> q.shift, x = (s & mask) * VEC;
-      const bool in = s < total && x < q.len;
-      at[k] = in ? q.first + r * q.pitch + x : q.first;
-      spot[k] = in ? r * q.sr + x * q.sx : -1;
+      place_run<VEC>(q, s0 + k * kThreads, at[k], spot[k]);
       load(k, at[k]);
     }
 #pragma unroll
@@ -314,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mat = blockIdx.x / ranks;
   const NsStack& s = st.s[stack_of(st, mat)];
   const size_t base = static_cast<size_t>(mat - s.first) * p.m * p.n;
-  const int c0 = rank * p.slice, width = max(0, min(p.slice, p.n - c0));
+  const int c0 = rank * p.slice, width = slice_width(p.n, p.slice, rank);
   volatile int* abort_flag = &ctl.abort;
 
   if (threadIdx.x == 0) {
@@ -560,11 +529,10 @@ cudaError_t launch_ns_small(const NsProblem& pr, cudaStream_t s) {
   unsigned int* err = nullptr;
   cudaError_t e = device_error_address(&err);
   if (e != cudaSuccess) return e;
-  int ranks = 1;
-  while (ranks * kSlice < pr.n) ranks *= 2;
+  const int ranks = cluster_ranks(pr.n);
   SmallArgs a{};
   a.count = pr.count, a.m = pr.m, a.n = pr.n;
-  a.slice = ((pr.n + ranks - 1) / ranks + 63) / 64 * 64;
+  a.slice = slice_columns(pr.n, ranks);
   a.steps = pr.steps;
   for (int k = 0; k < pr.steps; ++k)
     for (int j = 0; j < 3; ++j) a.coeff[k][j] = pr.coeff[k][j];
