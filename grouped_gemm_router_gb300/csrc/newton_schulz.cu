@@ -1050,26 +1050,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // epilogue warps spend on the next tile.  Where there is no next tile to
     // speak of they count their own parts, which is sooner (3 x 1001 x 363:
     // 177 -> 163 us; a step of 24 matrices of 768 x 1536: 490 -> 512 us).
+    //
+    // Each lane waits for one epilogue warp, and lane 0 alone fences, counts
+    // and gives the tile's place back.  So what the other lanes have acquired,
+    // and their reading of the place, are ordered before it by a __syncwarp
+    // (votes and shuffles order no memory), and all lanes leave together.
     int upto = 0;
     Tile t;
-    for (int i = 0; next_tile(ctl, i, t, abort_flag, dev_err); ++i) {
-      if (i >= upto) {  // all that every warp has issued by now, with one fence
+    for (int i = 0;; ++i) {
+      const bool got = next_tile(ctl, i, t, abort_flag, dev_err);
+      if (!__all_sync(0xffffffffu, got)) break;
+      bool fresh = false;  // newly seen stores to fence
+      if (i >= upto) {     // all that every warp has issued by now, with one fence
         int v = lane < kEpiWarps ? wait_count(&ctl.written[lane], i, abort_flag, dev_err) : 0x7fffffff;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
         if (v < 0) break;
         upto = v;
-        if (lane == 0 && !p.direct) {
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-          __threadfence();
-        }
-      }
-      if (lane == 0) {
-        if (!p.direct && t.prod + 1 < 3 * p.steps) count_done(p, t);
-        count_store(&ctl.counted, i + 1);
+        fresh = true;
       }
       __syncwarp();
+      if (lane == 0) {
+        if (!p.direct) {
+          if (fresh) {
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            __threadfence();
+          }
+          if (t.prod + 1 < 3 * p.steps) count_done(p, t);
+        }
+        count_store(&ctl.counted, i + 1);
+      }
     }
+    __syncwarp();
   } else if (warp == 3 + kEpiWarps) {
     // ===================== next tiles (both CTAs) =====================
     // The CTA's tiles in order, each posted when the product that it reads is
