@@ -894,6 +894,8 @@ MOE_DEV bool epilogue_last(const NsMaps& maps, const GemmArgs& p, const NsStacks
       }
     }
   }
+  // the next tile's hi comes into the buffer by TMA (a __syncwarp follows)
+  fence_proxy_async_smem();
   return true;
 }
 
