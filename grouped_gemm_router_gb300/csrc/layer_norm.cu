@@ -15,6 +15,7 @@
 // partial rows; there are no atomics, so the results do not change from run
 // to run.
 #include <algorithm>
+#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_kernels.cuh"
@@ -580,9 +581,21 @@ cudaError_t reduce_partials(const LayerNormBwdArgs& a, int nblk, cudaStream_t s)
                        static_cast<const float*>(a.part), nblk, a.D, a.dweight, a.dbias);
 }
 
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+// A kernel's limit of dynamic shared memory: one for all its calls, whatever
+// they ask for, so that host threads with different widths do not take it from
+// one another between setting it and launching.  Set once on each device.
+constexpr int kMaxDevices = 64;
+cudaError_t allow_smem(const void* kernel, size_t limit, bool (&done)[kMaxDevices]) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit));
+  done[dev] = e == cudaSuccess;
+  return e;
 }
 
 template <typename XT, int P, int N, int VEC>
@@ -592,10 +605,13 @@ cudaError_t run_bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
   int nblk = std::min({(a.T + kRows - 1) / kRows, 2 * sms, kLnMaxPartials});
   cudaError_t e = cudaSuccess;
   if (nblk == 0) return reduce_partials(a, 0, s);  // no rows: the sums are zeros
+  static bool smem_set[2][kMaxDevices];            // without and with d_stream
+  bool(&set)[kMaxDevices] = smem_set[a.d_stream != nullptr];
   if constexpr (VEC == 1) {
     auto kernel = a.d_stream ? layer_norm_bwd_kernel<XT, P, N, true> : layer_norm_bwd_kernel<XT, P, N, false>;
     const size_t smem = static_cast<size_t>(kRows) * 2 * a.D * sizeof(float);
-    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
+    constexpr size_t kLimit = static_cast<size_t>(kRows) * 2 * P * N * sizeof(float);  // D <= P N
+    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), kLimit, set)) != cudaSuccess) return e;
     e = launch_kernel(kernel, dim3(nblk), dim3(kLnThreads), smem, s, false, static_cast<const uint16_t*>(a.dy),
                       static_cast<const XT*>(a.x), a.weight, a.mean, a.rstd, static_cast<const XT*>(a.d_stream), a.T,
                       a.D, static_cast<XT*>(a.dx), a.part, a.dweight, a.dbias);
@@ -611,7 +627,7 @@ cudaError_t run_bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
     if ((e = device_error_address(&err)) != cudaSuccess) return e;
     auto kernel =
         a.d_stream ? layer_norm_bwd_ring_kernel<XT, P, N, true> : layer_norm_bwd_ring_kernel<XT, P, N, false>;
-    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(reinterpret_cast<const void*>(kernel), kLnWholeSm, set)) != cudaSuccess) return e;
     e = launch_kernel(kernel, dim3(nblk), dim3(kRingThreads), smem, s, false, static_cast<const uint16_t*>(a.dy),
                       static_cast<const XT*>(a.x), a.weight, a.mean, a.rstd, static_cast<const XT*>(a.d_stream), a.T,
                       a.D, stages, static_cast<XT*>(a.dx), a.part, a.dweight, a.dbias, err);
