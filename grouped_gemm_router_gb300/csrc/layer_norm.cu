@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
     const uint16_t* sdy = reinterpret_cast<const uint16_t*>(ring + st * slot) + group * D;
     const XT* sx = reinterpret_cast<const XT*>(ring + st * slot + kRows * D * 2) + group * D;
     const XT* sg = sx + kRows * D;
-    // n = x r - mu r
-    const f2 rr = pack2(r, r), mr = pack2(-mu * r, -mu * r);
+    // n = (x - mu) r and not x r - mu r: that would bring in the rounding of
+    // mu r, whatever the size of n (rows 2000 spreads from zero lost 11 bits)
+    const f2 rr = pack2(r, r), m0 = pack2(-mu, -mu);
     f2 q1 = 0ull, q2 = 0ull;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
         slot_vec(wsm + c, wv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          n[j] = fma2(n[j], rr, mr);
+          n[j] = mul2(add2(n[j], m0), rr);
           dw[i][j] = fma2(p[j], n[j], dw[i][j]);
           db[i][j] = add2(db[i][j], p[j]);
           p[j] = mul2(p[j], wv[j]);
@@ -491,11 +492,9 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
     float s1 = unpack2(q1).x + unpack2(q1).y, s2 = unpack2(q2).x + unpack2(q2).y;
     row_sum2<P>(s1, s2, group, red[flip]);
     flip ^= 1;
-    // dx = r dy w - r s1 / D - n r s2 / D, the last two as x k1 + k0
-    const float t2 = -r * s2 * inv_d;
-    const f2 k1 = pack2(t2 * r, t2 * r);
-    const float t0 = fmaf(-t2 * r, mu, -r * s1 * inv_d);
-    const f2 k0 = pack2(t0, t0);
+    // dx = r dy w - r s1 / D - n r s2 / D, the last two as (x - mu) k1 + k0
+    const float t2 = -r * s2 * inv_d, t0 = -r * s1 * inv_d;
+    const f2 k1 = pack2(t2 * r, t2 * r), k0 = pack2(t0, t0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * P + t) * 8;
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
         slot_vec(sdy + c, p);
         slot_vec(wsm + c, wv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fma2(p[j], mul2(wv[j], rr), fma2(n[j], k1, k0));
+        for (int j = 0; j < 4; ++j) p[j] = fma2(p[j], mul2(wv[j], rr), fma2(add2(n[j], m0), k1, k0));
         if constexpr (STREAM) {
           slot_vec(sg + c, n);
 #pragma unroll
