@@ -377,7 +377,7 @@ _STREAM_TYPES = {torch.bfloat16: N.MOE_BF16, torch.float32: N.MOE_FP32}
 _F32 = torch.float32
 _BF16 = torch.bfloat16
 _empty = torch.empty
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a torch without CUDA has none
 
 
 def _stream_of(t):
