@@ -386,10 +386,21 @@ def _stream_of(t):
     return _raw_stream(t.device.index)
 
 
-def _like(t, name, dtype, shape):
-    """As _need for a tensor that must be there, without the copies."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _like(t, name, dtype, shape, dev):
+    """As _need for a tensor that must be there, on device number dev, without
+    the copies."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{dev}")
+
+
+def _current(t, name):
+    """The number of t's device, which has to be the current one: that is where
+    the C ABI launches."""
+    dev, now = t.get_device(), torch.cuda.current_device()
+    if dev != now:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{now}")
+    return dev
 
 
 def _stream_type(x):
@@ -411,22 +422,23 @@ def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
     rounded to x's type, and that is what is normalised; the dict then holds
     h too.  weight, bias: [D] fp32.  Any D up to 8192."""
     kind = _stream_type(x)
+    dev = _current(x, "x")
     shape = x.shape
     T, D = shape
-    _like(weight, "weight", _F32, (D,))
+    _like(weight, "weight", _F32, (D,), dev)
     if bias is not None:
-        _like(bias, "bias", _F32, (D,))
-    dev = x.device
-    if y is None:
-        y = _empty(shape, dtype=_BF16, device=dev)
+        _like(bias, "bias", _F32, (D,), dev)
+    if add is not None:
+        _like(add, "add", _BF16, shape, dev)
+    if y is not None:
+        _like(y, "y", _BF16, shape, dev)
     else:
-        _like(y, "y", _BF16, shape)
-    mean = _empty(T, dtype=_F32, device=dev)
-    rstd = _empty(T, dtype=_F32, device=dev)
+        y = _empty(shape, dtype=_BF16, device=x.device)
+    mean = _empty(T, dtype=_F32, device=x.device)
+    rstd = _empty(T, dtype=_F32, device=x.device)
     out = dict(y=y, mean=mean, rstd=rstd)
     h = None
     if add is not None:
-        _like(add, "add", _BF16, shape)
         h = out["h"] = torch.empty_like(x)
     st = lib.moe_layer_norm_forward(x.data_ptr(), kind, None if add is None else add.data_ptr(), weight.data_ptr(),
                                     None if bias is None else bias.data_ptr(), eps, T, D, y.data_ptr(),
@@ -444,23 +456,23 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
     mean, rstd: the forward's; dy [T, D] bf16; d_stream [T, D] in x's type:
     the gradient that reaches these rows past the norm."""
     kind = _stream_type(x)
+    dev = _current(x, "x")
     shape = x.shape
     T, D = shape
-    _like(dy, "dy", _BF16, shape)
-    _like(weight, "weight", _F32, (D,))
-    _like(mean, "mean", _F32, (T,))
-    _like(rstd, "rstd", _F32, (T,))
+    _like(dy, "dy", _BF16, shape, dev)
+    _like(weight, "weight", _F32, (D,), dev)
+    _like(mean, "mean", _F32, (T,), dev)
+    _like(rstd, "rstd", _F32, (T,), dev)
     if d_stream is not None:
-        _like(d_stream, "d_stream", x.dtype, shape)
-    dev = x.device
+        _like(d_stream, "d_stream", x.dtype, shape, dev)
     dx = torch.empty_like(x)
-    dweight = _empty(D, dtype=_F32, device=dev)
+    dweight = _empty(D, dtype=_F32, device=x.device)
     out = dict(dx=dx, dweight=dweight)
     dbias = None
     if bias:
-        dbias = out["dbias"] = _empty(D, dtype=_F32, device=dev)
+        dbias = out["dbias"] = _empty(D, dtype=_F32, device=x.device)
     nscratch = lib.moe_layer_norm_backward_scratch_size(T, D)
-    scratch = _empty(max(nscratch, 16), dtype=torch.uint8, device=dev)
+    scratch = _empty(max(nscratch, 16), dtype=torch.uint8, device=x.device)
     st = lib.moe_layer_norm_backward(dy.data_ptr(), x.data_ptr(), kind, weight.data_ptr(), mean.data_ptr(),
                                      rstd.data_ptr(), None if d_stream is None else d_stream.data_ptr(), T, D,
                                      dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
@@ -503,16 +515,19 @@ def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, 
     if g.dim() not in (2, 3):
         raise ValueError(f"g has shape {tuple(g.shape)}, expected [rows, cols] or [B, rows, cols]")
     _need(g, "g", g.dtype)
+    dev = _current(g, "g")
+    if out is not None:
+        _like(out, "out", _BF16, g.shape, dev)
+    if workspace is not None:
+        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
     count = g.shape[0] if g.dim() == 3 else 1
     rows, cols = g.shape[-2:]
     c = _ns_coefficients(coefficients, steps)
+    nbytes = newton_schulz_workspace_size(count, rows, cols)
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-    _need(out, "out", torch.bfloat16, g.shape)
-    nbytes = newton_schulz_workspace_size(count, rows, cols)
     if workspace is None:
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=g.device)
-    _need(workspace, "workspace", torch.uint8)
     st = lib.moe_newton_schulz(g.data_ptr(), kind, count, rows, cols, steps, c, eps, out.data_ptr(),
                                workspace.data_ptr(), workspace.numel(), _stream_of(g))
     check(st, "moe_newton_schulz")
@@ -542,16 +557,24 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
     for t, name in ((wtype, "weights"), (gtype, "grads")):
         if t not in _STREAM_TYPES:
             raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t}")
-    groups = {}
+    dev = None
     for i, (w, g, m, b) in enumerate(zip(weights, grads, momenta, low)):
         if w.dim() not in (2, 3):
             raise ValueError(f"weights[{i}] has shape {tuple(w.shape)}, expected [rows, cols] or [B, rows, cols]")
         _need(w, f"weights[{i}]", wtype)
-        _need(g, f"grads[{i}]", gtype, w.shape)
-        _need(m, f"momenta[{i}]", torch.float32, w.shape)
-        _need(b, f"weights_bf16[{i}]", torch.bfloat16, w.shape)
-        if b is not None and wtype != torch.float32:
-            raise ValueError("weights_bf16 are the copies of fp32 weights")
+        if dev is None:
+            dev = _current(w, "weights[0]")
+        _like(w, f"weights[{i}]", wtype, w.shape, dev)
+        _like(g, f"grads[{i}]", gtype, w.shape, dev)
+        _like(m, f"momenta[{i}]", _F32, w.shape, dev)
+        if b is not None:
+            _like(b, f"weights_bf16[{i}]", _BF16, w.shape, dev)
+            if wtype != _F32:
+                raise ValueError("weights_bf16 are the copies of fp32 weights")
+    if workspace is not None:
+        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    groups = {}
+    for w, g, m, b in zip(weights, grads, momenta, low):
         rows, cols = w.shape[-2:]
         stack = N.MoeMatrixStack(w.data_ptr(), g.data_ptr(), m.data_ptr(), None if b is None else b.data_ptr(),
                                  w.shape[0] if w.dim() == 3 else 1, rows, cols)
@@ -562,7 +585,6 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
     sizes = [newton_schulz_workspace_size(sum(s.count for s in group), *key) for key, group in calls]
     if workspace is None:
         workspace = torch.empty(max(*sizes, 256), dtype=torch.uint8, device=weights[0].device)
-    _need(workspace, "workspace", torch.uint8)
     if workspace.numel() < max(sizes):
         raise N.MoeError(N.MOE_ERR_WORKSPACE, "moe_muon_step")
     stream = _stream_of(weights[0])
