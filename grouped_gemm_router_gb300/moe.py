@@ -403,6 +403,19 @@ def _current(t, name):
     return dev
 
 
+def _aligned(t):
+    """t, or a copy of it where it does not start on the 16-byte boundary that
+    the C ABI needs (a view into a larger tensor)."""
+    return t.clone() if t is not None and t.data_ptr() & 15 else t
+
+
+def _ns_workspace(t, dev):
+    if t is not None:
+        _like(t, "workspace", torch.uint8, t.shape, dev)
+        if t.data_ptr() & 255:
+            raise ValueError("workspace must start on a 256-byte boundary")
+
+
 def _stream_type(x):
     """The C ABI's element type of a residual stream x."""
     kind = _STREAM_TYPES.get(x.dtype)
@@ -420,7 +433,8 @@ def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
     the MoE layer: dict(y [T, D] bf16, mean [T] fp32, rstd [T] fp32).  With
     `add` [T, D] bf16 (a sublayer's output) the stream becomes h = x + add,
     rounded to x's type, and that is what is normalised; the dict then holds
-    h too.  weight, bias: [D] fp32.  Any D up to 8192."""
+    h too.  weight, bias: [D] fp32.  Any D up to 8192.  A tensor that does not
+    start on 16 bytes is copied first."""
     kind = _stream_type(x)
     dev = _current(x, "x")
     shape = x.shape
@@ -434,16 +448,22 @@ def layer_norm_forward(x, weight, bias=None, eps=1e-5, add=None, y=None):
         _like(y, "y", _BF16, shape, dev)
     else:
         y = _empty(shape, dtype=_BF16, device=x.device)
+    px, pw, py = x.data_ptr(), weight.data_ptr(), y.data_ptr()
+    pb = None if bias is None else bias.data_ptr()
+    pa = None if add is None else add.data_ptr()
+    if (px | pw | py | (pb or 0) | (pa or 0)) & 15:
+        out = layer_norm_forward(_aligned(x), _aligned(weight), _aligned(bias), eps, _aligned(add), _aligned(y))
+        if out["y"] is not y:
+            out["y"] = y.copy_(out["y"])
+        return out
     mean = _empty(T, dtype=_F32, device=x.device)
     rstd = _empty(T, dtype=_F32, device=x.device)
     out = dict(y=y, mean=mean, rstd=rstd)
     h = None
     if add is not None:
         h = out["h"] = torch.empty_like(x)
-    st = lib.moe_layer_norm_forward(x.data_ptr(), kind, None if add is None else add.data_ptr(), weight.data_ptr(),
-                                    None if bias is None else bias.data_ptr(), eps, T, D, y.data_ptr(),
-                                    None if h is None else h.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                    _stream_of(x))
+    st = lib.moe_layer_norm_forward(px, kind, pa, pw, pb, eps, T, D, py, None if h is None else h.data_ptr(),
+                                    mean.data_ptr(), rstd.data_ptr(), _stream_of(x))
     if st:
         check(st, "moe_layer_norm_forward")
     return out
@@ -454,7 +474,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
     dict(dx [T, D] in x's type, dweight [D] fp32, and with bias=True dbias [D]
     fp32).  x: the rows that were normalised (the forward's h where it added);
     mean, rstd: the forward's; dy [T, D] bf16; d_stream [T, D] in x's type:
-    the gradient that reaches these rows past the norm."""
+    the gradient that reaches these rows past the norm.  A tensor that does not
+    start on 16 bytes is copied first."""
     kind = _stream_type(x)
     dev = _current(x, "x")
     shape = x.shape
@@ -465,6 +486,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
     _like(rstd, "rstd", _F32, (T,), dev)
     if d_stream is not None:
         _like(d_stream, "d_stream", x.dtype, shape, dev)
+    pdy, px, pw, pm, pr = dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr()
+    pd = None if d_stream is None else d_stream.data_ptr()
+    if (pdy | px | pw | pm | pr | (pd or 0)) & 15:
+        return layer_norm_backward(*(_aligned(t) for t in (dy, x, weight, mean, rstd)), bias, _aligned(d_stream))
     dx = torch.empty_like(x)
     dweight = _empty(D, dtype=_F32, device=x.device)
     out = dict(dx=dx, dweight=dweight)
@@ -473,10 +498,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, d_stream=None):
         dbias = out["dbias"] = _empty(D, dtype=_F32, device=x.device)
     nscratch = lib.moe_layer_norm_backward_scratch_size(T, D)
     scratch = _empty(max(nscratch, 16), dtype=torch.uint8, device=x.device)
-    st = lib.moe_layer_norm_backward(dy.data_ptr(), x.data_ptr(), kind, weight.data_ptr(), mean.data_ptr(),
-                                     rstd.data_ptr(), None if d_stream is None else d_stream.data_ptr(), T, D,
-                                     dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
-                                     scratch.data_ptr(), nscratch, _stream_of(x))
+    st = lib.moe_layer_norm_backward(pdy, px, kind, pw, pm, pr, pd, T, D, dx.data_ptr(), dweight.data_ptr(),
+                                     None if dbias is None else dbias.data_ptr(), scratch.data_ptr(), nscratch,
+                                     _stream_of(x))
     if st:
         check(st, "moe_layer_norm_backward")
     return out
@@ -508,7 +532,7 @@ def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, 
     X <- a X + (b A + c A A) X with A = X X^T (X^T X where rows > cols).
     Returns bf16 of g's shape.  coefficients: one (a, b, c) or one for each
     step.  workspace: a uint8 CUDA tensor of newton_schulz_workspace_size
-    bytes."""
+    bytes.  A g or out that does not start on 16 bytes goes through a copy."""
     kind = _STREAM_TYPES.get(g.dtype)
     if kind is None:
         raise ValueError(f"g must be torch.bfloat16 or torch.float32, got {g.dtype}")
@@ -518,14 +542,16 @@ def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, 
     dev = _current(g, "g")
     if out is not None:
         _like(out, "out", _BF16, g.shape, dev)
-    if workspace is not None:
-        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _ns_workspace(workspace, dev)
     count = g.shape[0] if g.dim() == 3 else 1
     rows, cols = g.shape[-2:]
     c = _ns_coefficients(coefficients, steps)
     nbytes = newton_schulz_workspace_size(count, rows, cols)
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    if (g.data_ptr() | out.data_ptr()) & 15:
+        o = newton_schulz(_aligned(g), steps, coefficients, eps, _aligned(out), workspace)
+        return o if o is out else out.copy_(o)
     if workspace is None:
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=g.device)
     st = lib.moe_newton_schulz(g.data_ptr(), kind, count, rows, cols, steps, c, eps, out.data_ptr(),
@@ -546,7 +572,8 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
     all fp32 (as moe_ffn_backward returns them) or all bf16; momenta: fp32.
     scale: by default 0.2 sqrt(max(rows, cols)).  Matrices of the same shape
     up to transposition are worked on together.  workspace: a uint8 CUDA
-    tensor of the largest newton_schulz_workspace_size among those groups."""
+    tensor of the largest newton_schulz_workspace_size among those groups.
+    Tensors that do not start on 16 bytes are updated by way of copies."""
     n = len(weights)
     low = [None] * n if weights_bf16 is None else list(weights_bf16)
     if not (len(grads) == len(momenta) == len(low) == n):
@@ -571,10 +598,12 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
             _like(b, f"weights_bf16[{i}]", _BF16, w.shape, dev)
             if wtype != _F32:
                 raise ValueError("weights_bf16 are the copies of fp32 weights")
-    if workspace is not None:
-        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    groups = {}
-    for w, g, m, b in zip(weights, grads, momenta, low):
+    _ns_workspace(workspace, dev)
+    groups, copies = {}, []
+    for tensors in zip(weights, grads, momenta, low):
+        used = [_aligned(t) for t in tensors]
+        copies += [(t, a) for t, a in zip(tensors, used) if a is not t]
+        w, g, m, b = used
         rows, cols = w.shape[-2:]
         stack = N.MoeMatrixStack(w.data_ptr(), g.data_ptr(), m.data_ptr(), None if b is None else b.data_ptr(),
                                  w.shape[0] if w.dim() == 3 else 1, rows, cols)
@@ -594,6 +623,8 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
         st = lib.moe_muon_step((N.MoeMatrixStack * len(group))(*group), len(group), _STREAM_TYPES[gtype],
                                _STREAM_TYPES[wtype], ctypes.byref(p), workspace.data_ptr(), workspace.numel(), stream)
         check(st, "moe_muon_step")
+    for t, a in copies:
+        t.copy_(a)
 
 
 def device_error() -> int:
