@@ -124,12 +124,12 @@ MOE_DEV float row_sum(float v, float* red) {
 
 // Six blocks an SM where a thread holds 24 bf16 values or fewer: 36.3 us at T
 // = 32768, D = 768, against 40.3 without a bound and 40.2 with seven; with
-// fp32 or more values a bound costs more than it gives.
+// fp32 or more values a bound costs more than it gives.  h may be x itself
+// (no __restrict__): a thread stores only what it has loaded.
 template <typename XT, int P, int N, int VEC, bool ADD>
 __global__ void __launch_bounds__(kLnThreads, VEC == 8 && sizeof(XT) == 2 && N <= 3 ? 6 : 1) layer_norm_kernel(
-    const XT* __restrict__ x, const uint16_t* __restrict__ add, const float* __restrict__ w,
-    const float* __restrict__ b, float eps, int T, int D, uint16_t* __restrict__ y, XT* __restrict__ h,
-    float* __restrict__ mean, float* __restrict__ rstd) {
+    const XT* x, const uint16_t* __restrict__ add, const float* __restrict__ w, const float* __restrict__ b, float eps,
+    int T, int D, uint16_t* __restrict__ y, XT* h, float* __restrict__ mean, float* __restrict__ rstd) {
   __shared__ float red[kLnWarps];
   constexpr int kRows = kLnThreads / P;
   const int t = threadIdx.x % P;
@@ -215,12 +215,14 @@ MOE_DEV void block_sums(const float* sums, int D, float* part, float* dweight, f
 
 // Backward: block k takes row groups k, k + gridDim.x, ...; part[k] = its
 // sums of dy n (first D) and dy (next D).  This form, one element at a time,
-// is for rows that are no multiple of 16 bytes.
+// is for rows that are no multiple of 16 bytes.  dx may be d_stream itself (no
+// __restrict__ on the two, here and below): an element is read before it is
+// written, by the same thread or into the row's slot.
 template <typename XT, int P, int N, bool STREAM>
 __global__ void __launch_bounds__(kLnThreads) layer_norm_bwd_kernel(
     const uint16_t* __restrict__ dy, const XT* __restrict__ x, const float* __restrict__ w,
-    const float* __restrict__ mean, const float* __restrict__ rstd, const XT* __restrict__ d_stream, int T, int D,
-    XT* __restrict__ dx, float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias) {
+    const float* __restrict__ mean, const float* __restrict__ rstd, const XT* d_stream, int T, int D,
+    XT* dx, float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias) {
   constexpr int VEC = 1;
   extern __shared__ float sums[];  // [kRows][2][D]
   __shared__ float red[2 * kLnWarps];
@@ -391,8 +393,8 @@ MOE_DEV void store_pairs(uint16_t* p, const f2 (&v)[4]) {
 template <typename XT, int P, int N, bool STREAM>
 __global__ void __launch_bounds__(kRingThreads) layer_norm_bwd_ring_kernel(
     const uint16_t* __restrict__ dy, const XT* __restrict__ x, const float* __restrict__ w,
-    const float* __restrict__ mean, const float* __restrict__ rstd, const XT* __restrict__ d_stream, int T, int D,
-    int stages, XT* __restrict__ dx, float* __restrict__ part, float* __restrict__ dweight,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const XT* d_stream, int T, int D,
+    int stages, XT* dx, float* __restrict__ part, float* __restrict__ dweight,
     float* __restrict__ dbias, unsigned int* dev_err) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kLnMaxStages], empty[kLnMaxStages];
