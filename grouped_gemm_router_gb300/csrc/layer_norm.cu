@@ -122,12 +122,19 @@ MOE_DEV float row_sum(float v, float* red) {
   return v;
 }
 
-// Six blocks an SM where a thread holds 24 bf16 values or fewer: 36.3 us at T
-// = 32768, D = 768, against 40.3 without a bound and 40.2 with seven; with
-// fp32 or more values a bound costs more than it gives.  h may be x itself
-// (no __restrict__): a thread stores only what it has loaded.
+// Blocks an SM that the compiler keeps registers for: six for bf16 rows of up
+// to 512 columns, and with a residual sum up to 768; else its own choice.
+// Device time at 50 MB of x, bf16, with the bound / without: with the sum D =
+// 256 33.9 / 33.9 us, 512 33.2 / 35.4, 768 33.8 / 38.7 (seven blocks: 40.2),
+// 1024 37.5 / 38.4, 2048 39.5 / 41.2; without it 512 21.9 / 22.6, 768 24.7 /
+// 22.1, 1024 27.9 / 22.4, 2048 28.6 / 23.9.  fp32 (100 MB): 512 45.7 / 45.7
+// and 26.7 / 26.1, 768 47.8 / 47.8 and 26.2 / 25.8.
+template <typename XT, int N, int VEC, bool ADD>
+constexpr int kFwdBlocks = VEC == 8 && sizeof(XT) == 2 && N <= (ADD ? 3 : 2) ? 6 : 1;
+
+// h may be x itself (no __restrict__): a thread stores only what it has loaded.
 template <typename XT, int P, int N, int VEC, bool ADD>
-__global__ void __launch_bounds__(kLnThreads, VEC == 8 && sizeof(XT) == 2 && N <= 3 ? 6 : 1) layer_norm_kernel(
+__global__ void __launch_bounds__(kLnThreads, kFwdBlocks<XT, N, VEC, ADD>) layer_norm_kernel(
     const XT* x, const uint16_t* __restrict__ add, const float* __restrict__ w, const float* __restrict__ b, float eps,
     int T, int D, uint16_t* __restrict__ y, XT* h, float* __restrict__ mean, float* __restrict__ rstd) {
   __shared__ float red[kLnWarps];
