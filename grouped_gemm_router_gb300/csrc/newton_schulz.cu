@@ -1342,9 +1342,15 @@ cudaError_t launch_newton_schulz(const NsProblem& pr, void* workspace, cudaStrea
   a.steps = pr.steps;
   // Narrow tiles while one wave of them holds the widest product, two with a
   // short k: what counts then is how long a tile takes, and not that operands
-  // are loaded twice as often.  3 x 1001 x 363: 163 -> 133 us; 12 x 256 x 1024
-  // 132 -> 119, 3 x 512 x 2048 167 -> 151, 4 x 768 x 1536 (1.9 waves) 181 both
-  // ways; but 30 x 256 x 1024 (3.2) 153 -> 160, 1 x 2048 x 2048 (1.7) 248 -> 288.
+  // are loaded twice as often.  3 x 1001 x 363: 163 -> 133 us.  Between one and
+  // two waves, wide / narrow: 12 x 256 x 1024 132 / 119, 12 x 512 x 512 139 /
+  // 127, 4 x 512 x 2048 175 / 164, 3 x 640 x 1280 156 / 141, 3 x 768 x 1536
+  // 173 / 162, 4 x 768 x 1536 (1.9 waves) 184 / 185; where 1.9 waves of narrow
+  // ones are one of wide ones they lose (18 x 512 x 512 147 / 161, 8 x 768 x 768
+  // 166 / 173).  Past 768 rows there is little to gain and more to lose: 3 x 832
+  // x 832 156 / 146, 3 x 1024 x 1024 174 / 170, 2 x 1280 x 1280 190 / 193, 3 x
+  // 1280 x 1280 212 / 211, 2 x 1536 x 1536 227 / 228, 1 x 2048 x 2048 251 / 280.
+  // Past two waves 30 x 256 x 1024 (3.2) takes 153 / 160.
   a.tn = 128;
   if (static_cast<long>(count) * Walk::tiles(a, kApply) > (mp <= 3 * kTile ? 2 : 1) * pairs) a.tn = kTile;
   a.direct = static_cast<long>(count) * Walk::tiles(a, kGram) <= pairs;
