@@ -28,7 +28,12 @@
 // Simulated 2-norm errors, of which the bf16 rounding of the result is
 // 1.66e-3: full rank 1.8e-3 to 2.1e-3 (2.3e-3 to 2.6e-3 without the fp32
 // diagonal), rank m/4 2.0e-3 (1.1e-2 to 2.6e-2 without lo; with bf16 operands
-// 0.9e-1 to 2e-1).
+// 0.9e-1 to 2e-1).  Measured before that rounding, five steps: 0.6e-3 (4096 x
+// 4096) to 1.3e-3 (65 x 200) at full rank, 1.0e-3 to 1.6e-3 at rank m/4.  The
+// roundings of X (in A and in B X), A and B share it about evenly, over all
+// steps: simulated, leaving out any one of them takes off a tenth to a fifth.
+// So a result as exact as fp32 products would take operands split in two, three
+// products for each one here; the update that this is for has far more noise.
 //
 // A and B are symmetric: only the tiles on and below the diagonal are computed
 // and stored.  Where a product needs one from above, it loads the tile from
@@ -51,12 +56,12 @@
 // every tile depend on lower-numbered ones only and the launch is
 // cooperative, so the waits end; they are bounded all the same.
 //
-// Measured, whole calls: 24 matrices of 768 x 1536 500 us (0.76 PFLOP/s of the
-// operations that symmetry leaves), 12 of 2048 x 8192 5.4 ms (1.24, at the
-// power limit), 8 of 768 x 1536 without the step's weights 213 us.  Of the 500
+// Measured, whole calls: 24 matrices of 768 x 1536 513 us (0.74 PFLOP/s of the
+// operations that symmetry leaves), 12 of 2048 x 8192 5.6 ms (1.19, at the
+// power limit), 8 of 768 x 1536 without the step's weights 218 us.  Of the 513
 // us the kernels before the products take about 98, near the memory's rate.
-// With the epilogues taken out the call took 354: what bounds these sizes is
-// the epilogues' traffic and the way from product to product.
+// With the epilogues taken out an earlier state's 509 became 354: what bounds
+// these sizes is the epilogues' traffic and the way from product to product.
 //
 // Warp roles (one CTA per SM):
 //   warp 0      TMA producer (one lane) -- both CTAs load their own halves

@@ -6,7 +6,7 @@
 // small each takes well under a microsecond: what counts is the way from one
 // to the next.  Through memory and a counter 4 matrices of 128 x 256 take
 // 82 us for five steps (the tiled kernel of newton_schulz.cu); here X, A and B
-// stay in shared memory and TMEM, and they take 31 us.
+// stay in shared memory and TMEM, and they take 30 us.
 //
 //   TMEM (512 columns): X in fp32 (256), A = X X^T (128), A A (128)
 //   shared memory: X in fp16 (64 KB), A and then B in fp16 (32 KB), A's

@@ -531,7 +531,9 @@ def newton_schulz(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, 
     or fp32): X = G / (|G| + eps), then `steps` times
     X <- a X + (b A + c A A) X with A = X X^T (X^T X where rows > cols).
     Returns bf16 of g's shape.  coefficients: one (a, b, c) or one for each
-    step.  workspace: a uint8 CUDA tensor of newton_schulz_workspace_size
+    step.  The products take fp16 operands and fp32 sums: before its rounding
+    to bf16 the result is about 1e-3 off in the 2-norm (moe_ffn.h has the
+    ranges).  workspace: a uint8 CUDA tensor of newton_schulz_workspace_size
     bytes.  A g or out that does not start on 16 bytes goes through a copy."""
     kind = _STREAM_TYPES.get(g.dtype)
     if kind is None:
@@ -571,8 +573,9 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
     may be None) the bf16 copies that the layer reads are written too; grads:
     all fp32 (as moe_ffn_backward returns them) or all bf16; momenta: fp32.
     scale: by default 0.2 sqrt(max(rows, cols)).  Matrices of the same shape
-    up to transposition are worked on together.  workspace: a uint8 CUDA
-    tensor of the largest newton_schulz_workspace_size among those groups.
+    up to transposition are worked on together, and the weights move by
+    newton_schulz's result before its rounding to bf16.  workspace: a uint8
+    CUDA tensor of the largest newton_schulz_workspace_size among those groups.
     Tensors that do not start on 16 bytes are updated by way of copies."""
     n = len(weights)
     low = [None] * n if weights_bf16 is None else list(weights_bf16)
