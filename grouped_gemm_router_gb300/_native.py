@@ -26,6 +26,9 @@ CHAINED_MAX_D = 256
 MOE_BF16 = 0
 MOE_FP32 = 1
 
+MOE_I32 = 0
+MOE_I64 = 1
+
 MAX_EXPERTS = 128
 MAX_TOPK = 16
 MAX_DIM = 8192
@@ -41,6 +44,15 @@ class MoeOptions(ctypes.Structure):
                 ("ids_in", ctypes.c_void_p),
                 ("weights_in", ctypes.c_void_p),
                 ("flags", ctypes.c_uint32)]
+
+
+MAX_VOCAB = 1 << 22
+MAX_TEACHER = 256
+
+
+class MoeTeacher(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("ids_type", ctypes.c_int),
+                ("logits_type", ctypes.c_int), ("K", ctypes.c_int32), ("temperature", ctypes.c_float)]
 
 
 MAX_STACKS = 16
@@ -91,6 +103,18 @@ _SIGNATURES = {
     "moe_newton_schulz_workspace_size": (_sz, [_i32, _i32, _i32]),
     "moe_newton_schulz": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _sz, _vp]),
     "moe_muon_step": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "moe_embedding_forward": (_i32, [_vp, _i32, _vp, _i32, _f32, _i32, _i32, _i32, _vp, _i32, _vp]),
+    "moe_embedding_backward_scratch_size": (_sz, [_i32, _i32, _i32]),
+    "moe_embedding_backward": (_i32, [_vp, _i32, _vp, _i32, _f32, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "moe_vocab_forward_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_vocab_backward_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_cross_entropy_forward": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "moe_cross_entropy_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                          _sz, _vp]),
+    "moe_distill_forward": (_i32, [_vp, _vp, ctypes.POINTER(MoeTeacher), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz,
+                                   _vp]),
+    "moe_distill_backward": (_i32, [_vp, _vp, _vp, ctypes.POINTER(MoeTeacher), _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                                    _vp, _sz, _vp]),
     "moe_permute_noalloc": (_i32, [_vp, MoeDims, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_device_error": (_i32, []),
     "moe_selftest_wait_timeout": (_i32, [_i32, _vp, _vp]),

@@ -203,6 +203,70 @@ cudaError_t launch_newton_schulz(const NsProblem& p, void* workspace, cudaStream
 bool ns_small_fits(int m, int n);
 cudaError_t launch_ns_small(const NsProblem& p, cudaStream_t s);
 
+// ---- embedding (embedding.cu) ----
+struct EmbeddingArgs {
+  const void* ids;    // [T]
+  int ids64;
+  const void* table;  // [V, D]
+  int table_fp32;
+  float scale;
+  int T, V, D;
+  void* out;          // [T, D]
+  int out_fp32;
+};
+cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s);
+struct EmbeddingBwdArgs {
+  const void* d_out;  // [T, D]
+  int d_fp32;
+  const void* ids;    // [T]
+  int ids64;
+  float scale;
+  const void* add;    // [V, D] bf16 or nullptr
+  int T, V, D;
+  float* d_table;     // [V, D]
+};
+size_t embedding_bwd_scratch_bytes(int T, int V, int D);
+cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaStream_t s);
+
+// ---- the vocabulary product under a loss (vocab_head.cu) ----
+// What the softmax of a row is compared with: K = 0, one label a row; K > 0, a
+// teacher's logits at K ids.
+struct VocabTargets {
+  const void* ids;  // [T] or [T, K]
+  int ids64;
+  int K;
+  const void* logits;  // [T, K] or nullptr
+  int logits_fp32;
+};
+struct VocabForward {
+  const void* x;  // [T, D] bf16
+  const void* W;  // [V, D] bf16
+  VocabTargets targets;
+  float temperature;
+  int T, D, V;
+  float* loss;    // [T]
+  float* lse;     // [T]
+  float* target;  // [T, K]: z at the ids (K > 0)
+};
+size_t vocab_forward_workspace_bytes(int T, int D, int V, int K);
+cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStream_t s);
+struct VocabBackward {
+  const float* d_loss;  // [T]
+  const float* d_lse;   // [T] or nullptr (K = 0)
+  const void* x;
+  const void* W;
+  VocabTargets targets;
+  float temperature;
+  const float* loss;    // [T] (K = 0)
+  const float* lse;     // [T]
+  const float* target;  // [T, K] (K > 0)
+  int T, D, V;
+  uint16_t* dx;  // [T, D] bf16
+  uint16_t* dW;  // [V, D] bf16
+};
+size_t vocab_backward_workspace_bytes(int T, int D, int V, int K);
+cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaStream_t s);
+
 // 2-D bf16 TMA descriptor of a row-major [rows, cols] matrix with a
 // {box_cols, box_rows} box: 128-byte swizzle (64-byte for 32-column boxes),
 // zero fill outside the tensor (grouped_gemm.cu).

@@ -1,0 +1,978 @@
+// The vocabulary product at the end of a language model, z = x W^T with
+// x [T, D] and the table W [V, D] (bf16), under a softmax that is compared with
+// one label a token (cross entropy) or with a teacher's K entries a token
+// (distillation).  The logits z [T, V] never reach memory.
+//
+// Forward: with c = log2(e) / temperature, every token needs
+//   lse = ln 2 * log2 sum_v 2^(c z_v)
+// and z at its targets.  vocab_kernel<kStats> computes 256 x 256 tiles of z on
+// CTA pairs (tcgen05.mma.cta_group::2, fp32 in TMEM); its epilogue keeps the
+// running maximum and sum of a row in registers over a run of tiles, picks the
+// targets that lie in the tile, and writes one (maximum, sum) pair a row and
+// run.  vocab_finish_kernel joins them and writes lse and the loss.
+//
+// Backward, by pieces of the vocabulary:
+//   dz_v = a 2^(c z_v - lse / ln 2)  (+ the targets' own terms)
+// vocab_kernel<kDz> recomputes z and stores dz of the piece as bf16 [T, Vc];
+// vocab_kernel<kGrad> runs both products of it in one launch,
+//   dx [T, D] += dz W[piece],   dW[piece] = dz^T x,
+// so that the tiles of one fill the last wave of the other.  The values at the
+// targets (a q - p, where the two terms nearly cancel for a token that is
+// known well) come in fp32 from vocab_ce_rows_kernel or
+// vocab_distill_rows_kernel and replace the epilogue's.
+// dz is the one intermediate that is rounded to fewer than 32 bits: a bf16
+// operand is what the tensor cores take at full rate, and a relative rounding
+// of 2^-9 of each term averages out in sums over V or T.
+//
+// Shared-memory operand layouts (TMA, 128-byte swizzle): x, W and dz are all
+// read in boxes {64 columns, 128 rows, 2 column blocks} of the view
+// {64, rows, columns / 64}.  Along the reduction such a box is two K-major
+// swizzle atoms of 128 rows (slice kk at atom kk / 4, byte 32 (kk % 4)), across
+// it 128 M- or N-major columns of 128 k (LBO = one block of 16 KB, slice kk at
+// byte 2048 kk), so one tensor map serves every use.  Rows and columns outside
+// the tensor read zeros.
+#include <algorithm>
+#include <mutex>
+
+#include "moe_device.cuh"
+#include "moe_kernels.cuh"
+#include "vocab_plan.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kStages = 3;
+constexpr int kOperandBytes = 128 * kBK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBoxes = 4;      // 32-column boxes of an epilogue warp
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.442695040888963407f;
+constexpr int kNoTarget = 0x7fffffff;
+
+// A warp's buffer: 32 rows x 32 columns, fp32 targets or bf16 / fp32 results.
+constexpr int kBoxStats = 4096, kBoxOut = 2048;
+constexpr int smem_bytes(int mode) {
+  return kStages * kStageBytes + kEpiWarps * (mode == kStats ? kBoxStats : kBoxOut) + 1024;
+}
+
+struct VocabArgs : VocabWork {
+  int T, V, D;
+  int v0, Vc, Vcp;         // kDz, kGrad: the piece's first row, its rows, and those rounded up to 64
+  float c;
+  unsigned int* dev_err;
+  // targets: labels (K = 0), or sorted (id << 8 | entry) keys [T, K]
+  const void* labels;
+  int labels64;
+  const uint32_t* keys;
+  int K;
+  float* target;           // kStats: z at the targets [T] or [T, K]
+  float2* part;            // kStats: (maximum, sum) [2 runs, rows_padded]
+  int rows_padded;
+  const float* row_a;      // kDz: a of each row, lse log2(e)
+  const float* row_l;
+  const uint16_t* value;   // kDz: dz at the targets [T] or [T, K]
+  int direct[2];           // kGrad, dx and dW: stored as bf16; otherwise fp32 partials
+  int accumulate;          // dx partials are added to those of the piece before
+  const float* dx_part;    // [splits, T, D]
+};
+
+struct Ctl {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+MOE_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+MOE_DEV long long load_index(const void* p, int is64, size_t i) {
+  return is64 ? static_cast<const long long*>(p)[i] : static_cast<const int*>(p)[i];
+}
+
+// A row's targets in ascending order of their columns.
+struct Targets {
+  const uint32_t* keys;
+  int left;      // keys that remain, with the current one
+  int id;        // current column, or kNoTarget
+  int entry;
+
+  MOE_DEV void set() {
+    if (left > 0) {
+      const uint32_t k = *keys;
+      id = static_cast<int>(k >> 8);
+      entry = static_cast<int>(k & 255u);
+    } else {
+      id = kNoTarget;
+    }
+  }
+  MOE_DEV void step() {
+    ++keys;
+    --left;
+    set();
+  }
+  // From the first target at or past column `col`.
+  MOE_DEV void start(const VocabArgs& p, int row, int col) {
+    left = 0;
+    id = kNoTarget;
+    entry = 0;
+    keys = nullptr;
+    if (row >= p.T) return;
+    if (p.K == 0) {
+      const long long l = load_index(p.labels, p.labels64, row);
+      id = l >= col && l < p.V ? static_cast<int>(l) : kNoTarget;
+      left = 1;
+      return;
+    }
+    const uint32_t* k = p.keys + static_cast<size_t>(row) * p.K;
+    const uint32_t want = static_cast<uint32_t>(col) << 8;
+    int lo = 0, hi = p.K;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (k[mid] < want) lo = mid + 1;
+      else hi = mid;
+    }
+    keys = k + lo;
+    left = p.K - lo;
+    set();
+  }
+  // What lies past the current target (of labels there is no other).
+  MOE_DEV void next(const VocabArgs& p) {
+    if (p.K == 0) id = kNoTarget;
+    else step();
+  }
+  // Position of the current target among the row's keys.
+  MOE_DEV size_t at(const VocabArgs& p, int row) const {
+    return p.K == 0 ? static_cast<size_t>(row) : static_cast<size_t>(row + 1) * p.K - left;
+  }
+};
+
+MOE_DEV void tma_store_f32(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  tma_store_3d(map, src, c0, c1, c2);
+  bulk_commit_group();
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    vocab_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+                 const __grid_constant__ CUtensorMap mapZ, const __grid_constant__ CUtensorMap mapOut0,
+                 const __grid_constant__ CUtensorMap mapOut1, const VocabArgs p) {
+  extern __shared__ uint8_t vocab_smem_raw[];
+  __shared__ Ctl ctl;
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(vocab_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t smem_base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(cluster_id_x());
+  const int npairs = static_cast<int>(num_clusters_x());
+
+  if (warp == 0 && lane == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(smem_u32(&ctl.full[st]), 1);
+      mbar_init(smem_u32(&ctl.empty[st]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&ctl.tfull[b]), 1);
+      mbar_init(smem_u32(&ctl.tempty[b]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish_pair();
+    tc_fence_before_sync();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = ctl.tmem_base;
+  volatile int* abort_flag = &ctl.abort;
+  unsigned int* dev_err = p.dev_err;
+  Walk<kMode> walk;
+  Unit u;
+
+  if (warp == 0) {
+    // ===================== TMA producer (both CTAs) =====================
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      while (ok && walk.next(p, pair, npairs, u)) {
+        const int m0 = u.m * kTile + 128 * rank, n0 = u.n * kTile + 128 * rank;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&ctl.empty[stage]), phase ^ 1u, abort_flag, dev_err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_leader = map_to_cta(smem_u32(&ctl.full[stage]), 0);
+          const uint32_t sa = smem_base + stage * kStageBytes, sb = sa + kOperandBytes;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), 2 * kStageBytes);
+          if constexpr (kMode == kGrad) {
+            if (u.which == 0) {  // dz rows, W's rows as k
+              tma_load_3d_pair(sa, &mapZ, full_leader, 0, m0, kb * (kBK / 64), pol);
+              tma_load_3d_pair(sb, &mapW, full_leader, 0, p.v0 + kb * kBK, n0 / 64, pol);
+            } else {  // dz columns, tokens as k
+              tma_load_3d_pair(sa, &mapZ, full_leader, 0, kb * kBK, m0 / 64, pol);
+              tma_load_3d_pair(sb, &mapX, full_leader, 0, kb * kBK, n0 / 64, pol);
+            }
+          } else {
+            tma_load_3d_pair(sa, &mapX, full_leader, 0, m0, kb * (kBK / 64), pol);
+            tma_load_3d_pair(sb, &mapW, full_leader, 0, p.v0 + n0, kb * (kBK / 64), pol);
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) {
+        // Let the copies already in flight land before the CTA exits.
+        int st = stage;
+        uint32_t ph = phase;
+        for (int i = 0; i < kStages && i < issued; ++i) {
+          if (--st < 0) {
+            st = kStages - 1;
+            ph ^= 1u;
+          }
+          volatile int local_abort = 0;
+          mbar_wait_cluster(smem_u32(&ctl.full[st]), ph, &local_abort, dev_err);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ===================== MMA issuer (leader only) =====================
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int i = 0;
+      bool ok = true;
+      for (; ok && walk.next(p, pair, npairs, u); ++i) {
+        const int buf = i & 1;
+        if (!mbar_wait_cluster(smem_u32(&ctl.tempty[buf]), ((i >> 1) & 1) ^ 1u, abort_flag, dev_err)) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + buf * 256;
+        // kGrad: B is N-major, A M-major where the tokens are the reduction
+        const uint32_t a_mn = kMode == kGrad && u.which == 1, b_mn = kMode == kGrad;
+        const uint32_t idesc = idesc_bf16_f32_ab(kTile, kTile, a_mn, b_mn);
+        const uint32_t a_lbo = a_mn ? 16384 : 16;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&ctl.full[stage]), phase, abort_flag, dev_err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sa = smem_base + stage * kStageBytes, sb = sa + kOperandBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint32_t k_major = (kk >> 2) * 16384 + (kk & 3) * 32, mn_major = kk * 2048;
+            const uint64_t adesc = smem_desc_sw128(sa + (a_mn ? mn_major : k_major), a_lbo, 1024);
+            const uint64_t bdesc = smem_desc_sw128(sb + (b_mn ? mn_major : k_major), b_mn ? 16384 : 16, 1024);
+            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kb != u.kb0 || kk != 0) ? 1u : 0u);
+          }
+          umma_commit_pair(smem_u32(&ctl.empty[stage]), 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(smem_u32(&ctl.tfull[buf]), 0x3);
+      }
+      // All MMAs issued by this thread are complete once `drain` flips.
+      umma_commit_pair(smem_u32(&ctl.drain), 0x1);
+      volatile int local_abort = 0;
+      mbar_wait_cluster(smem_u32(&ctl.drain), 0, &local_abort, dev_err);
+    }
+    __syncwarp();
+  } else {
+    // ===================== epilogue (both CTAs) =====================
+    // Warp w owns TMEM lanes 32 (w % 4) .. + 31, a row a lane, and half
+    // (w - 2) / 4 of the tile's columns.  It reads its 128 columns in one burst
+    // and hands the accumulator back before any math.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int c_first = half * 128;
+    const uint32_t tempty_leader0 = map_to_cta(smem_u32(&ctl.tempty[0]), 0);
+    const uint32_t tempty_leader1 = map_to_cta(smem_u32(&ctl.tempty[1]), 0);
+    uint8_t* box = smem + kStages * kStageBytes + (warp - 2) * (kMode == kStats ? kBoxStats : kBoxOut);
+    float run_max = -INFINITY, run_sum = 0.f;
+    Targets tg;
+    float row_a = 0.f, row_l = 0.f;
+    for (int i = 0; walk.next(p, pair, npairs, u); ++i) {
+      const int buf = i & 1;
+      const int warp_row0 = u.m * kTile + 128 * rank + q * 32;
+      const int row = warp_row0 + lane;
+      const int col0 = u.n * kTile + c_first;  // first column of this warp (of the piece, in kDz)
+      if constexpr (kMode == kStats) {
+        if (u.first) {
+          run_max = -INFINITY;
+          run_sum = 0.f;
+          tg.start(p, row, col0);
+        } else if (tg.id < col0) {  // the other half's targets
+          tg.start(p, row, col0);
+        }
+      } else if constexpr (kMode == kDz) {
+        tg.start(p, row, p.v0 + col0);
+        row_a = row < p.T ? p.row_a[row] : 0.f;
+        row_l = row < p.T ? p.row_l[row] : 0.f;
+      }
+      const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[buf]), (i >> 1) & 1, abort_flag, dev_err);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after_sync();
+      uint32_t acc[kBoxes][32];
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + c_first;
+#pragma unroll
+      for (int b = 0; b < kBoxes; ++b) tmem_ld_32cols(taddr + b * 32, acc[b]);
+      tmem_ld_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
+
+      if constexpr (kMode == kStats) {
+        if (col0 + 128 > p.V) {  // columns past the vocabulary
+#pragma unroll
+          for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + b * 32 + j >= p.V) acc[b][j] = 0xff800000u;
+        }
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b) {
+          const int end = col0 + b * 32 + 32;
+          if (__any_sync(0xffffffffu, tg.id < end)) {
+            // a lane writes its row and reads its targets back from it
+            // (16-byte chunk c of row r at c ^ (r % 8): free of bank conflicts)
+            uint8_t* mine = box + lane * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(mine + ((c ^ (lane & 7)) << 4)) =
+                  make_uint4(acc[b][4 * c], acc[b][4 * c + 1], acc[b][4 * c + 2], acc[b][4 * c + 3]);
+            while (tg.id < end) {
+              const int j = tg.id - (end - 32);
+              const float z = *reinterpret_cast<const float*>(mine + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4);
+              p.target[p.K == 0 ? static_cast<size_t>(row) : static_cast<size_t>(row) * p.K + tg.entry] = z;
+              tg.next(p);
+            }
+            __syncwarp();
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(acc[b][j]));
+        const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+        const float new_max = fmaxf(run_max, tile_max);
+        const float ref = new_max == -INFINITY ? 0.f : new_max;  // nothing but -inf so far
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_fast(fmaf(__uint_as_float(acc[b][j]), p.c, -ref));
+        run_sum = run_sum * exp2_fast(run_max - ref) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        run_max = new_max;
+        if (u.last && row < p.T)
+          p.part[static_cast<size_t>(2 * u.slot + half) * p.rows_padded + row] = make_float2(run_max, run_sum);
+      } else if constexpr (kMode == kDz) {
+        if (warp_row0 >= p.T) continue;
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b) {
+          const int cc = col0 + b * 32;
+          if (cc >= p.Vcp) break;
+          uint32_t packed[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float lo = row_a * exp2_fast(fmaf(__uint_as_float(acc[b][2 * j]), p.c, -row_l));
+            float hi = row_a * exp2_fast(fmaf(__uint_as_float(acc[b][2 * j + 1]), p.c, -row_l));
+            packed[j] = row_a == 0.f ? 0u : pack_bf16x2(lo, hi);  // whatever a row without a loss holds
+          }
+          if (cc + 32 > p.Vc) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (cc + 2 * j >= p.Vc) packed[j] = 0u;
+              else if (cc + 2 * j + 1 >= p.Vc) packed[j] &= 0xffffu;
+            }
+          }
+          bulk_wait_group_read0();
+          __syncwarp();
+          uint8_t* mine = box + lane * 64;
+          // 64B swizzle: 16-byte chunk c of row r lives at chunk c ^ ((r / 2) % 4)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<uint4*>(mine + ((v ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
+          const int end = p.v0 + cc + 32;
+          while (tg.id < end) {
+            const int j = tg.id - (end - 32);
+            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ ((lane >> 1) & 3)) << 4) + (j & 7) * 2) =
+                p.value[tg.at(p, row)];
+            tg.next(p);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&mapOut0, smem_u32(box), cc, warp_row0);
+            bulk_commit_group();
+          }
+        }
+      } else {
+        const int rows = u.which == 0 ? p.T : p.Vc;
+        if (warp_row0 >= rows) continue;
+        const int out_row = u.which == 0 ? warp_row0 : p.v0 + warp_row0;
+        const CUtensorMap* map = u.which == 0 ? &mapOut0 : &mapOut1;
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b) {
+          const int cc = col0 + b * 32;
+          if (cc >= p.D) break;
+          if (p.direct[u.which]) {
+            bulk_wait_group_read0();
+            __syncwarp();
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = pack_bf16x2(__uint_as_float(acc[b][8 * v + 2 * j]), __uint_as_float(acc[b][8 * v + 2 * j + 1]));
+              *reinterpret_cast<uint4*>(box + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(map, smem_u32(box), cc, out_row);
+              bulk_commit_group();
+            }
+            continue;
+          }
+          if (u.which == 0 && p.accumulate && row < p.T) {
+            const float4* before = reinterpret_cast<const float4*>(
+                p.dx_part + (static_cast<size_t>(u.split) * p.T + row) * p.D + cc);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const float4 f = before[v];
+              acc[b][4 * v] = __float_as_uint(__uint_as_float(acc[b][4 * v]) + f.x);
+              acc[b][4 * v + 1] = __float_as_uint(__uint_as_float(acc[b][4 * v + 1]) + f.y);
+              acc[b][4 * v + 2] = __float_as_uint(__uint_as_float(acc[b][4 * v + 2]) + f.z);
+              acc[b][4 * v + 3] = __float_as_uint(__uint_as_float(acc[b][4 * v + 3]) + f.w);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bulk_wait_group_read0();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(acc[b][16 * h + 4 * c], acc[b][16 * h + 4 * c + 1], acc[b][16 * h + 4 * c + 2],
+                             acc[b][16 * h + 4 * c + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_f32(map, smem_u32(box), cc + 16 * h, out_row, u.split);
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  // Both CTAs done with TMEM and with each other's barriers before freeing.
+  tc_fence_before_sync();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows: what the products need of them and what is left to do after them
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 8;
+constexpr int kMaxK = MOE_MAX_TEACHER;
+
+// (maximum, sum) pairs joined; an empty one is (-inf, 0).
+MOE_DEV void join(float& m, float& s, float m2, float s2) {
+  const float n = fmaxf(m, m2);
+  const float ref = n == -INFINITY ? 0.f : n;
+  s = s * exp2_fast(m - ref) + s2 * exp2_fast(m2 - ref);
+  m = n;
+}
+
+// The teacher's entries of one row, by one warp, kPerLane of each lane: entry
+// j = lane + 32 i.  Entries outside the vocabulary or of -inf are none.
+struct Teacher {
+  float p[kMaxK / 32];      // probability (0 where there is none)
+  float log_p[kMaxK / 32];
+  int id[kMaxK / 32];       // or -1
+  float mass;               // 1, or 0 for a row without entries
+};
+
+MOE_DEV float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+MOE_DEV float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, Teacher& out) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    out.id[i] = -1;
+    out.p[i] = -INFINITY;
+    const int j = lane + 32 * i;
+    if (32 * i < t.K && j < t.K) {
+      const size_t at = static_cast<size_t>(row) * t.K + j;
+      const long long id = load_index(t.ids, t.ids64, at);
+      const float l = t.logits_fp32 ? static_cast<const float*>(t.logits)[at]
+                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(t.logits)[at]);
+      if (id >= 0 && id < V) {
+        out.id[i] = static_cast<int>(id);
+        out.p[i] = l * inv_tau;
+      }
+    }
+    top = fmaxf(top, out.p[i]);
+  }
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    out.log_p[i] = out.p[i] - ref;
+    out.p[i] = expf(out.log_p[i]);
+    total += out.p[i];
+  }
+  total = warp_sum(total);
+  out.mass = total == 0.f ? 0.f : 1.f;  // NaN entries keep their row's mass
+  const float log_total = logf(total), inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    out.p[i] *= inv;
+    out.log_p[i] -= log_total;
+  }
+}
+
+// Sorts the row's keys (id << 8 | entry; none: all ones) in the warp's buffer.
+MOE_DEV void sort_keys(uint32_t* k, int K, const Teacher& t) {
+  const int lane = threadIdx.x & 31;
+  int n = 32;
+  while (n < K) n <<= 1;
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    const int j = lane + 32 * i;
+    if (j < n) k[j] = t.id[i] >= 0 ? (static_cast<uint32_t>(t.id[i]) << 8 | static_cast<uint32_t>(j)) : 0xffffffffu;
+  }
+  __syncwarp();
+  for (int size = 2; size <= n; size <<= 1)
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      for (int i = lane; i < n / 2; i += 32) {
+        const int a = 2 * i - (i & (d - 1)), b = a + d;
+        const uint32_t x = k[a], y = k[b];
+        if ((x > y) == ((a & size) == 0)) {
+          k[a] = y;
+          k[b] = x;
+        }
+      }
+      __syncwarp();
+    }
+}
+
+// Forward of distillation: the rows' sorted keys.
+__global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets t, int T, int V, float inv_tau,
+                                                                    uint32_t* keys, float* target) {
+  __shared__ uint32_t buf[kRowWarps][kMaxK];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kRowWarps + warp;
+  if (row >= T) return;
+  Teacher te;
+  read_teacher(t, row, V, inv_tau, te);
+  sort_keys(buf[warp], t.K, te);
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    const int j = lane + 32 * i;
+    if (j < t.K) {
+      keys[static_cast<size_t>(row) * t.K + j] = buf[warp][j];
+      if (te.id[i] < 0) target[static_cast<size_t>(row) * t.K + j] = 0.f;
+    }
+  }
+}
+
+// Joins a row's (maximum, sum) pairs and writes lse and the loss: 32 rows a
+// block, the pairs dealt to its warps.  With the sum s relative to 2^m,
+//   lse - z / temperature = ln 2 (log2 s - (c z - m)),
+// where c z - m is one fused product: for a target that outweighs the rest both
+// terms are next to 0, and the difference of the rounded lse and z, which would
+// be off by 2^-24 of their size, is never formed.
+__global__ void __launch_bounds__(32 * kRowWarps)
+    vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
+                        float c, float inv_tau, float* loss, float* lse) {
+  __shared__ float2 got[kRowWarps][33];
+  __shared__ float2 row[32];  // m, log2 s
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int at = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  if (at < T)
+    for (int i = warp; i < parts; i += kRowWarps) {
+      const float2 v = part[static_cast<size_t>(i) * rows_padded + at];
+      join(m, s, v.x, v.y);
+    }
+  got[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp == 0) {
+    for (int i = 1; i < kRowWarps; ++i) join(m, s, got[i][lane].x, got[i][lane].y);
+    const float log_s = log2f(s);
+    row[lane] = make_float2(m, log_s);
+    if (at < T) {
+      lse[at] = (m + log_s) * kLn2;
+      if (t.K == 0) {
+        const long long id = load_index(t.ids, t.ids64, at);
+        loss[at] = id >= 0 && id < V ? (log_s - fmaf(target[at], c, -m)) * kLn2 : 0.f;
+      }
+    }
+  }
+  if (t.K == 0) return;
+  __syncthreads();
+  for (int r = warp; r < 32; r += kRowWarps) {
+    const int i_row = blockIdx.x * 32 + r;
+    if (i_row >= T) break;
+    Teacher te;
+    read_teacher(t, i_row, V, inv_tau, te);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxK / 32; ++i) {
+      const int j = lane + 32 * i;
+      if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+        sum += te.p[i] * (te.log_p[i] +
+                          (row[r].y - fmaf(target[static_cast<size_t>(i_row) * t.K + j], c, -row[r].x)) * kLn2);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) loss[i_row] = sum;
+  }
+}
+
+// Backward of cross entropy: a and lse log2(e) of each row, and dz at its label,
+//   d_loss (q - 1) + d_lse q with q - 1 = expm1(-loss).
+__global__ void __launch_bounds__(256) vocab_ce_rows_kernel(const float* d_loss, const float* d_lse, const float* loss,
+                                                            const float* lse, VocabTargets t, int T, int V, float* row_a,
+                                                            float* row_l, uint16_t* value) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int row = blockIdx.x * 256 + threadIdx.x;
+  if (row >= T) return;
+  const long long id = load_index(t.ids, t.ids64, row);
+  const float d = id >= 0 && id < V ? d_loss[row] : 0.f;
+  const float e = d_lse ? d_lse[row] : 0.f;
+  row_a[row] = d + e;
+  row_l[row] = lse[row] * kLog2e;
+  const float v = d * expm1f(-loss[row]) + e * expf(-loss[row]);
+  value[row] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+}
+
+// Backward of distillation: the same, with the sorted keys and dz at each of them,
+//   d_loss / temperature (q - p),
+// p summed over the entries of one id.
+__global__ void __launch_bounds__(32 * kRowWarps)
+    vocab_distill_rows_kernel(const float* d_loss, const float* lse, const float* target, VocabTargets t, int T, int V,
+                              float inv_tau, float* row_a, float* row_l, uint32_t* keys, uint16_t* value) {
+  __shared__ uint32_t buf[kRowWarps][kMaxK];
+  __shared__ float prob[kRowWarps][kMaxK];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kRowWarps + warp;
+  if (row >= T) return;
+  Teacher te;
+  read_teacher(t, row, V, inv_tau, te);
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) prob[warp][lane + 32 * i] = te.p[i];
+  sort_keys(buf[warp], t.K, te);
+  const float d = te.mass == 0.f ? 0.f : d_loss[row] * inv_tau;
+  const float l = lse[row];
+  if (lane == 0) {
+    row_a[row] = d;
+    row_l[row] = l * kLog2e;
+  }
+  for (int i = lane; i < t.K; i += 32) {
+    const uint32_t key = buf[warp][i];
+    const size_t at = static_cast<size_t>(row) * t.K;
+    keys[at + i] = key;
+    if (key == 0xffffffffu) continue;
+    float p = 0.f;
+    int a = i;
+    while (a > 0 && (buf[warp][a - 1] >> 8) == (key >> 8)) --a;
+    for (; a < t.K && (buf[warp][a] >> 8) == (key >> 8); ++a) p += prob[warp][buf[warp][a] & 255u];
+    const float q = expf(target[at + (key & 255u)] * inv_tau - l);
+    value[at + i] = static_cast<uint16_t>(pack_bf16x2(d * (q - p), 0.f) & 0xffffu);
+  }
+}
+
+// bf16 sums of fp32 partials [n_parts, n] in their order, n a multiple of 8.
+__global__ void __launch_bounds__(256) vocab_sum_kernel(const float* part, int n_parts, size_t n, uint16_t* out) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  for (int s = 0; s < n_parts; ++s) {
+    const float4* f = reinterpret_cast<const float4*>(part + static_cast<size_t>(s) * n + i);
+    const float4 x = f[0], y = f[1];
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+  }
+  *reinterpret_cast<uint4*>(out + i) =
+      make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+std::mutex g_mu;
+struct Setup {
+  int pairs[3] = {0, 0, 0};  // co-resident CTA pairs of each mode
+};
+Setup g_setup[64];
+
+const void* kernel_of(int mode) {
+  return mode == kStats ? reinterpret_cast<const void*>(vocab_kernel<kStats>)
+         : mode == kDz  ? reinterpret_cast<const void*>(vocab_kernel<kDz>)
+                        : reinterpret_cast<const void*>(vocab_kernel<kGrad>);
+}
+
+cudaLaunchConfig_t pair_config(int mode, int pairs, cudaStream_t s, cudaLaunchAttribute (&attr)[2], bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes(mode);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cfg;
+}
+
+cudaError_t setup(Setup* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mu);
+  Setup& st = g_setup[dev];
+  if (st.pairs[kGrad] == 0) {
+    Setup got;
+    const int sms = current_device_sms();
+    if (sms < 2) return cudaErrorInvalidDevice;
+    for (int mode = 0; mode < 3; ++mode) {
+      e = cudaFuncSetAttribute(kernel_of(mode), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(mode));
+      if (e != cudaSuccess) return e;
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = pair_config(mode, sms / 2, nullptr, attr, false);
+      e = cudaOccupancyMaxActiveClusters(&got.pairs[mode], kernel_of(mode), &cfg);
+      if (e != cudaSuccess) return e;
+      if (got.pairs[mode] < 1) return cudaErrorInvalidConfiguration;
+    }
+    st = got;
+  }
+  *out = st;
+  return cudaSuccess;
+}
+
+template <int kMode>
+cudaError_t launch_vocab(int pairs, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& z,
+                         const CUtensorMap& out0, const CUtensorMap& out1, const VocabArgs& a, cudaStream_t s, bool pdl) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pair_config(kMode, pairs, s, attr, pdl);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_kernel<kMode>, x, w, z, out0, out1, a);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+size_t padded(size_t n) { return (n + 255) / 256 * 256; }
+
+// Takes regions of the workspace one after the other.
+struct Take {
+  uint8_t* base;
+  size_t off = 0;
+  template <typename Tp>
+  Tp* get(size_t n) {
+    Tp* p = reinterpret_cast<Tp*>(base + off);
+    off += padded(n * sizeof(Tp));
+    return p;
+  }
+};
+
+struct BackwardRegions {
+  float* row_a;
+  float* row_l;
+  uint32_t* keys;
+  uint16_t* value;
+  uint16_t* dz;
+  float* dx_part;
+  float* dw_part;
+};
+size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const BackwardPlan& b, BackwardRegions* r) {
+  Take t{base};
+  const size_t rows = static_cast<size_t>(T);
+  r->row_a = t.get<float>(rows);
+  r->row_l = t.get<float>(rows);
+  r->keys = t.get<uint32_t>(rows * K);
+  r->value = t.get<uint16_t>(rows * std::max(K, 1));
+  r->dz = t.get<uint16_t>(rows * b.piece);
+  r->dx_part = t.get<float>(b.pieces > 1 || b.splits_x > 1 ? rows * D * b.splits_x : 0);
+  r->dw_part = t.get<float>(b.splits_w > 1 ? static_cast<size_t>(V) * D * b.splits_w : 0);
+  return t.off;
+}
+
+cudaError_t launch_sum(const float* part, int n_parts, size_t n, uint16_t* out, cudaStream_t s) {
+  return launch_kernel(vocab_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0, s, true, part,
+                       n_parts, n, out);
+}
+
+}  // namespace
+
+size_t vocab_forward_workspace_bytes(int T, int D, int V, int K) {
+  const ForwardPlan f = forward_plan(T, V);
+  Take t{nullptr};
+  t.get<float2>(static_cast<size_t>(2) * f.runs * f.rows_padded);
+  t.get<uint32_t>(static_cast<size_t>(T) * K);
+  t.get<float>(K == 0 ? T : 0);
+  return t.off;
+}
+
+cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStream_t s) {
+  Setup st;
+  cudaError_t e = setup(&st);
+  if (e != cudaSuccess) return e;
+  const ForwardPlan f = forward_plan(a.T, a.V);
+  Take t{static_cast<uint8_t*>(workspace)};
+  VocabArgs v = {};
+  v.T = a.T;
+  v.V = v.Vc = v.Vcp = a.V;
+  v.D = a.D;
+  v.VocabWork::operator=(forward_work(f, a.D));
+  v.c = kLog2e / a.temperature;
+  v.K = a.targets.K;
+  v.labels = a.targets.ids;
+  v.labels64 = a.targets.ids64;
+  v.part = t.get<float2>(static_cast<size_t>(2) * f.runs * f.rows_padded);
+  v.rows_padded = f.rows_padded;
+  uint32_t* keys = t.get<uint32_t>(static_cast<size_t>(a.T) * v.K);
+  v.keys = keys;
+  v.target = v.K ? a.target : t.get<float>(a.T);
+  if ((e = device_error_address(&v.dev_err)) != cudaSuccess) return e;
+  CUtensorMap mx, mw;
+  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
+  if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
+  const float inv_tau = 1.f / a.temperature;
+  if (v.K) {
+    e = launch_kernel(vocab_keys_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false, a.targets,
+                      a.T, a.V, inv_tau, keys, v.target);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_vocab<kStats>(std::min(st.pairs[kStats], v.items), mx, mw, mx, mx, mx, v, s, v.K != 0);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(vocab_finish_kernel, dim3(ceil_div(a.T, 32)), dim3(32 * kRowWarps), 0, s, true,
+                       static_cast<const float2*>(v.part), 2 * f.runs, f.rows_padded, a.targets,
+                       static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau, a.loss, a.lse);
+}
+
+size_t vocab_backward_workspace_bytes(int T, int D, int V, int K) {
+  BackwardRegions r;
+  return backward_regions(nullptr, T, D, V, K, backward_plan(T, D, V), &r);
+}
+
+cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaStream_t s) {
+  Setup st;
+  cudaError_t e = setup(&st);
+  if (e != cudaSuccess) return e;
+  const int K = a.targets.K;
+  const BackwardPlan b = backward_plan(a.T, a.D, a.V);
+  BackwardRegions r;
+  backward_regions(static_cast<uint8_t*>(workspace), a.T, a.D, a.V, K, b, &r);
+  VocabArgs v = {};
+  v.T = a.T;
+  v.D = a.D;
+  v.V = a.V;
+  v.c = kLog2e / a.temperature;
+  v.K = K;
+  v.labels = a.targets.ids;
+  v.labels64 = a.targets.ids64;
+  v.keys = r.keys;
+  v.row_a = r.row_a;
+  v.row_l = r.row_l;
+  v.value = r.value;
+  const bool dx_direct = b.pieces == 1 && b.splits_x == 1, dw_direct = b.splits_w == 1;
+  v.direct[0] = dx_direct;
+  v.direct[1] = dw_direct;
+  v.dx_part = r.dx_part;
+  if ((e = device_error_address(&v.dev_err)) != cudaSuccess) return e;
+  CUtensorMap mx, mw, mz, mz_out, mdx, mdw;
+  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
+  if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
+  e = dx_direct ? tensor_map_2d(&mdx, a.dx, a.T, a.D, 32, 32)
+                : tensor_map_f32_3d(&mdx, r.dx_part, a.D, a.T, b.splits_x, 16, 32);
+  if (e != cudaSuccess) return e;
+  e = dw_direct ? tensor_map_2d(&mdw, a.dW, a.V, a.D, 32, 32)
+                : tensor_map_f32_3d(&mdw, r.dw_part, a.D, a.V, b.splits_w, 16, 32);
+  if (e != cudaSuccess) return e;
+  const float inv_tau = 1.f / a.temperature;
+  e = K ? launch_kernel(vocab_distill_rows_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
+                        a.d_loss, a.lse, a.target, a.targets, a.T, a.V, inv_tau, r.row_a, r.row_l, r.keys, r.value)
+        : launch_kernel(vocab_ce_rows_kernel, dim3(ceil_div(a.T, 256)), dim3(256), 0, s, false, a.d_loss, a.d_lse,
+                        a.loss, a.lse, a.targets, a.T, a.V, r.row_a, r.row_l, r.value);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < b.pieces; ++i) {
+    v.v0 = i * b.piece;
+    v.Vc = std::min(b.piece, a.V - v.v0);
+    v.Vcp = ceil_div(v.Vc, 64) * 64;
+    v.accumulate = i > 0;
+    if ((e = tensor_map_blocks(&mz, r.dz, a.T, v.Vcp, 2, 128)) != cudaSuccess) return e;
+    if ((e = tensor_map_2d(&mz_out, r.dz, a.T, v.Vcp, 32, 32)) != cudaSuccess) return e;
+    v.VocabWork::operator=(dz_work(b, a.D, v.Vc));
+    e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, true);
+    if (e != cudaSuccess) return e;
+    v.VocabWork::operator=(grad_work(b, a.T, v.Vc));
+    e = launch_vocab<kGrad>(std::min(st.pairs[kGrad], v.n_units[0] + v.n_units[1]), mx, mw, mz, mdx, mdw, v, s, true);
+    if (e != cudaSuccess) return e;
+  }
+  if (!dx_direct) {
+    e = launch_sum(r.dx_part, b.splits_x, static_cast<size_t>(a.T) * a.D, a.dx, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!dw_direct) e = launch_sum(r.dw_part, b.splits_w, static_cast<size_t>(a.V) * a.D, a.dW, s);
+  return e;
+}
+
+}  // namespace moe

@@ -1,0 +1,195 @@
+// How vocab_head.cu cuts its products into tiles, deals them to the CTA pairs
+// and cuts the vocabulary into pieces.  Index arithmetic only, for the host as
+// well.
+#pragma once
+
+#include <algorithm>
+
+#include "moe_device.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 256;      // rows and columns of a pair's tile
+constexpr int kBK = 128;        // k of a stage
+constexpr int kGroupRows = 64;  // row tiles that are worked on side by side
+
+enum Mode { kStats, kDz, kGrad };
+
+// What one launch has to do.
+struct VocabWork {
+  int nmt, nnt;    // kStats, kDz: row tiles, vocabulary tiles
+  int run, items;  // vocabulary tiles of one item; items in all
+  // k blocks of a tile; kGrad: of dx (0) and of dW (1), with the splits along
+  // them, the tiles and the units that this makes
+  int nkb[2];
+  int splits[2], n_units[2], tiles_m[2], tiles_n;
+};
+
+__host__ MOE_DEV int least(int a, int b) { return a < b ? a : b; }
+
+struct Unit {
+  int m, n;         // tile
+  int kb0, kb1;     // k blocks
+  int which;        // kGrad: 0 dx, 1 dW
+  int split;
+  int first, last;  // kStats: of its run
+  int slot;         // kStats: the run
+};
+
+// The units of pair `pair` in order; every role of both CTAs walks the same list.
+template <int kMode>
+struct Walk {
+  int it = -1;
+
+  __host__ MOE_DEV bool next(const VocabWork& p, int pair, int npairs, Unit& u) {
+    if constexpr (kMode == kGrad) {
+      ++it;
+      // The class of longer units first, dealt round robin; then the other's:
+      // as many as fit go to the pairs that got one long unit less.
+      const int big = p.nkb[0] / p.splits[0] >= p.nkb[1] / p.splits[1] ? 0 : 1, small = big ^ 1;
+      const int na = p.n_units[big], nb = p.n_units[small];
+      int i = it, which = big, idx;
+      const int len_a = pair < na ? (na - pair - 1) / npairs + 1 : 0;
+      if (i < len_a) {
+        idx = pair + i * npairs;
+      } else {
+        i -= len_a;
+        which = small;
+        const int r = na % npairs;
+        const int cost_a = (p.nkb[big] + p.splits[big] - 1) / p.splits[big];
+        const int cost_b = (p.nkb[small] + p.splits[small] - 1) / p.splits[small];
+        const int fill = r == 0 ? 0 : least(nb, (npairs - r) * (cost_a / cost_b));
+        int len_f = 0;
+        const int first = pair - r;
+        if (first >= 0 && first < fill) len_f = (fill - first - 1) / (npairs - r) + 1;
+        if (i < len_f) {
+          idx = first + i * (npairs - r);
+        } else {
+          idx = fill + (pair - r + npairs) % npairs + (i - len_f) * npairs;
+          if (idx >= nb) return false;
+        }
+      }
+      u.which = which;
+      u.n = idx % p.tiles_n;
+      idx /= p.tiles_n;
+      u.m = idx % p.tiles_m[which];
+      u.split = idx / p.tiles_m[which];
+      // splits differ by at most one block, and none is empty
+      u.kb0 = static_cast<int>(static_cast<long long>(p.nkb[which]) * u.split / p.splits[which]);
+      u.kb1 = static_cast<int>(static_cast<long long>(p.nkb[which]) * (u.split + 1) / p.splits[which]);
+      return true;
+    } else {
+      for (;;) {
+        ++it;
+        const int item = pair + it / p.run * npairs;
+        if (item >= p.items) return false;
+        const int sub = it % p.run;
+        // row tiles in groups; within a group all its rows before the next run of the vocabulary
+        const int runs = (p.nnt + p.run - 1) / p.run;
+        const int g = item / (kGroupRows * runs);
+        const int in_group = least(kGroupRows, p.nmt - g * kGroupRows);
+        const int r = item - g * kGroupRows * runs;
+        u.slot = r / in_group;
+        u.m = g * kGroupRows + r % in_group;
+        u.n = u.slot * p.run + sub;
+        if (u.n >= p.nnt) continue;
+        u.first = sub == 0;
+        u.last = sub == p.run - 1 || u.n == p.nnt - 1;
+        u.kb0 = 0;
+        u.kb1 = p.nkb[0];
+        u.which = 0;
+        u.split = 0;
+        return true;
+      }
+    }
+  }
+};
+
+inline int ceil_div(long a, long b) { return static_cast<int>((a + b - 1) / b); }
+
+// Vocabulary tiles of one item of the forward.  A longer run writes fewer
+// pairs; the items are dealt round robin, so it must leave each pair many.
+inline int run_of(int nmt, int nnt) {
+  const long tiles = static_cast<long>(nmt) * nnt;
+  return tiles >= 64 * 76 ? 4 : tiles >= 24 * 76 ? 2 : 1;
+}
+
+struct ForwardPlan {
+  int nmt, nnt, run, runs, rows_padded;
+};
+inline ForwardPlan forward_plan(int T, int V) {
+  ForwardPlan f;
+  f.nmt = ceil_div(T, kTile);
+  f.nnt = ceil_div(V, kTile);
+  f.run = run_of(f.nmt, f.nnt);
+  f.runs = ceil_div(f.nnt, f.run);
+  f.rows_padded = ceil_div(T, 32) * 32;
+  return f;
+}
+
+constexpr size_t kPieceBytes = static_cast<size_t>(1) << 31;  // most bytes of dz that one piece holds
+constexpr int kMinSplitBlocks = 4;                            // k blocks that a split has at least
+constexpr int kMaxSplits = 16;
+constexpr int kPlanPairs = 76;  // pairs that the splits are planned for (the plan decides the workspace)
+
+struct BackwardPlan {
+  int piece, pieces;       // vocabulary rows of a piece
+  int nmt, ndt;
+  int splits_x, splits_w;
+};
+inline BackwardPlan backward_plan(int T, int D, int V) {
+  BackwardPlan b;
+  const long most = static_cast<long>(kPieceBytes / 2 / static_cast<size_t>(std::max(T, 1))) / kTile * kTile;
+  b.pieces = ceil_div(V, std::max<long>(most, 8 * kTile));
+  b.piece = b.pieces == 1 ? ceil_div(V, 64) * 64 : ceil_div(ceil_div(V, b.pieces), kTile) * kTile;
+  b.pieces = ceil_div(V, b.piece);
+  b.nmt = ceil_div(T, kTile);
+  b.ndt = ceil_div(D, kTile);
+  // A tile whose reduction is longer than a pair's share of all work is split
+  // along it.
+  const long kx = ceil_div(b.piece, kBK), kw = ceil_div(T, kBK);
+  const long ux = static_cast<long>(b.nmt) * b.ndt, uw = static_cast<long>(ceil_div(b.piece, kTile)) * b.ndt;
+  const long share = std::max<long>(kMinSplitBlocks, (ux * kx + uw * kw + kPlanPairs - 1) / kPlanPairs);
+  b.splits_x = static_cast<int>(std::min<long>(kMaxSplits, (kx + share - 1) / share));
+  b.splits_w = b.pieces > 1 ? 1 : static_cast<int>(std::min<long>(kMaxSplits, (kw + share - 1) / share));
+  return b;
+}
+
+inline VocabWork forward_work(const ForwardPlan& f, int D) {
+  VocabWork w = {};
+  w.nmt = f.nmt;
+  w.nnt = f.nnt;
+  w.run = f.run;
+  w.items = f.nmt * f.runs;
+  w.nkb[0] = ceil_div(D, kBK);
+  return w;
+}
+
+// Both launches of a piece of Vc rows: the tiles of dz and the units of its products.
+inline VocabWork dz_work(const BackwardPlan& b, int D, int Vc) {
+  VocabWork w = {};
+  w.nmt = b.nmt;
+  w.nnt = ceil_div(Vc, kTile);
+  w.run = 1;
+  w.items = w.nmt * w.nnt;
+  w.nkb[0] = ceil_div(D, kBK);
+  return w;
+}
+inline VocabWork grad_work(const BackwardPlan& b, int T, int Vc) {
+  VocabWork w = {};
+  w.nkb[0] = ceil_div(Vc, kBK);
+  w.nkb[1] = ceil_div(T, kBK);
+  w.splits[0] = std::min(b.splits_x, w.nkb[0]);  // the last piece may be a short one
+  w.splits[1] = b.splits_w;
+  w.tiles_n = b.ndt;
+  w.tiles_m[0] = b.nmt;
+  w.tiles_m[1] = ceil_div(Vc, kTile);
+  for (int i = 0; i < 2; ++i) w.n_units[i] = w.tiles_m[i] * w.tiles_n * w.splits[i];
+  return w;
+}
+
+}  // namespace
+
+}  // namespace moe

@@ -1,5 +1,7 @@
 """PyTorch-facing entry points of the MoE SwiGLU FFN forward and backward passes,
-and of layer norm, Newton-Schulz orthogonalisation and the Muon step beside them.
+and of the operators beside them in a training step: layer norm, Newton-Schulz
+orthogonalisation and the Muon step, embedding, cross entropy and distillation
+over a vocabulary.
 
 These functions only allocate outputs with torch, check shapes/dtypes, and
 call the C ABI of libmoeffn.so on the current CUDA stream.  Tensor layouts:
@@ -628,6 +630,242 @@ def muon_step(weights, grads, momenta, lr, momentum=0.95, nesterov=True, weight_
         check(st, "moe_muon_step")
     for t, a in copies:
         t.copy_(a)
+
+
+_INDEX_TYPES = {torch.int32: N.MOE_I32, torch.int64: N.MOE_I64}
+
+
+def _index_type(t, name):
+    kind = _INDEX_TYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be torch.int32 or torch.int64, got {t.dtype}")
+    return kind
+
+
+def _float_type(t, name):
+    kind = _STREAM_TYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return kind
+
+
+def _matrix(t, name, of):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{of}]")
+    if not t.is_cuda or not t.is_contiguous():
+        _need(t, name, t.dtype)
+    return t.shape
+
+
+def _buffer(workspace, nbytes, dev, device, where):
+    """The caller's workspace, or one of nbytes."""
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    _ns_workspace(workspace, dev)
+    if workspace.numel() < max(nbytes, 1):
+        raise N.MoeError(N.MOE_ERR_WORKSPACE, where)
+    return workspace
+
+
+def embedding_forward(ids, table, scale=1.0, out_type=None):
+    """out [T, D] = scale * table[ids], in out_type (by default the table's
+    type): ids [T] int32 or int64, table [V, D] bf16 or fp32.  An id outside
+    [0, V) gives a row of zeros.  Any D up to 8192.  A tensor that does not
+    start on 16 bytes is copied first."""
+    ikind, tkind = _index_type(ids, "ids"), _float_type(table, "table")
+    V, D = _matrix(table, "table", "V, D")
+    dev = _current(table, "table")
+    if ids.dim() != 1:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [T]")
+    _like(ids, "ids", ids.dtype, ids.shape, dev)
+    out_type = table.dtype if out_type is None else out_type
+    okind = _STREAM_TYPES.get(out_type)
+    if okind is None:
+        raise ValueError(f"out_type must be torch.bfloat16 or torch.float32, got {out_type}")
+    pi, pt = ids.data_ptr(), table.data_ptr()
+    if (pi | pt) & 15:
+        return embedding_forward(_aligned(ids), _aligned(table), scale, out_type)
+    T = ids.shape[0]
+    out = _empty(T, D, dtype=out_type, device=table.device)
+    st = lib.moe_embedding_forward(pi, ikind, pt, tkind, scale, T, V, D, out.data_ptr(), okind, _stream_of(table))
+    if st:
+        check(st, "moe_embedding_forward")
+    return out
+
+
+def embedding_backward(d_out, ids, V, scale=1.0, add=None, workspace=None):
+    """Gradient of sum(d_out * embedding_forward(ids, table, scale)) in the
+    table: [V, D] fp32, (add +) scale * the sums of d_out's rows by id.  d_out
+    [T, D] bf16 or fp32; add [V, D] bf16: a gradient that reaches the table
+    elsewhere (a tied head's dW).  The sums run in a fixed order.  workspace: a
+    uint8 CUDA tensor of embedding_backward_workspace_size bytes.  A tensor that
+    does not start on 16 bytes is copied first."""
+    ikind, dkind = _index_type(ids, "ids"), _float_type(d_out, "d_out")
+    T, D = _matrix(d_out, "d_out", "T, D")
+    dev = _current(d_out, "d_out")
+    _like(ids, "ids", ids.dtype, (T,), dev)
+    if add is not None:
+        _like(add, "add", _BF16, (V, D), dev)
+    nbytes = embedding_backward_workspace_size(T, V, D)
+    ws = _buffer(workspace, nbytes, dev, d_out.device, "moe_embedding_backward")
+    pd, pi = d_out.data_ptr(), ids.data_ptr()
+    pa = None if add is None else add.data_ptr()
+    if (pd | pi | (pa or 0)) & 15:
+        return embedding_backward(_aligned(d_out), _aligned(ids), V, scale, _aligned(add), ws)
+    out = _empty(V, D, dtype=_F32, device=d_out.device)
+    st = lib.moe_embedding_backward(pd, dkind, pi, ikind, scale, pa, T, V, D, out.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), _stream_of(d_out))
+    if st:
+        check(st, "moe_embedding_backward")
+    return out
+
+
+def embedding_backward_workspace_size(T, V, D) -> int:
+    n = int(lib.moe_embedding_backward_scratch_size(T, V, D))
+    if n == 0 and T > 0:
+        raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, "moe_embedding_backward_scratch_size")
+    return n
+
+
+def vocab_workspace_size(T, D, V, n_teacher=0, backward=False) -> int:
+    """Bytes of workspace of cross_entropy_* (n_teacher = 0) and distill_*."""
+    name = "moe_vocab_backward_workspace_size" if backward else "moe_vocab_forward_workspace_size"
+    n = int(getattr(lib, name)(T, D, V, n_teacher))
+    if n == 0 and T > 0:
+        raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, name)
+    return n
+
+
+def _head(x, W):
+    """(T, D, V, device number) of the hidden states and the table."""
+    if x.dtype != _BF16:
+        raise ValueError(f"x must be torch.bfloat16, got {x.dtype}")
+    T, D = _matrix(x, "x", "T, D")
+    dev = _current(x, "x")
+    if W.dim() != 2:
+        raise ValueError(f"W has shape {tuple(W.shape)}, expected [V, {D}]")
+    V = W.shape[0]
+    _like(W, "W", _BF16, (V, D), dev)
+    return T, D, V, dev
+
+
+def _labels(labels, T, dev):
+    kind = _index_type(labels, "labels")
+    _like(labels, "labels", labels.dtype, (T,), dev)
+    return kind
+
+
+def cross_entropy_forward(x, W, labels, workspace=None):
+    """Softmax cross entropy of the logits z = x W^T, which are never stored:
+    dict(loss [T], lse [T]) fp32 with lse = log sum exp z and loss = lse -
+    z[label].  x [T, D] bf16 (D a multiple of 64), W [V, D] bf16 (an embedding
+    table's layout), labels [T] int32 or int64; a label outside [0, V) is a
+    token without a loss: 0.  workspace: a uint8 CUDA tensor of
+    vocab_workspace_size bytes.  A tensor that does not start on 16 bytes is
+    copied first."""
+    T, D, V, dev = _head(x, W)
+    kind = _labels(labels, T, dev)
+    nbytes = vocab_workspace_size(T, D, V)
+    ws = _buffer(workspace, nbytes, dev, x.device, "moe_cross_entropy_forward")
+    px, pw, pl = x.data_ptr(), W.data_ptr(), labels.data_ptr()
+    if (px | pw | pl) & 15:
+        return cross_entropy_forward(_aligned(x), _aligned(W), _aligned(labels), ws)
+    loss = _empty(T, dtype=_F32, device=x.device)
+    lse = _empty(T, dtype=_F32, device=x.device)
+    st = lib.moe_cross_entropy_forward(px, pw, pl, kind, T, D, V, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), _stream_of(x))
+    if st:
+        check(st, "moe_cross_entropy_forward")
+    return dict(loss=loss, lse=lse)
+
+
+def cross_entropy_backward(d_loss, x, W, labels, loss, lse, d_lse=None, workspace=None):
+    """Gradients of sum(d_loss * loss) (+ sum(d_lse * lse), a penalty on log Z)
+    for cross_entropy_forward: dict(dx [T, D], dW [V, D]) bf16.  d_loss, d_lse
+    [T] fp32; loss, lse: the forward's.  The logits are computed again, by
+    pieces of the vocabulary; their gradient is rounded to bf16 for the two
+    products.  workspace: a uint8 CUDA tensor of vocab_workspace_size(...,
+    backward=True) bytes.  A tensor that does not start on 16 bytes is copied
+    first."""
+    T, D, V, dev = _head(x, W)
+    kind = _labels(labels, T, dev)
+    for t, name in ((d_loss, "d_loss"), (loss, "loss"), (lse, "lse")):
+        _like(t, name, _F32, (T,), dev)
+    if d_lse is not None:
+        _like(d_lse, "d_lse", _F32, (T,), dev)
+    nbytes = vocab_workspace_size(T, D, V, backward=True)
+    ws = _buffer(workspace, nbytes, dev, x.device, "moe_cross_entropy_backward")
+    pd, px, pw, pl, po, ps = (t.data_ptr() for t in (d_loss, x, W, labels, loss, lse))
+    pe = None if d_lse is None else d_lse.data_ptr()
+    if (pd | px | pw | pl | po | ps | (pe or 0)) & 15:
+        return cross_entropy_backward(*(_aligned(t) for t in (d_loss, x, W, labels, loss, lse, d_lse)), ws)
+    dx, dW = torch.empty_like(x), torch.empty_like(W)
+    st = lib.moe_cross_entropy_backward(pd, pe, px, pw, pl, kind, po, ps, T, D, V, dx.data_ptr(), dW.data_ptr(),
+                                        ws.data_ptr(), ws.numel(), _stream_of(x))
+    if st:
+        check(st, "moe_cross_entropy_backward")
+    return dict(dx=dx, dW=dW)
+
+
+def _teacher(ids, logits, temperature, T, dev):
+    ikind, lkind = _index_type(ids, "teacher_ids"), _float_type(logits, "teacher_logits")
+    if ids.dim() != 2:
+        raise ValueError(f"teacher_ids has shape {tuple(ids.shape)}, expected [{T}, K]")
+    K = ids.shape[1]
+    _like(ids, "teacher_ids", ids.dtype, (T, K), dev)
+    _like(logits, "teacher_logits", logits.dtype, (T, K), dev)
+    return N.MoeTeacher(None, None, ikind, lkind, K, temperature)
+
+
+def distill_forward(x, W, teacher_ids, teacher_logits, temperature=1.0, workspace=None):
+    """Distillation of z = x W^T, which is never stored, from a teacher's top
+    logits: with p the softmax of a token's teacher_logits / temperature among
+    its K entries, dict(loss [T], lse [T], logits [T, K]) fp32, where lse = log
+    sum exp(z / temperature), logits = z at the ids and loss = sum p (log p -
+    logits / temperature + lse).  teacher_ids [T, K] int32 or int64 (an id
+    outside [0, V) is no entry), teacher_logits [T, K] bf16 or fp32 (-inf is no
+    entry), K up to 256; a token without entries has loss 0.  x, W, workspace as
+    in cross_entropy_forward (vocab_workspace_size with n_teacher=K)."""
+    T, D, V, dev = _head(x, W)
+    te = _teacher(teacher_ids, teacher_logits, temperature, T, dev)
+    nbytes = vocab_workspace_size(T, D, V, te.K)
+    ws = _buffer(workspace, nbytes, dev, x.device, "moe_distill_forward")
+    te.ids, te.logits = teacher_ids.data_ptr(), teacher_logits.data_ptr()
+    px, pw = x.data_ptr(), W.data_ptr()
+    if (px | pw | (te.ids or 0) | (te.logits or 0)) & 15:
+        return distill_forward(*(_aligned(t) for t in (x, W, teacher_ids, teacher_logits)), temperature, ws)
+    loss = _empty(T, dtype=_F32, device=x.device)
+    lse = _empty(T, dtype=_F32, device=x.device)
+    logits = _empty(T, te.K, dtype=_F32, device=x.device)
+    st = lib.moe_distill_forward(px, pw, te, T, D, V, loss.data_ptr(), lse.data_ptr(), logits.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _stream_of(x))
+    if st:
+        check(st, "moe_distill_forward")
+    return dict(loss=loss, lse=lse, logits=logits)
+
+
+def distill_backward(d_loss, x, W, teacher_ids, teacher_logits, lse, logits, temperature=1.0, workspace=None):
+    """Gradients of sum(d_loss * loss) for distill_forward: dict(dx [T, D], dW
+    [V, D]) bf16.  d_loss [T] fp32; lse, logits: the forward's; the rest as
+    there and in cross_entropy_backward."""
+    T, D, V, dev = _head(x, W)
+    te = _teacher(teacher_ids, teacher_logits, temperature, T, dev)
+    for t, name in ((d_loss, "d_loss"), (lse, "lse")):
+        _like(t, name, _F32, (T,), dev)
+    _like(logits, "logits", _F32, (T, te.K), dev)
+    nbytes = vocab_workspace_size(T, D, V, te.K, backward=True)
+    ws = _buffer(workspace, nbytes, dev, x.device, "moe_distill_backward")
+    te.ids, te.logits = teacher_ids.data_ptr(), teacher_logits.data_ptr()
+    pd, px, pw, ps, pz = (t.data_ptr() for t in (d_loss, x, W, lse, logits))
+    if (pd | px | pw | ps | pz | (te.ids or 0) | (te.logits or 0)) & 15:
+        return distill_backward(*(_aligned(t) for t in (d_loss, x, W, teacher_ids, teacher_logits, lse, logits)),
+                                temperature, ws)
+    dx, dW = torch.empty_like(x), torch.empty_like(W)
+    st = lib.moe_distill_backward(pd, px, pw, te, ps, pz, T, D, V, dx.data_ptr(), dW.data_ptr(), ws.data_ptr(),
+                                  ws.numel(), _stream_of(x))
+    if st:
+        check(st, "moe_distill_backward")
+    return dict(dx=dx, dW=dW)
 
 
 def device_error() -> int:

@@ -1,7 +1,9 @@
 /*
  * moe_ffn.h -- C ABI of the GB300 (sm_103a) mixture-of-experts SwiGLU FFN
  * forward and backward passes, and of the operators around the layer in a
- * training step: layer norm, Newton-Schulz orthogonalisation, Muon step.
+ * training step: layer norm, Newton-Schulz orthogonalisation, Muon step, and
+ * the two ends of a language model: embedding, and the vocabulary product under
+ * a cross entropy or a distillation loss.
  *
  * The layer (per token t of x [T, D]):
  *   logits = x[t] . Wg (+ router_bias)                 router GEMM
@@ -357,6 +359,97 @@ typedef struct {
 moe_status moe_muon_step(const moe_matrix_stack* stacks, int32_t n_stacks, moe_dtype grad_type,
                          moe_dtype weight_type, const moe_muon_params* params, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* ---- The ends of a language model: embedding, loss over the vocabulary ---- */
+
+#define MOE_MAX_VOCAB (1 << 22) /* rows of a table */
+#define MOE_MAX_TEACHER 256     /* teacher entries a token */
+
+typedef enum { MOE_I32 = 0, MOE_I64 = 1 } moe_index_type;
+
+/* Embedding lookup:  out[t] = scale * table[ids[t]], rounded once.
+ *   ids [T] of type ids_type; an id outside [0, V) gives a row of zeros;
+ *   table [V, D] of type table_type; out [T, D] of type out_type.
+ * 1 <= D <= 8192, any D; 1 <= V <= MOE_MAX_VOCAB; 0 <= T <= 2^24; scale finite. */
+moe_status moe_embedding_forward(const void* ids, moe_index_type ids_type, const void* table,
+                                 moe_dtype table_type, float scale, int32_t T, int32_t V, int32_t D,
+                                 void* out, moe_dtype out_type, void* stream);
+
+/* Bytes of scratch moe_embedding_backward needs (0 for a bad shape). */
+size_t moe_embedding_backward_scratch_size(int32_t T, int32_t V, int32_t D);
+
+/* Gradient of sum(d_out * out) for the forward above:
+ *   d_table[v] = (add[v] +) scale * sum over t with ids[t] = v of d_out[t]
+ *   d_out [T, D] of type d_type; add [V, D] bf16 or NULL: a gradient that
+ *   reaches the table elsewhere (the dW of the calls below, where the table is
+ *   the head's too); d_table [V, D] fp32.  The tokens are sorted, and the sums
+ *   run in fp32 in a fixed order (the same bits every time). */
+moe_status moe_embedding_backward(const void* d_out, moe_dtype d_type, const void* ids,
+                                  moe_index_type ids_type, float scale, const void* add, int32_t T,
+                                  int32_t V, int32_t D, float* d_table, void* scratch,
+                                  size_t scratch_bytes, void* stream);
+
+/* Limits of the four calls below: 1 <= T <= 2^24 (T = 0 does nothing, or gives
+ * zero weight gradients); D a multiple of 64 in [64, 8192]; 1 <= V <= MOE_MAX_VOCAB.
+ * x [T, D] and the table W [V, D] are bf16, z = x W^T has fp32 sums and never
+ * reaches memory.  Workspaces start on 256 bytes and hold nothing between
+ * calls; the size functions return 0 for a bad shape.  n_teacher is 0 for the
+ * cross entropy. */
+size_t moe_vocab_forward_workspace_size(int32_t T, int32_t D, int32_t V, int32_t n_teacher);
+size_t moe_vocab_backward_workspace_size(int32_t T, int32_t D, int32_t V, int32_t n_teacher);
+
+/* Softmax cross entropy over the vocabulary:
+ *   lse[t] = log sum_v exp(z[t, v]),  loss[t] = lse[t] - z[t, labels[t]]
+ * A label outside [0, V) is a token without a loss: loss 0 (lse as above). */
+moe_status moe_cross_entropy_forward(const void* x, const void* W, const void* labels,
+                                     moe_index_type labels_type, int32_t T, int32_t D, int32_t V,
+                                     float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Gradients of sum(d_loss * loss) (+ sum(d_lse * lse)) for the call above:
+ *   dz[t, v] = d_loss[t] (exp(z[t, v] - lse[t]) - [v = labels[t]])
+ *              + d_lse[t] exp(z[t, v] - lse[t])
+ *   dx = dz W [T, D] bf16,  dW = dz^T x [V, D] bf16
+ * d_loss [T] fp32 (not read where a token has no loss); d_lse [T] fp32 or
+ * NULL; loss and lse: the forward's.  z is computed again, piece by piece of
+ * the vocabulary; dz is rounded to bf16 for its two products, whose sums are
+ * fp32. */
+moe_status moe_cross_entropy_backward(const float* d_loss, const float* d_lse, const void* x,
+                                      const void* W, const void* labels, moe_index_type labels_type,
+                                      const float* loss, const float* lse, int32_t T, int32_t D,
+                                      int32_t V, void* dx, void* dW, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* A teacher's top logits for each token. */
+typedef struct {
+  const void* ids;       /* [T, K] of type ids_type; outside [0, V): no entry */
+  const void* logits;    /* [T, K] of type logits_type; -inf: no entry */
+  moe_index_type ids_type;
+  moe_dtype logits_type;
+  int32_t K;             /* 1 <= K <= MOE_MAX_TEACHER */
+  float temperature;     /* > 0, finite */
+} moe_teacher;
+
+/* Distillation from the teacher's entries, with p = softmax of its logits over
+ * temperature among the token's entries:
+ *   lse[t] = log sum_v exp(z[t, v] / temperature)
+ *   loss[t] = sum_j p[t, j] (log p[t, j] - z[t, ids[t, j]] / temperature + lse[t])
+ * loss, lse [T] fp32; logits [T, K] fp32: z at the ids (0 where there is no
+ * entry for the id's sake).  A token without entries has loss 0; an id that
+ * comes twice counts twice. */
+moe_status moe_distill_forward(const void* x, const void* W, const moe_teacher* teacher, int32_t T,
+                               int32_t D, int32_t V, float* loss, float* lse, float* logits,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(d_loss * loss) for the call above, as in
+ * moe_cross_entropy_backward:
+ *   dz[t, v] = d_loss[t] / temperature (exp(z[t, v] / temperature - lse[t])
+ *              - sum over j with ids[t, j] = v of p[t, j])
+ * lse, logits: the forward's. */
+moe_status moe_distill_backward(const float* d_loss, const void* x, const void* W,
+                                const moe_teacher* teacher, const float* lse, const float* logits,
+                                int32_t T, int32_t D, int32_t V, void* dx, void* dW, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* ---- Allocation-free variant ---- */
 
