@@ -5,12 +5,15 @@
 // 16-byte pieces each.
 //
 // The gradient sorts the tokens by id (stable radix sort, most of 10 bits a
-// pass, so two passes up to a million ids), then a warp a few rows of the table:
-// it finds its rows' tokens in the sorted list by a 33-way search, adds their
-// gradients in token order in fp32 and writes the row, so that every row is
-// written once, in order, and no sum depends on timing.  Frequent tokens would
-// leave one warp with thousands of rows to add: aligned runs of `chunk` sorted
-// tokens with one id are summed beforehand by warps of their own.
+// pass, so two passes up to a million ids).  Then a warp takes 8 sorted tokens
+// and writes the rows of the table whose tokens begin there, sums in token order
+// in fp32: no sum depends on timing.  Rows without tokens (zeros, or `add`) are
+// most of a large table: all rows are filled with those first, by blocks that
+// the sorting kernels carry along, since a sort keeps few SMs busy and a fill
+// is bound by memory; the rows with tokens are then written a second time.
+// Frequent tokens would leave one warp with thousands of rows to add: aligned
+// runs of `chunk` sorted tokens with one id are summed by warps of their own
+// beforehand, and a long run is then added by a whole block.
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -113,7 +116,8 @@ cudaError_t launch_fwd(const EmbeddingArgs& a, cudaStream_t s) {
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1024;
-constexpr int kMaxPasses = 3;
+constexpr int kFillThreads = 1024;  // of an SM, that fill beside the others
+constexpr int kHeld = 4;  // rounds of 32 tokens that a warp keeps in registers
 
 struct SortPlan {
   int passes, bits;       // of a pass
@@ -136,6 +140,15 @@ SortPlan sort_plan(int T, int V) {
   return p;
 }
 
+// The part of the table that one of the launches fills.
+struct Fill {
+  float* out;
+  const uint16_t* add;  // bf16 or nullptr
+  size_t n;             // elements
+  int first;            // block that is the first to fill
+  int part, parts;
+};
+
 struct SortArgs {
   const void* ids;
   int ids64;
@@ -147,7 +160,40 @@ struct SortArgs {
   uint32_t* key_out;
   uint32_t* tok_out;
   int pass, passes;
+  Fill fill;
 };
+
+MOE_DEV void fill_rows(const Fill& f) {
+  constexpr int kEach = 4;  // pieces of 8 that a thread has in flight
+  const size_t pieces = f.n / 8;
+  const size_t p0 = pieces * f.part / f.parts, p1 = pieces * (f.part + 1) / f.parts;
+  const size_t block = blockIdx.x - f.first, blocks = gridDim.x - f.first;
+  const size_t step = static_cast<size_t>(blockDim.x) * kEach;
+  for (size_t p = p0 + block * step; p < p1; p += blocks * step) {
+    Piece<8, false> v[kEach] = {};
+    if (f.add) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const size_t q = p + static_cast<size_t>(i) * blockDim.x + threadIdx.x;
+        v[i].load(f.add, (q < p1 ? q : p0) * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const size_t q = p + static_cast<size_t>(i) * blockDim.x + threadIdx.x;
+      if (q < p1) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[i][e];
+        store_vec<8, true>(f.out, q * 8, o);
+      }
+    }
+  }
+  if (f.part + 1 == f.parts && block == 0) {
+    const size_t i = pieces * 8 + threadIdx.x;
+    if (i < f.n) f.out[i] = f.add ? __uint_as_float(static_cast<uint32_t>(f.add[i]) << 16) : 0.f;
+  }
+}
 
 MOE_DEV uint32_t sort_key(const SortArgs& a, int i) {
   if (a.key_in) return a.key_in[i];
@@ -159,10 +205,15 @@ MOE_DEV uint32_t sort_key(const SortArgs& a, int i) {
 __global__ void __launch_bounds__(kSortThreads) embedding_hist_kernel(SortArgs a) {
   __shared__ uint32_t h[kMaxBins];
   griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    fill_rows(a.fill);
+    return;
+  }
   const int bins = 1 << a.bits;
   for (int d = threadIdx.x; d < bins; d += kSortThreads) h[d] = 0;
   __syncthreads();
   const int i0 = blockIdx.x * a.block, i1 = min(a.T, i0 + a.block);
+#pragma unroll 4
   for (int i = i0 + threadIdx.x; i < i1; i += kSortThreads) atomicAdd(&h[sort_key(a, i) & (bins - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += kSortThreads) {
@@ -178,8 +229,22 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
   __shared__ uint32_t warp_total[kSortWarps];
   griddep_launch_dependents();
   griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    fill_rows(a.fill);
+    return;
+  }
   const int bins = 1 << a.bits, shift = a.pass * a.bits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_warp = a.block / kSortWarps;
+  const int w0 = blockIdx.x * a.block + warp * per_warp, w1 = min(a.T, w0 + per_warp);
+  // the first kHeld rounds' tokens stay in registers
+  uint32_t key[kHeld], tok[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = w0 + 32 * k + lane;
+    key[k] = i < w1 ? sort_key(a, i) : 0u;
+    tok[k] = i < w1 && a.key_in ? a.tok_in[i] : static_cast<uint32_t>(i);
+  }
   for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads)
     reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
   // where the block's tokens of each digit begin: all smaller digits, then the
@@ -216,14 +281,20 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     base[threadIdx.x * kPer + k] = run + before[k];
     run += total[k];
   }
-  const int i0 = blockIdx.x * a.block, per_warp = a.block / kSortWarps;
-  const int w0 = i0 + warp * per_warp, w1 = min(a.T, w0 + per_warp);
-  for (int r = w0; r < w1; r += 32) {
-    const bool there = r + lane < w1;
-    const uint32_t d = there ? (sort_key(a, r + lane) >> shift) & (bins - 1) : 0xffffffffu;
+  const int rounds = (max(w1 - w0, 0) + 31) / 32;
+  auto count = [&](int r, uint32_t k) {
+    const bool there = w0 + 32 * r + lane < w1;
+    const uint32_t d = there ? (k >> shift) & (bins - 1) : 0xffffffffu;
     const uint32_t peers = __match_any_sync(0xffffffffu, d);
     if (there && __ffs(peers) - 1 == lane) cnt[warp][d] += static_cast<uint16_t>(__popc(peers));
     __syncwarp();
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r < rounds) count(r, key[r]);
+  for (int r = kHeld; r < rounds; ++r) {
+    const int i = w0 + 32 * r + lane;
+    count(r, i < w1 ? sort_key(a, i) : 0u);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += kSortThreads) {
@@ -236,23 +307,29 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     }
   }
   __syncthreads();
-  for (int r = w0; r < w1; r += 32) {
-    const bool there = r + lane < w1;
-    const uint32_t key = there ? sort_key(a, r + lane) : 0;
-    const uint32_t d = there ? (key >> shift) & (bins - 1) : 0xffffffffu;
+  auto place = [&](int r, uint32_t k, uint32_t t) {
+    const bool there = w0 + 32 * r + lane < w1;
+    const uint32_t d = there ? (k >> shift) & (bins - 1) : 0xffffffffu;
     const uint32_t peers = __match_any_sync(0xffffffffu, d);
     if (there) {
       const uint32_t pos = base[d] + cnt[warp][d] + __popc(peers & ((1u << lane) - 1));
-      a.key_out[pos] = key;
-      a.tok_out[pos] = a.key_in ? a.tok_in[r + lane] : static_cast<uint32_t>(r + lane);
+      a.key_out[pos] = k;
+      a.tok_out[pos] = t;
       if (a.pass + 1 < a.passes)
         atomicAdd(&a.hist[(static_cast<size_t>(a.pass + 1) * a.blocks + pos / a.block) * bins +
-                          ((key >> (shift + a.bits)) & (bins - 1))],
+                          ((k >> (shift + a.bits)) & (bins - 1))],
                   1u);
     }
     __syncwarp();
     if (there && __ffs(peers) - 1 == lane) cnt[warp][d] += static_cast<uint16_t>(__popc(peers));
     __syncwarp();
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r < rounds) place(r, key[r], tok[r]);
+  for (int r = kHeld; r < rounds; ++r) {
+    const int i = w0 + 32 * r + lane;
+    place(r, i < w1 ? sort_key(a, i) : 0u, i < w1 && a.key_in ? a.tok_in[i] : static_cast<uint32_t>(i));
   }
 }
 
@@ -261,144 +338,230 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
 // ---------------------------------------------------------------------------
 struct SumArgs {
   const void* d_out;
-  const void* add;         // bf16
+  const void* add;         // bf16 or nullptr
   const uint32_t* key;     // sorted
   const uint32_t* tok;
   float* part;             // [chunks, D]
   float* d_table;
   float scale;
   int T, V, D, chunk, chunks;
+  Fill fill;
 };
 
-constexpr int kVecs = 4;     // pieces of a lane
-constexpr int kRowsPerWarp = 4;
+constexpr int kWindow = 8;     // sorted tokens of a warp
+constexpr int kSumWarps = 8;
+constexpr int kLong = 32;      // tokens past its window that a warp adds alone
 
-// acc += rows index(0) .. index(n - 1) of `src`, in that order; kAhead of them
-// in flight.
-template <int VEC, bool kF32, typename Index>
-MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index index, float (&acc)[kVecs][VEC]) {
-  constexpr int kAhead = kF32 ? 2 : 4;
-#pragma unroll 1
-  for (int j = 0; j < n; j += kAhead) {
-    Piece<VEC, kF32> v[kAhead][kVecs];
+// A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
+template <int VEC>
+struct Shape {
+  static constexpr int kVecs = VEC == 8 ? 4 : 16;
+  static constexpr int kAhead = VEC == 8 ? 4 : 2;
+  static constexpr int kColumns = 32 * kVecs * VEC;
+};
+
+// acc += R rows of `src`; lanes past the last column read another's piece
+// (a load under a condition would be waited for on the spot).
+template <int VEC, bool kF32, int R, typename Index>
+MOE_DEV void add_step(const void* src, int D, int v0, int nv, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
+  Piece<VEC, kF32> v[R][Shape<VEC>::kVecs];
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r) {
-      const size_t at = static_cast<size_t>(index(min(j + r, n - 1))) * D;
+  for (int r = 0; r < R; ++r) {
+    const size_t at = static_cast<size_t>(row(r)) * D;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (j + r < n && v0 + 32 * i < nv) v[r][i].load(src, at + static_cast<size_t>(v0 + 32 * i) * VEC);
-        else v[r][i] = {};  // (registers that are written under a condition alone stay live around the loop)
-    }
-#pragma unroll
-    for (int r = 0; r < kAhead; ++r)
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[i][e] += v[r][i][e];
+    for (int i = 0; i < Shape<VEC>::kVecs; ++i) v[r][i].load(src, at + static_cast<size_t>(min(v0 + 32 * i, nv - 1)) * VEC);
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[i][e] += v[r][i][e];
+}
+
+// acc += rows row(0) .. row(n - 1), in that order.
+template <int VEC, bool kF32, typename Index>
+MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
+  constexpr int R = kF32 && VEC == 8 ? 2 : Shape<VEC>::kAhead;
+  int j = 0;
+#pragma unroll 1
+  for (; j + R <= n; j += R) add_step<VEC, kF32, R>(src, D, v0, nv, [&](int r) { return row(j + r); }, acc);
+#pragma unroll 1
+  for (; j < n; ++j) add_step<VEC, kF32, 1>(src, D, v0, nv, [&](int) { return row(j); }, acc);
 }
 
 // Aligned runs of `chunk` sorted tokens with one id, a warp each.
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(256) embedding_chunk_kernel(SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps) embedding_chunk_kernel(SumArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) >= a.fill.first) {
+    fill_rows(a.fill);
+    return;
+  }
+  const int c = blockIdx.x * kSumWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (c >= a.chunks) return;
   const size_t p0 = static_cast<size_t>(c) * a.chunk;
   const uint32_t k = a.key[p0];
   if (k != a.key[p0 + a.chunk - 1] || k >= static_cast<uint32_t>(a.V)) return;
   const int nv = a.D / VEC;
 #pragma unroll 1
-  for (int v0 = lane; v0 < nv; v0 += 32 * kVecs) {
-    float acc[kVecs][VEC] = {};
+  for (int v0 = lane; v0 - lane < nv; v0 += 32 * Shape<VEC>::kVecs) {
+    float acc[Shape<VEC>::kVecs][VEC] = {};
     add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, a.chunk, [&](int j) { return a.tok[p0 + j]; }, acc);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < Shape<VEC>::kVecs; ++i)
       if (v0 + 32 * i < nv)
         store_vec<VEC, true>(a.part, static_cast<size_t>(c) * a.D + static_cast<size_t>(v0 + 32 * i) * VEC, acc[i]);
   }
 }
 
-// First sorted position whose key is at least k (whole warp).
-MOE_DEV int lower_bound(const uint32_t* key, int T, uint32_t k) {
+// First sorted position from lo on whose key is more than k (whole warp).
+MOE_DEV int end_of(const uint32_t* key, int lo, int T, uint32_t k) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = T;  // the answer lies in [lo, hi]
+  int hi = T;  // the answer lies in [lo, hi]
   while (hi - lo > 32) {
     const int at = lo + static_cast<int>(static_cast<long long>(hi - lo) * (lane + 1) / 33);
-    const uint32_t less = __ballot_sync(0xffffffffu, key[at] < k);
-    const int n = __popc(less);  // the probes ascend, so the first n are less
+    const uint32_t le = __ballot_sync(0xffffffffu, key[at] <= k);
+    const int n = __popc(le);  // the probes ascend, so the first n are at most k
     const int left = n == 0 ? lo : __shfl_sync(0xffffffffu, at, n - 1) + 1;
     const int right = n == 32 ? hi : __shfl_sync(0xffffffffu, at, n & 31);
     lo = left;
     hi = right;
   }
-  const uint32_t less = __ballot_sync(0xffffffffu, lo + lane < hi && key[lo + lane] < k);
-  return lo + __popc(less);
+  return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && key[lo + lane] <= k));
+}
+
+template <int VEC>
+MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float (&acc)[Shape<VEC>::kVecs][VEC]) {
+  const size_t dst = static_cast<size_t>(v) * a.D;
+#pragma unroll
+  for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+    if (v0 + 32 * i < nv) {
+      const size_t at = dst + static_cast<size_t>(v0 + 32 * i) * VEC;
+      float o[VEC];
+      Piece<VEC, false> before = {};
+      if (a.add) before.load(a.add, at);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = a.add ? fmaf(a.scale, acc[i][e], before[e]) : a.scale * acc[i][e];
+      store_vec<VEC, true>(a.d_table, at, o);
+    }
 }
 
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(256) embedding_rows_kernel(SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps) embedding_rows_kernel(SumArgs a) {
+  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns;
+  __shared__ float red[kSumWarps][kColumns];
+  __shared__ int long_start[kSumWarps], long_end[kSumWarps];
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long v_first = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRowsPerWarp;
-  if (v_first >= a.V) return;
-  const int v_end = static_cast<int>(min(static_cast<long long>(a.V), v_first + kRowsPerWarp));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p0 = (blockIdx.x * kSumWarps + warp) * kWindow;
   const int nv = a.D / VEC;
-  int start = lower_bound(a.key, a.T, static_cast<uint32_t>(v_first));
+  const uint32_t none = static_cast<uint32_t>(a.V);  // tokens without a row, sorted to the end, and what lies past it
+  const int at = p0 - 1 + lane;                      // lane 0 sees the token before the window
+  const uint32_t k = at < 0 ? 0xffffffffu : at < a.T ? a.key[at] : none;
+  const uint32_t my_tok = a.tok[min(max(at, 0), a.T - 1)];
+  const uint32_t k_before = __shfl_up_sync(0xffffffffu, k, 1);
+  const uint32_t begins = __ballot_sync(0xffffffffu, lane >= 1 && lane <= kWindow && k != k_before && k < none) >> 1;
+  int len_past = 0;  // of the last run, behind the window
+  if (begins) {
+    const uint32_t last = __shfl_sync(0xffffffffu, k, kWindow);
+    if (last < none && __shfl_sync(0xffffffffu, k, kWindow + 1) == last) {
+      const int begin = p0 + 31 - __clz(begins);
+      const int end = end_of(a.key, p0 + kWindow, a.T, last);
+      len_past = end - (p0 + kWindow);
+      if (lane == 0) long_start[warp] = begin, long_end[warp] = end;
+    }
+  }
+  const bool is_long = len_past > kLong;
+  if (lane == 0 && !is_long) long_start[warp] = -1;
+  if (begins) {
+    const int first = __ffs(begins) - 1;
+    // past the window, a run too long for this warp, or the tokens without a row
+    const uint32_t rows = __ballot_sync(0xffffffffu, lane >= 1 && lane <= kWindow && k < none) >> 1;
+    const int stop = is_long ? 31 - __clz(begins) : 32 - __clz(rows);
 #pragma unroll 1
-  for (int v = static_cast<int>(v_first); v < v_end; ++v) {
-    const bool there = start + lane < a.T;
-    const uint32_t mine = there ? a.key[start + lane] : 0xffffffffu;
-    const uint32_t tok = there ? a.tok[start + lane] : 0u;
-    int n = __popc(__ballot_sync(0xffffffffu, mine == static_cast<uint32_t>(v)));
-    const bool few = n < 32;
-    if (!few) n = lower_bound(a.key, a.T, static_cast<uint32_t>(v) + 1) - start;
-    const size_t dst = static_cast<size_t>(v) * a.D;
-#pragma unroll 1
-    for (int v0 = lane; v0 - lane < nv; v0 += 32 * kVecs) {  // the same turns for every lane
+    for (int v0 = lane; v0 - lane < nv; v0 += 32 * kVecs) {
       float acc[kVecs][VEC] = {};
-      if (few) {
-        add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, n, [&](int j) { return __shfl_sync(0xffffffffu, tok, j); }, acc);
-      } else {
-        // up to the first chunk that lies inside, the chunks, the rest
-        const int end = start + n;
-        const int c0 = (start + a.chunk - 1) / a.chunk, c1 = end / a.chunk;
-        const int head = c0 < c1 ? c0 * a.chunk - start : n;
-        add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, head, [&](int j) { return a.tok[start + j]; }, acc);
-        if (c0 < c1) {
-          add_rows<VEC, true>(a.part, a.D, v0, nv, c1 - c0, [&](int j) { return c0 + j; }, acc);
-          const int tail = c1 * a.chunk;
-          add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, end - tail, [&](int j) { return a.tok[tail + j]; }, acc);
-        }
+#pragma unroll 1
+      for (int j = first; j < stop;) {
+        // up to the next run's begin, or the window's end
+        const uint32_t later = begins & ~((2u << j) - 1);
+        const int next = later ? __ffs(later) - 1 : kWindow;
+        const int n = min(next, stop) - j;
+        add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, n, [&](int r) { return __shfl_sync(0xffffffffu, my_tok, j + r + 1); }, acc);
+        if (next == kWindow)
+          add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past, [&](int r) { return a.tok[p0 + kWindow + r]; }, acc);
+        write_row<VEC>(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[i][e] = 0.f;
+        j += n;
       }
+    }
+  }
+  __syncthreads();
+  // Long runs, each by the whole block: rows up to the first chunk that lies
+  // inside, the chunks' sums, the rows behind them; every warp takes a share.
+  for (int w = 0; w < kSumWarps; ++w) {
+    const int start = long_start[w];
+    if (start < 0) continue;
+    const int end = long_end[w];
+    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = max(c0, end / a.chunk);
+    const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
+    const int tail = c0 < c1 ? c1 * a.chunk : end;
+    auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
+    for (int col = 0; col < nv; col += 32 * kVecs) {
+      const int v0 = col + lane;
+      float acc[kVecs][VEC] = {};
+      const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
+      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
+      const int m0 = c0 + share(c1 - c0, warp), m1 = c0 + share(c1 - c0, warp + 1);
+      add_rows<VEC, true>(a.part, a.D, v0, nv, m1 - m0, [&](int r) { return m0 + r; }, acc);
+      const int t0 = tail + share(end - tail, warp), t1 = tail + share(end - tail, warp + 1);
+      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, t1 - t0, [&](int r) { return a.tok[t0 + r]; }, acc);
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
-        if (v0 + 32 * i < nv) {
-          const size_t at = dst + static_cast<size_t>(v0 + 32 * i) * VEC;
-          float o[VEC];
-          Piece<VEC, false> before;
-          if (a.add) before.load(a.add, at);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) o[e] = a.add ? fmaf(a.scale, acc[i][e], before[e]) : a.scale * acc[i][e];
-          store_vec<VEC, true>(a.d_table, at, o);
-        }
+        for (int e = 0; e < VEC; ++e) red[warp][(32 * i + lane) * VEC + e] = acc[i][e];
+      __syncthreads();
+      const size_t dst = static_cast<size_t>(a.key[start]) * a.D;
+      for (int c = threadIdx.x; c < kColumns; c += 32 * kSumWarps) {
+        const int column = col * VEC + c;
+        if (column >= a.D) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
+        const float before = a.add ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.add)[dst + column]) << 16) : 0.f;
+        a.d_table[dst + column] = a.add ? fmaf(a.scale, sum, before) : a.scale * sum;
+      }
+      __syncthreads();
     }
-    start += n;
   }
 }
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
+// Blocks that fill beside the `first` blocks of a launch: enough to keep the
+// memory busy, and no more than have something to do.
+Fill with_blocks(Fill f, int first, int threads, unsigned* grid) {
+  const size_t pieces = f.n / 8 / f.parts + 1, most = (pieces + threads * 4 - 1) / (static_cast<size_t>(threads) * 4);
+  const size_t fit = static_cast<size_t>(kFillThreads / threads) * std::max(current_device_sms(), 1);
+  f.first = first;
+  *grid = static_cast<unsigned>(first + std::min(most, fit));
+  return f;
+}
+
 template <int VEC, bool kF32>
-cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (a.chunks > 0) {
-    e = launch_kernel(embedding_chunk_kernel<VEC, kF32>, dim3((a.chunks + 7) / 8), dim3(256), 0, s, true, a);
-    if (e != cudaSuccess) return e;
-  }
-  const int warps = (a.V + kRowsPerWarp - 1) / kRowsPerWarp;
-  return launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3((warps + 7) / 8), dim3(256), 0, s, a.T > 0, a);
+cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
+  unsigned grid;
+  a.fill = with_blocks(a.fill, (a.chunks + kSumWarps - 1) / kSumWarps, 32 * kSumWarps, &grid);
+  const cudaError_t e = launch_kernel(embedding_chunk_kernel<VEC, kF32>, dim3(grid), dim3(32 * kSumWarps), 0, s, true, a);
+  if (e != cudaSuccess) return e;
+  constexpr int kPerBlock = kSumWarps * kWindow;
+  return launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3((a.T + kPerBlock - 1) / kPerBlock), dim3(32 * kSumWarps), 0,
+                       s, true, a);
 }
 
 }  // namespace
@@ -434,20 +597,25 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   uint32_t* lists[4];
   for (auto& l : lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
-  cudaError_t e = cudaSuccess;
-  if (a.T > 0) {
-    e = launch_kernel(embedding_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, false, q);
-    for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
-      q.pass = i;
-      q.key_out = lists[2 * (i & 1)];
-      q.tok_out = lists[2 * (i & 1) + 1];
-      e = launch_kernel(embedding_sort_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, true, q);
-      q.key_in = q.key_out;
-      q.tok_in = q.tok_out;
-    }
+  // the fill is shared out among the launches before the last
+  Fill fill{a.d_table, static_cast<const uint16_t*>(a.add), static_cast<size_t>(a.V) * a.D, 0, 0,
+            a.T > 0 ? p.passes + 2 : 1};
+  unsigned grid;
+  q.fill = with_blocks(fill, p.blocks, kSortThreads, &grid);
+  cudaError_t e = launch_kernel(embedding_hist_kernel, dim3(grid), dim3(kSortThreads), 0, s, false, q);
+  if (e != cudaSuccess || a.T == 0) return e;
+  for (int i = 0; i < p.passes; ++i) {
+    q.pass = i;
+    q.key_out = lists[2 * (i & 1)];
+    q.tok_out = lists[2 * (i & 1) + 1];
+    ++q.fill.part;
+    e = launch_kernel(embedding_sort_kernel, dim3(grid), dim3(kSortThreads), 0, s, true, q);
     if (e != cudaSuccess) return e;
+    q.key_in = q.key_out;
+    q.tok_in = q.tok_out;
   }
-  const SumArgs m{a.d_out, a.add, q.key_in, q.tok_in, part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks};
+  fill.part = fill.parts - 1;
+  const SumArgs m{a.d_out, a.add, q.key_in, q.tok_in, part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks, fill};
   if (a.D % 8 == 0) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
   return a.d_fp32 ? launch_sums<1, true>(m, s) : launch_sums<1, false>(m, s);
 }
