@@ -27,22 +27,29 @@ MOE_DEV long long load_id(const void* p, int is64, size_t i) {
 }
 
 // VEC consecutive elements as they are stored (16 or 32 bytes where VEC = 8),
-// and their values.
+// and their values.  The loads are volatile, and the kernels that add rows state
+// how many blocks an SM is to hold, so that the loads stay together: left to
+// itself the compiler puts each next to its use, to save registers, and the
+// memory's latency is paid for every one (chunks of 32 rows of 768: 39 us).
 template <int VEC, bool kF32>
 struct Piece {
   static constexpr int kWords = VEC == 1 ? 1 : kF32 ? 8 : 4;
   uint32_t w[kWords];
 
   MOE_DEV void load(const void* p, size_t i) {
-    if constexpr (VEC == 1) {
-      w[0] = kF32 ? static_cast<const uint32_t*>(p)[i] : static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16;
+    const uint8_t* q = static_cast<const uint8_t*>(p) + i * (kF32 ? 4 : 2);
+    if constexpr (VEC == 1 && kF32) {
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(q));
+    } else if constexpr (VEC == 1) {
+      uint16_t h;
+      asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(q));
+      w[0] = static_cast<uint32_t>(h) << 16;
+    } else if constexpr (kF32) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(q));
     } else {
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (kF32 ? 4 : 2));
-#pragma unroll
-      for (int k = 0; k < kWords / 4; ++k) {
-        const uint4 x = q[k];
-        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
-      }
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(q));
     }
   }
   MOE_DEV float operator[](int e) const {
@@ -51,15 +58,23 @@ struct Piece {
   }
 };
 
+// 8 floats as one store of 32 bytes: as two of 16, each touching half of every
+// sector, a fill of 1 GB took 290 us instead of 145.
 template <int VEC, bool kF32>
 MOE_DEV void store_vec(void* p, size_t i, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     if (kF32) static_cast<float*>(p)[i] = v[0];
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
   } else if constexpr (kF32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    __stcs(q, make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(q + 1, make_float4(v[4], v[5], v[6], v[7]));
+    float* q = static_cast<float*>(p) + i;
+    if (reinterpret_cast<uintptr_t>(q) & 31) {
+      *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                   "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
+    }
   } else {
     __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i),
            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
@@ -116,7 +131,8 @@ cudaError_t launch_fwd(const EmbeddingArgs& a, cudaStream_t s) {
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1024;
-constexpr int kFillThreads = 1024;  // of an SM, that fill beside the others
+constexpr int kFillBlocks = 32;     // of an SM, one after the other, that fill beside the others
+constexpr size_t kFillBeside = 6u << 20;  // elements that are filled beside one pass of the sort
 constexpr int kHeld = 4;  // rounds of 32 tokens that a warp keeps in registers
 
 struct SortPlan {
@@ -136,17 +152,17 @@ SortPlan sort_plan(int T, int V) {
   p.blocks = (T + p.block - 1) / p.block;
   p.chunk = 32;
   while (p.chunk < 1024 && static_cast<long long>(p.chunk) * p.chunk * 16 < T) p.chunk *= 2;
-  p.chunks = T / p.chunk;
+  p.chunks = T > 2048 ? T / p.chunk : 0;  // a short list's long runs need no sums beforehand
   return p;
 }
 
-// The part of the table that one of the launches fills.
+// The part of the table that one of the launches fills: elements [from, to),
+// from a multiple of 8.
 struct Fill {
   float* out;
   const uint16_t* add;  // bf16 or nullptr
-  size_t n;             // elements
+  size_t from, to;
   int first;            // block that is the first to fill
-  int part, parts;
 };
 
 struct SortArgs {
@@ -165,8 +181,7 @@ struct SortArgs {
 
 MOE_DEV void fill_rows(const Fill& f) {
   constexpr int kEach = 4;  // pieces of 8 that a thread has in flight
-  const size_t pieces = f.n / 8;
-  const size_t p0 = pieces * f.part / f.parts, p1 = pieces * (f.part + 1) / f.parts;
+  const size_t p0 = f.from / 8, p1 = f.to / 8;
   const size_t block = blockIdx.x - f.first, blocks = gridDim.x - f.first;
   const size_t step = static_cast<size_t>(blockDim.x) * kEach;
   for (size_t p = p0 + block * step; p < p1; p += blocks * step) {
@@ -189,9 +204,9 @@ MOE_DEV void fill_rows(const Fill& f) {
       }
     }
   }
-  if (f.part + 1 == f.parts && block == 0) {
-    const size_t i = pieces * 8 + threadIdx.x;
-    if (i < f.n) f.out[i] = f.add ? __uint_as_float(static_cast<uint32_t>(f.add[i]) << 16) : 0.f;
+  if (block == 0) {  // the table's last few
+    const size_t i = p1 * 8 + threadIdx.x;
+    if (i < f.to) f.out[i] = f.add ? __uint_as_float(static_cast<uint32_t>(f.add[i]) << 16) : 0.f;
   }
 }
 
@@ -345,32 +360,36 @@ struct SumArgs {
   float* d_table;
   float scale;
   int T, V, D, chunk, chunks;
-  Fill fill;
 };
 
 constexpr int kWindow = 8;     // sorted tokens of a warp
 constexpr int kSumWarps = 8;
-constexpr int kLong = 32;      // tokens past its window that a warp adds alone
+constexpr int kLong = 16;      // tokens past its window that a warp adds alone
 
 // A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
 template <int VEC>
 struct Shape {
   static constexpr int kVecs = VEC == 8 ? 4 : 16;
-  static constexpr int kAhead = VEC == 8 ? 4 : 2;
   static constexpr int kColumns = 32 * kVecs * VEC;
 };
+template <int VEC, bool kF32>
+constexpr int kAhead = VEC == 8 && kF32 ? 2 : 4;
 
-// acc += R rows of `src`; lanes past the last column read another's piece
-// (a load under a condition would be waited for on the spot).
+// A lane's pieces of one row; lanes past the last column read another's (a load
+// under a condition would be waited for on the spot).
+template <int VEC, bool kF32, int N>
+MOE_DEV void load_row(const void* src, uint32_t row, int D, int v0, int nv, Piece<VEC, kF32> (&v)[N]) {
+  const size_t at = static_cast<size_t>(row) * D;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i].load(src, at + static_cast<size_t>(min(v0 + 32 * i, nv - 1)) * VEC);
+}
+
+// acc += R rows of `src`.
 template <int VEC, bool kF32, int R, typename Index>
 MOE_DEV void add_step(const void* src, int D, int v0, int nv, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
   Piece<VEC, kF32> v[R][Shape<VEC>::kVecs];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const size_t at = static_cast<size_t>(row(r)) * D;
-#pragma unroll
-    for (int i = 0; i < Shape<VEC>::kVecs; ++i) v[r][i].load(src, at + static_cast<size_t>(min(v0 + 32 * i, nv - 1)) * VEC);
-  }
+  for (int r = 0; r < R; ++r) load_row(src, row(r), D, v0, nv, v[r]);
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -380,9 +399,8 @@ MOE_DEV void add_step(const void* src, int D, int v0, int nv, Index row, float (
 }
 
 // acc += rows row(0) .. row(n - 1), in that order.
-template <int VEC, bool kF32, typename Index>
+template <int VEC, bool kF32, int R = kAhead<VEC, kF32>, typename Index>
 MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
-  constexpr int R = kF32 && VEC == 8 ? 2 : Shape<VEC>::kAhead;
   int j = 0;
 #pragma unroll 1
   for (; j + R <= n; j += R) add_step<VEC, kF32, R>(src, D, v0, nv, [&](int r) { return row(j + r); }, acc);
@@ -390,35 +408,36 @@ MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, 
   for (; j < n; ++j) add_step<VEC, kF32, 1>(src, D, v0, nv, [&](int) { return row(j); }, acc);
 }
 
-// Aligned runs of `chunk` sorted tokens with one id, a warp each.
+// Aligned runs of `chunk` sorted tokens with one id, a warp each (and turn of
+// columns).  Few warps have one, so each has many rows in flight.
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(32 * kSumWarps) embedding_chunk_kernel(SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps, 1) embedding_chunk_kernel(SumArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  if (static_cast<int>(blockIdx.x) >= a.fill.first) {
-    fill_rows(a.fill);
-    return;
-  }
   const int c = blockIdx.x * kSumWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (c >= a.chunks) return;
   const size_t p0 = static_cast<size_t>(c) * a.chunk;
   const uint32_t k = a.key[p0];
   if (k != a.key[p0 + a.chunk - 1] || k >= static_cast<uint32_t>(a.V)) return;
-  const int nv = a.D / VEC;
-#pragma unroll 1
-  for (int v0 = lane; v0 - lane < nv; v0 += 32 * Shape<VEC>::kVecs) {
-    float acc[Shape<VEC>::kVecs][VEC] = {};
-    add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, a.chunk, [&](int j) { return a.tok[p0 + j]; }, acc);
-#pragma unroll
-    for (int i = 0; i < Shape<VEC>::kVecs; ++i)
-      if (v0 + 32 * i < nv)
-        store_vec<VEC, true>(a.part, static_cast<size_t>(c) * a.D + static_cast<size_t>(v0 + 32 * i) * VEC, acc[i]);
+  const int nv = a.D / VEC, v0 = blockIdx.y * 32 * Shape<VEC>::kVecs + lane;
+  float acc[Shape<VEC>::kVecs][VEC] = {};
+  for (int j = 0; j < a.chunk; j += 32) {
+    const uint32_t tok = a.tok[p0 + j + lane];
+    add_rows<VEC, kF32, VEC == 8 ? 2 * kAhead<VEC, kF32> : kAhead<VEC, kF32>>(
+        a.d_out, a.D, v0, nv, 32, [&](int r) { return __shfl_sync(0xffffffffu, tok, r); }, acc);
   }
+#pragma unroll
+  for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+    if (v0 + 32 * i < nv)
+      store_vec<VEC, true>(a.part, static_cast<size_t>(c) * a.D + static_cast<size_t>(v0 + 32 * i) * VEC, acc[i]);
 }
 
 // First sorted position from lo on whose key is more than k (whole warp).
 MOE_DEV int end_of(const uint32_t* key, int lo, int T, uint32_t k) {
   const int lane = threadIdx.x & 31;
+  const int near = __popc(__ballot_sync(0xffffffffu, lo + lane < T && key[min(lo + lane, T - 1)] <= k));
+  if (near < 32) return lo + near;
+  lo += 32;
   int hi = T;  // the answer lies in [lo, hi]
   while (hi - lo > 32) {
     const int at = lo + static_cast<int>(static_cast<long long>(hi - lo) * (lane + 1) / 33);
@@ -432,25 +451,39 @@ MOE_DEV int end_of(const uint32_t* key, int lo, int T, uint32_t k) {
   return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && key[lo + lane] <= k));
 }
 
+// The row's only addition to what it was filled with: nothing to wait for, and
+// no order that could change the result.
+template <int VEC>
+MOE_DEV void add_vec(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v[0]) : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4)
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + k), "f"(v[k]), "f"(v[k + 1]), "f"(v[k + 2]),
+                   "f"(v[k + 3])
+                   : "memory");
+  }
+}
+
 template <int VEC>
 MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float (&acc)[Shape<VEC>::kVecs][VEC]) {
-  const size_t dst = static_cast<size_t>(v) * a.D;
+  float* dst = a.d_table + static_cast<size_t>(v) * a.D;
 #pragma unroll
   for (int i = 0; i < Shape<VEC>::kVecs; ++i)
     if (v0 + 32 * i < nv) {
-      const size_t at = dst + static_cast<size_t>(v0 + 32 * i) * VEC;
       float o[VEC];
-      Piece<VEC, false> before = {};
-      if (a.add) before.load(a.add, at);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) o[e] = a.add ? fmaf(a.scale, acc[i][e], before[e]) : a.scale * acc[i][e];
-      store_vec<VEC, true>(a.d_table, at, o);
+      for (int e = 0; e < VEC; ++e) o[e] = a.scale * acc[i][e];
+      if (a.add) add_vec<VEC>(dst + (v0 + 32 * i) * VEC, o);
+      else store_vec<VEC, true>(dst, static_cast<size_t>(v0 + 32 * i) * VEC, o);
     }
 }
 
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(32 * kSumWarps) embedding_rows_kernel(SumArgs a) {
-  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns;
+__global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumArgs a) {
+  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns, R = kAhead<VEC, kF32>;
+  static_assert(kWindow % R == 0);
   __shared__ float red[kSumWarps][kColumns];
   __shared__ int long_start[kSumWarps], long_end[kSumWarps];
   griddep_wait();
@@ -484,20 +517,25 @@ __global__ void __launch_bounds__(32 * kSumWarps) embedding_rows_kernel(SumArgs 
     for (int v0 = lane; v0 - lane < nv; v0 += 32 * kVecs) {
       float acc[kVecs][VEC] = {};
 #pragma unroll 1
-      for (int j = first; j < stop;) {
-        // up to the next run's begin, or the window's end
-        const uint32_t later = begins & ~((2u << j) - 1);
-        const int next = later ? __ffs(later) - 1 : kWindow;
-        const int n = min(next, stop) - j;
-        add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, n, [&](int r) { return __shfl_sync(0xffffffffu, my_tok, j + r + 1); }, acc);
-        if (next == kWindow)
-          add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past, [&](int r) { return a.tok[p0 + kWindow + r]; }, acc);
-        write_row<VEC>(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
+      for (int b = 0; b < stop; b += R) {
+        if (b + R <= first) continue;
+        Piece<VEC, kF32> x[R][kVecs];
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int r = 0; r < R; ++r) load_row(a.d_out, __shfl_sync(0xffffffffu, my_tok, b + r + 1), a.D, v0, nv, x[r]);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) acc[i][e] = 0.f;
-        j += n;
+        for (int r = 0; r < R; ++r) {
+          const int j = b + r;
+          if (j < first || j >= stop) continue;
+          const bool begin = begins >> j & 1;
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[i][e] = begin ? x[r][i][e] : acc[i][e] + x[r][i][e];
+          if (j + 1 < stop && !(begins >> (j + 1) & 1)) continue;
+          if (j + 1 == kWindow)
+            add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past, [&](int q) { return a.tok[p0 + kWindow + q]; }, acc);
+          write_row<VEC>(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
+        }
       }
     }
   }
@@ -508,7 +546,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) embedding_rows_kernel(SumArgs 
     const int start = long_start[w];
     if (start < 0) continue;
     const int end = long_end[w];
-    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = max(c0, end / a.chunk);
+    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = a.chunks ? max(c0, end / a.chunk) : c0;
     const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
     const int tail = c0 < c1 ? c1 * a.chunk : end;
     auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
@@ -533,32 +571,39 @@ __global__ void __launch_bounds__(32 * kSumWarps) embedding_rows_kernel(SumArgs 
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
-        const float before = a.add ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.add)[dst + column]) << 16) : 0.f;
-        a.d_table[dst + column] = a.add ? fmaf(a.scale, sum, before) : a.scale * sum;
+        const float o[1] = {a.scale * sum};
+        if (a.add) add_vec<1>(a.d_table + dst + column, o);
+        else a.d_table[dst + column] = o[0];
       }
       __syncthreads();
     }
   }
 }
 
+// fp32 rows are read 32 bytes at a time.
+bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
-// Blocks that fill beside the `first` blocks of a launch: enough to keep the
-// memory busy, and no more than have something to do.
-Fill with_blocks(Fill f, int first, int threads, unsigned* grid) {
-  const size_t pieces = f.n / 8 / f.parts + 1, most = (pieces + threads * 4 - 1) / (static_cast<size_t>(threads) * 4);
-  const size_t fit = static_cast<size_t>(kFillThreads / threads) * std::max(current_device_sms(), 1);
-  f.first = first;
-  *grid = static_cast<unsigned>(first + std::min(most, fit));
-  return f;
+// The next `elements` of the table for a launch whose first `first` blocks sort;
+// the fill's blocks are enough to keep the memory busy, and no more than have
+// something to do.
+unsigned fill_grid(Fill* f, size_t elements, size_t n, int first) {
+  f->from = f->to;
+  f->to = std::min(n, f->from + (elements + 7) / 8 * 8);
+  f->first = first;
+  const size_t per = static_cast<size_t>(kSortThreads) * 32, most = (f->to - f->from + per - 1) / per;
+  return static_cast<unsigned>(
+      first + std::min(most, static_cast<size_t>(kFillBlocks) * std::max(current_device_sms(), 1)));
 }
 
 template <int VEC, bool kF32>
-cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
-  unsigned grid;
-  a.fill = with_blocks(a.fill, (a.chunks + kSumWarps - 1) / kSumWarps, 32 * kSumWarps, &grid);
-  const cudaError_t e = launch_kernel(embedding_chunk_kernel<VEC, kF32>, dim3(grid), dim3(32 * kSumWarps), 0, s, true, a);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
+  if (a.chunks) {
+    const dim3 grid((a.chunks + kSumWarps - 1) / kSumWarps, (a.D + Shape<VEC>::kColumns - 1) / Shape<VEC>::kColumns);
+    const cudaError_t e = launch_kernel(embedding_chunk_kernel<VEC, kF32>, grid, dim3(32 * kSumWarps), 0, s, true, a);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int kPerBlock = kSumWarps * kWindow;
   return launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3((a.T + kPerBlock - 1) / kPerBlock), dim3(32 * kSumWarps), 0,
                        s, true, a);
@@ -567,7 +612,7 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s) {
-  return a.D % 8 == 0 ? launch_fwd<8>(a, s) : launch_fwd<1>(a, s);
+  return a.D % 8 == 0 && (!a.table_fp32 || on32(a.table)) ? launch_fwd<8>(a, s) : launch_fwd<1>(a, s);
 }
 
 size_t embedding_bwd_scratch_bytes(int T, int V, int D) {
@@ -597,26 +642,27 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   uint32_t* lists[4];
   for (auto& l : lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
-  // the fill is shared out among the launches before the last
-  Fill fill{a.d_table, static_cast<const uint16_t*>(a.add), static_cast<size_t>(a.V) * a.D, 0, 0,
-            a.T > 0 ? p.passes + 2 : 1};
-  unsigned grid;
-  q.fill = with_blocks(fill, p.blocks, kSortThreads, &grid);
-  cudaError_t e = launch_kernel(embedding_hist_kernel, dim3(grid), dim3(kSortThreads), 0, s, false, q);
+  // what the sorting passes can fill beside their own work, and the rest before them
+  const size_t n = static_cast<size_t>(a.V) * a.D, beside = a.T > 0 ? std::min(n, p.passes * kFillBeside) : 0;
+  Fill fill{a.d_table, static_cast<const uint16_t*>(a.add), 0, 0, 0};
+  const unsigned first = fill_grid(&fill, n - beside, n, p.blocks);
+  q.fill = fill;
+  cudaError_t e = cudaSuccess;
+  if (first > 0) e = launch_kernel(embedding_hist_kernel, dim3(first), dim3(kSortThreads), 0, s, false, q);
   if (e != cudaSuccess || a.T == 0) return e;
   for (int i = 0; i < p.passes; ++i) {
     q.pass = i;
     q.key_out = lists[2 * (i & 1)];
     q.tok_out = lists[2 * (i & 1) + 1];
-    ++q.fill.part;
+    const unsigned grid = fill_grid(&fill, i + 1 < p.passes ? kFillBeside : n, n, p.blocks);
+    q.fill = fill;
     e = launch_kernel(embedding_sort_kernel, dim3(grid), dim3(kSortThreads), 0, s, true, q);
     if (e != cudaSuccess) return e;
     q.key_in = q.key_out;
     q.tok_in = q.tok_out;
   }
-  fill.part = fill.parts - 1;
-  const SumArgs m{a.d_out, a.add, q.key_in, q.tok_in, part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks, fill};
-  if (a.D % 8 == 0) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
+  const SumArgs m{a.d_out, a.add, q.key_in, q.tok_in, part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks};
+  if (a.D % 8 == 0 && (!a.d_fp32 || on32(a.d_out))) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
   return a.d_fp32 ? launch_sums<1, true>(m, s) : launch_sums<1, false>(m, s);
 }
 
