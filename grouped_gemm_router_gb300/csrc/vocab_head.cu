@@ -52,11 +52,10 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
 constexpr int kNoTarget = 0x7fffffff;
 
-// A warp's buffer: 32 rows x 32 columns, fp32 targets or bf16 / fp32 results.
-constexpr int kBoxStats = 4096, kBoxOut = 2048;
-constexpr int smem_bytes(int mode) {
-  return kStages * kStageBytes + kEpiWarps * (mode == kStats ? kBoxStats : kBoxOut) + 1024;
-}
+// A warp's buffer: 32 rows of 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)
+// (TMA's 128-byte swizzle, and free of bank conflicts when a lane has a row).
+constexpr int kBoxBytes = 4096;
+constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kBoxBytes + 1024;
 
 struct VocabArgs : VocabWork {
   int T, V, D;
@@ -145,6 +144,12 @@ struct Targets {
     left = p.K - lo;
     set();
   }
+  // Past the targets of the columns in between, which another warp has: few as
+  // a rule, and a search where they are not.
+  MOE_DEV void skip(const VocabArgs& p, int row, int col) {
+    for (int i = 0; i < 3 && id < col; ++i) next(p);
+    if (id < col) start(p, row, col);
+  }
   // What lies past the current target (of labels there is no other).
   MOE_DEV void next(const VocabArgs& p) {
     if (p.K == 0) id = kNoTarget;
@@ -156,9 +161,12 @@ struct Targets {
   }
 };
 
-MOE_DEV void tma_store_f32(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  tma_store_3d(map, src, c0, c1, c2);
-  bulk_commit_group();
+// 128 bytes into a lane's row of its warp's buffer.
+MOE_DEV void put_row(uint8_t* mine, const uint32_t (&w)[32]) {
+  const uint32_t turn = lane_id() & 7u;
+#pragma unroll
+  for (uint32_t c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(mine + ((c ^ turn) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 
 template <int kMode>
@@ -312,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c_first = half * 128;
     const uint32_t tempty_leader0 = map_to_cta(smem_u32(&ctl.tempty[0]), 0);
     const uint32_t tempty_leader1 = map_to_cta(smem_u32(&ctl.tempty[1]), 0);
-    uint8_t* box = smem + kStages * kStageBytes + (warp - 2) * (kMode == kStats ? kBoxStats : kBoxOut);
+    uint8_t* box = smem + kStages * kStageBytes + (warp - 2) * kBoxBytes;
+    uint8_t* mine = box + lane * 128;  // a lane's row of it
     float run_max = -INFINITY, run_sum = 0.f;
     Targets tg;
     float row_a = 0.f, row_l = 0.f;
@@ -321,18 +330,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int warp_row0 = u.m * kTile + 128 * rank + q * 32;
       const int row = warp_row0 + lane;
       const int col0 = u.n * kTile + c_first;  // first column of this warp (of the piece, in kDz)
-      if constexpr (kMode == kStats) {
+      if constexpr (kMode != kGrad) {
         if (u.first) {
+          tg.start(p, row, p.v0 + col0);
           run_max = -INFINITY;
           run_sum = 0.f;
-          tg.start(p, row, col0);
-        } else if (tg.id < col0) {  // the other half's targets
-          tg.start(p, row, col0);
+          if constexpr (kMode == kDz) {
+            row_a = row < p.T ? p.row_a[row] : 0.f;
+            row_l = row < p.T ? p.row_l[row] : 0.f;
+          }
+        } else {
+          tg.skip(p, row, p.v0 + col0);
         }
-      } else if constexpr (kMode == kDz) {
-        tg.start(p, row, p.v0 + col0);
-        row_a = row < p.T ? p.row_a[row] : 0.f;
-        row_l = row < p.T ? p.row_l[row] : 0.f;
       }
       const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[buf]), (i >> 1) & 1, abort_flag, dev_err);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -359,12 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int end = col0 + b * 32 + 32;
           if (__any_sync(0xffffffffu, tg.id < end)) {
             // a lane writes its row and reads its targets back from it
-            // (16-byte chunk c of row r at c ^ (r % 8): free of bank conflicts)
-            uint8_t* mine = box + lane * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(mine + ((c ^ (lane & 7)) << 4)) =
-                  make_uint4(acc[b][4 * c], acc[b][4 * c + 1], acc[b][4 * c + 2], acc[b][4 * c + 3]);
+            put_row(mine, acc[b]);
             while (tg.id < end) {
               const int j = tg.id - (end - 32);
               const float z = *reinterpret_cast<const float*>(mine + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4);
@@ -394,36 +398,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if constexpr (kMode == kDz) {
         if (warp_row0 >= p.T) continue;
 #pragma unroll
-        for (int b = 0; b < kBoxes; ++b) {
+        for (int b = 0; b < kBoxes; b += 2) {
           const int cc = col0 + b * 32;
           if (cc >= p.Vcp) break;
-          uint32_t packed[16];
+          uint32_t packed[32];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float lo = row_a * exp2_fast(fmaf(__uint_as_float(acc[b][2 * j]), p.c, -row_l));
-            float hi = row_a * exp2_fast(fmaf(__uint_as_float(acc[b][2 * j + 1]), p.c, -row_l));
+          for (int j = 0; j < 32; ++j) {
+            const float lo = row_a * exp2_fast(fmaf(__uint_as_float(acc[b + j / 16][2 * (j & 15)]), p.c, -row_l));
+            const float hi = row_a * exp2_fast(fmaf(__uint_as_float(acc[b + j / 16][2 * (j & 15) + 1]), p.c, -row_l));
             packed[j] = row_a == 0.f ? 0u : pack_bf16x2(lo, hi);  // whatever a row without a loss holds
           }
-          if (cc + 32 > p.Vc) {
+          if (cc + 64 > p.Vc) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 32; ++j) {
               if (cc + 2 * j >= p.Vc) packed[j] = 0u;
               else if (cc + 2 * j + 1 >= p.Vc) packed[j] &= 0xffffu;
             }
           }
           bulk_wait_group_read0();
           __syncwarp();
-          uint8_t* mine = box + lane * 64;
-          // 64B swizzle: 16-byte chunk c of row r lives at chunk c ^ ((r / 2) % 4)
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            *reinterpret_cast<uint4*>(mine + ((v ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
-          const int end = p.v0 + cc + 32;
+          put_row(mine, packed);
+          const int end = p.v0 + cc + 64;
           while (tg.id < end) {
-            const int j = tg.id - (end - 32);
-            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ ((lane >> 1) & 3)) << 4) + (j & 7) * 2) =
-                p.value[tg.at(p, row)];
+            const int j = tg.id - (end - 64);
+            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) = p.value[tg.at(p, row)];
             tg.next(p);
           }
           fence_proxy_async_smem();
@@ -438,30 +436,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp_row0 >= rows) continue;
         const int out_row = u.which == 0 ? warp_row0 : p.v0 + warp_row0;
         const CUtensorMap* map = u.which == 0 ? &mapOut0 : &mapOut1;
+        if (p.direct[u.which]) {
 #pragma unroll
-        for (int b = 0; b < kBoxes; ++b) {
-          const int cc = col0 + b * 32;
-          if (cc >= p.D) break;
-          if (p.direct[u.which]) {
+          for (int b = 0; b < kBoxes; b += 2) {
+            const int cc = col0 + b * 32;
+            if (cc >= p.D) break;
+            uint32_t packed[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              packed[j] = pack_bf16x2(__uint_as_float(acc[b + j / 16][2 * (j & 15)]),
+                                      __uint_as_float(acc[b + j / 16][2 * (j & 15) + 1]));
             bulk_wait_group_read0();
             __syncwarp();
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack_bf16x2(__uint_as_float(acc[b][8 * v + 2 * j]), __uint_as_float(acc[b][8 * v + 2 * j + 1]));
-              *reinterpret_cast<uint4*>(box + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            put_row(mine, packed);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               tma_store_2d(map, smem_u32(box), cc, out_row);
               bulk_commit_group();
             }
-            continue;
           }
+          continue;
+        }
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b) {
+          const int cc = col0 + b * 32;
+          if (cc >= p.D) break;
           if (u.which == 0 && p.accumulate && row < p.T) {
             const float4* before = reinterpret_cast<const float4*>(
                 p.dx_part + (static_cast<size_t>(u.split) * p.T + row) * p.D + cc);
@@ -474,18 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[b][4 * v + 3] = __float_as_uint(__uint_as_float(acc[b][4 * v + 3]) + f.w);
             }
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            bulk_wait_group_read0();
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(acc[b][16 * h + 4 * c], acc[b][16 * h + 4 * c + 1], acc[b][16 * h + 4 * c + 2],
-                             acc[b][16 * h + 4 * c + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tma_store_f32(map, smem_u32(box), cc + 16 * h, out_row, u.split);
+          bulk_wait_group_read0();
+          __syncwarp();
+          put_row(mine, acc[b]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(map, smem_u32(box), cc, out_row, u.split);
+            bulk_commit_group();
           }
         }
       }
@@ -624,58 +620,68 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets
 }
 
 // Joins a row's (maximum, sum) pairs and writes lse and the loss: 32 rows a
-// block, the pairs dealt to its warps.  With the sum s relative to 2^m,
+// block, the pairs dealt to its 32 warps, then a row to each.  With the sum s relative to 2^m,
 //   lse - z / temperature = ln 2 (log2 s - (c z - m)),
 // where c z - m is one fused product: for a target that outweighs the rest both
 // terms are next to 0, and the difference of the rounded lse and z, which would
 // be off by 2^-24 of their size, is never formed.
-__global__ void __launch_bounds__(32 * kRowWarps)
+constexpr int kFinishWarps = 32;
+
+__global__ void __launch_bounds__(32 * kFinishWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
                         float c, float inv_tau, float* loss, float* lse) {
-  __shared__ float2 got[kRowWarps][33];
-  __shared__ float2 row[32];  // m, log2 s
+  __shared__ float2 got[kFinishWarps][33];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int at = blockIdx.x * 32 + lane;
+  const int row0 = blockIdx.x * 32;
+  // lane: a row of the block; warp: every kFinishWarps-th pair of it
   float m = -INFINITY, s = 0.f;
-  if (at < T)
-    for (int i = warp; i < parts; i += kRowWarps) {
-      const float2 v = part[static_cast<size_t>(i) * rows_padded + at];
-      join(m, s, v.x, v.y);
+  if (row0 + lane < T) {
+    const float2* mine = part + row0 + lane;
+    constexpr int kBatch = 4;
+    for (int i = warp; i < parts; i += kBatch * kFinishWarps) {
+      float2 v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        v[j] = mine[static_cast<size_t>(min(i + j * kFinishWarps, parts - 1)) * rows_padded];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + j * kFinishWarps < parts) join(m, s, v[j].x, v[j].y);
     }
+  }
   got[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if (warp == 0) {
-    for (int i = 1; i < kRowWarps; ++i) join(m, s, got[i][lane].x, got[i][lane].y);
-    const float log_s = log2f(s);
-    row[lane] = make_float2(m, log_s);
-    if (at < T) {
-      lse[at] = (m + log_s) * kLn2;
-      if (t.K == 0) {
-        const long long id = load_index(t.ids, t.ids64, at);
-        loss[at] = id >= 0 && id < V ? (log_s - fmaf(target[at], c, -m)) * kLn2 : 0.f;
-      }
-    }
-  }
-  if (t.K == 0) return;
-  __syncthreads();
-  for (int r = warp; r < 32; r += kRowWarps) {
-    const int i_row = blockIdx.x * 32 + r;
-    if (i_row >= T) break;
-    Teacher te;
-    read_teacher(t, i_row, V, inv_tau, te);
-    float sum = 0.f;
+  // from here on a warp has one row
+  const int row = row0 + warp;
+  if (row >= T) return;
+  m = got[lane][warp].x;
+  s = got[lane][warp].y;
 #pragma unroll
-    for (int i = 0; i < kMaxK / 32; ++i) {
-      const int j = lane + 32 * i;
-      if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
-        sum += te.p[i] * (te.log_p[i] +
-                          (row[r].y - fmaf(target[static_cast<size_t>(i_row) * t.K + j], c, -row[r].x)) * kLn2);
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) loss[i_row] = sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    join(m, s, m2, s2);
   }
+  const float log_s = log2f(s);
+  if (lane == 0) lse[row] = (m + log_s) * kLn2;
+  if (t.K == 0) {
+    if (lane == 0) {
+      const long long id = load_index(t.ids, t.ids64, row);
+      loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
+    }
+    return;
+  }
+  Teacher te;
+  read_teacher(t, row, V, inv_tau, te);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxK / 32; ++i) {
+    const int j = lane + 32 * i;
+    if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+      sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) loss[row] = sum;
 }
 
 // Backward of cross entropy: a and lse log2(e) of each row, and dz at its label,
@@ -757,6 +763,7 @@ __global__ void __launch_bounds__(256) vocab_sum_kernel(const float* part, int n
 std::mutex g_mu;
 struct Setup {
   int pairs[3] = {0, 0, 0};  // co-resident CTA pairs of each mode
+  unsigned int* dev_err = nullptr;
 };
 Setup g_setup[64];
 
@@ -770,7 +777,7 @@ cudaLaunchConfig_t pair_config(int mode, int pairs, cudaStream_t s, cudaLaunchAt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes(mode);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -794,8 +801,9 @@ cudaError_t setup(Setup* out) {
     Setup got;
     const int sms = current_device_sms();
     if (sms < 2) return cudaErrorInvalidDevice;
+    if ((e = device_error_address(&got.dev_err)) != cudaSuccess) return e;
     for (int mode = 0; mode < 3; ++mode) {
-      e = cudaFuncSetAttribute(kernel_of(mode), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(mode));
+      e = cudaFuncSetAttribute(kernel_of(mode), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e != cudaSuccess) return e;
       cudaLaunchAttribute attr[2];
       cudaLaunchConfig_t cfg = pair_config(mode, sms / 2, nullptr, attr, false);
@@ -891,7 +899,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   uint32_t* keys = t.get<uint32_t>(static_cast<size_t>(a.T) * v.K);
   v.keys = keys;
   v.target = v.K ? a.target : t.get<float>(a.T);
-  if ((e = device_error_address(&v.dev_err)) != cudaSuccess) return e;
+  v.dev_err = st.dev_err;
   CUtensorMap mx, mw;
   if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
   if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
@@ -903,7 +911,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   }
   e = launch_vocab<kStats>(std::min(st.pairs[kStats], v.items), mx, mw, mx, mx, mx, v, s, v.K != 0);
   if (e != cudaSuccess) return e;
-  return launch_kernel(vocab_finish_kernel, dim3(ceil_div(a.T, 32)), dim3(32 * kRowWarps), 0, s, true,
+  return launch_kernel(vocab_finish_kernel, dim3(ceil_div(a.T, 32)), dim3(32 * kFinishWarps), 0, s, true,
                        static_cast<const float2*>(v.part), 2 * f.runs, f.rows_padded, a.targets,
                        static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau, a.loss, a.lse);
 }
@@ -937,15 +945,15 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   v.direct[0] = dx_direct;
   v.direct[1] = dw_direct;
   v.dx_part = r.dx_part;
-  if ((e = device_error_address(&v.dev_err)) != cudaSuccess) return e;
+  v.dev_err = st.dev_err;
   CUtensorMap mx, mw, mz, mz_out, mdx, mdw;
   if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
   if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
-  e = dx_direct ? tensor_map_2d(&mdx, a.dx, a.T, a.D, 32, 32)
-                : tensor_map_f32_3d(&mdx, r.dx_part, a.D, a.T, b.splits_x, 16, 32);
+  e = dx_direct ? tensor_map_2d(&mdx, a.dx, a.T, a.D, 32, 64)
+                : tensor_map_f32_3d(&mdx, r.dx_part, a.D, a.T, b.splits_x, 32, 32);
   if (e != cudaSuccess) return e;
-  e = dw_direct ? tensor_map_2d(&mdw, a.dW, a.V, a.D, 32, 32)
-                : tensor_map_f32_3d(&mdw, r.dw_part, a.D, a.V, b.splits_w, 16, 32);
+  e = dw_direct ? tensor_map_2d(&mdw, a.dW, a.V, a.D, 32, 64)
+                : tensor_map_f32_3d(&mdw, r.dw_part, a.D, a.V, b.splits_w, 32, 32);
   if (e != cudaSuccess) return e;
   const float inv_tau = 1.f / a.temperature;
   e = K ? launch_kernel(vocab_distill_rows_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
@@ -959,7 +967,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
     v.Vcp = ceil_div(v.Vc, 64) * 64;
     v.accumulate = i > 0;
     if ((e = tensor_map_blocks(&mz, r.dz, a.T, v.Vcp, 2, 128)) != cudaSuccess) return e;
-    if ((e = tensor_map_2d(&mz_out, r.dz, a.T, v.Vcp, 32, 32)) != cudaSuccess) return e;
+    if ((e = tensor_map_2d(&mz_out, r.dz, a.T, v.Vcp, 32, 64)) != cudaSuccess) return e;
     v.VocabWork::operator=(dz_work(b, a.D, v.Vc));
     e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, true);
     if (e != cudaSuccess) return e;

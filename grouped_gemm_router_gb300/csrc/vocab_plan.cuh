@@ -34,8 +34,8 @@ struct Unit {
   int kb0, kb1;     // k blocks
   int which;        // kGrad: 0 dx, 1 dW
   int split;
-  int first, last;  // kStats: of its run
-  int slot;         // kStats: the run
+  int first, last;  // kStats, kDz: of its run
+  int slot;         // the run
 };
 
 // The units of pair `pair` in order; every role of both CTAs walks the same list.
@@ -129,8 +129,8 @@ inline ForwardPlan forward_plan(int T, int V) {
   return f;
 }
 
-constexpr size_t kPieceBytes = static_cast<size_t>(1) << 31;  // most bytes of dz that one piece holds
-constexpr int kMinSplitBlocks = 4;                            // k blocks that a split has at least
+constexpr size_t kPieceBytes = static_cast<size_t>(1) << 32;  // most bytes of dz that one piece holds
+constexpr int kMinSplitBlocks = 12;                           // k blocks that a split has at least
 constexpr int kMaxSplits = 16;
 constexpr int kPlanPairs = 76;  // pairs that the splits are planned for (the plan decides the workspace)
 
@@ -172,8 +172,8 @@ inline VocabWork dz_work(const BackwardPlan& b, int D, int Vc) {
   VocabWork w = {};
   w.nmt = b.nmt;
   w.nnt = ceil_div(Vc, kTile);
-  w.run = 1;
-  w.items = w.nmt * w.nnt;
+  w.run = run_of(w.nmt, w.nnt);
+  w.items = w.nmt * ceil_div(w.nnt, w.run);
   w.nkb[0] = ceil_div(D, kBK);
   return w;
 }

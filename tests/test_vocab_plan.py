@@ -13,7 +13,7 @@ using namespace moe;
 static long bad = 0;
 #define CHECK(ok, ...) do { if (!(ok) && ++bad <= 10) { std::printf(__VA_ARGS__); std::printf("\n"); } } while (0)
 
-void tiles(const VocabWork& w, int npairs, bool stats, int runs, const char* what) {
+void tiles(const VocabWork& w, int npairs, int runs, const char* what) {
   std::vector<int> seen(static_cast<size_t>(w.nmt) * w.nnt, 0);
   npairs = std::min(npairs, w.items);
   for (int pair = 0; pair < npairs; ++pair) {
@@ -24,7 +24,6 @@ void tiles(const VocabWork& w, int npairs, bool stats, int runs, const char* wha
       CHECK(u.m >= 0 && u.m < w.nmt && u.n >= 0 && u.n < w.nnt, "%s: tile %d %d", what, u.m, u.n);
       ++seen[static_cast<size_t>(u.m) * w.nnt + u.n];
       CHECK(u.kb0 == 0 && u.kb1 == w.nkb[0] && u.kb1 > 0, "%s: k blocks", what);
-      if (!stats) continue;
       CHECK(u.slot >= 0 && u.slot < runs, "%s: slot %d of %d", what, u.slot, runs);
       if (u.first) { CHECK(!open, "%s: a run begins inside another", what); m = u.m; slot = u.slot; open = 1; next = u.n; }
       CHECK(open && u.m == m && u.slot == slot && u.n == next, "%s: a run is broken", what);
@@ -65,7 +64,7 @@ int main() {
     std::snprintf(what, sizeof what, "T %d V %d pairs %d", T, V, npairs);
     if (static_cast<long>(f.nmt) * f.nnt > 200000) continue;
     CHECK(f.rows_padded >= T && f.run * f.runs >= f.nnt, "%s: plan", what);
-    tiles(forward_work(f, 768), npairs, true, f.runs, what);
+    tiles(forward_work(f, 768), npairs, f.runs, what);
     for (int D : ds) {
       const BackwardPlan b = backward_plan(T, D, V);
       CHECK(b.piece > 0 && static_cast<long>(b.piece) * b.pieces >= V && static_cast<long>(b.piece) * (b.pieces - 1) < V, "%s: pieces", what);
@@ -74,7 +73,8 @@ int main() {
       CHECK(b.piece <= 8 * kTile || static_cast<size_t>(b.piece) * T * 2 <= kPieceBytes + static_cast<size_t>(T) * 2 * kTile, "%s: piece of %d", what, b.piece);
       for (int i = 0; i < b.pieces; i += std::max(1, b.pieces - 1)) {
         const int Vc = std::min(b.piece, V - i * b.piece);
-        tiles(dz_work(b, D, Vc), npairs, false, 0, what);
+        const VocabWork d = dz_work(b, D, Vc);
+        tiles(d, npairs, ceil_div(d.nnt, d.run), what);
         const VocabWork w = grad_work(b, T, Vc);
         CHECK(w.splits[0] <= b.splits_x && w.splits[1] <= b.splits_w, "%s: splits", what);
         CHECK(i > 0 || w.splits[0] == b.splits_x, "%s: the first piece writes every part", what);
