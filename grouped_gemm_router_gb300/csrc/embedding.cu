@@ -8,9 +8,9 @@
 // pass, so two passes up to a million ids).  Then a warp takes 8 sorted tokens
 // and writes the rows of the table whose tokens begin there, sums in token order
 // in fp32: no sum depends on timing.  Rows without tokens (zeros, or `add`) are
-// most of a large table: all rows are filled with those first, by blocks that
-// the sorting kernels carry along, since a sort keeps few SMs busy and a fill
-// is bound by memory; the rows with tokens are then written a second time.
+// most of a large table: all rows are filled with those, by a kernel that runs
+// beside the sort, since a sort keeps few SMs busy; the rows with tokens are then
+// written a second time.
 // Frequent tokens would leave one warp with thousands of rows to add: aligned
 // runs of `chunk` sorted tokens with one id are summed by warps of their own
 // beforehand, and a long run is then added by a whole block.
@@ -131,9 +131,10 @@ cudaError_t launch_fwd(const EmbeddingArgs& a, cudaStream_t s) {
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1024;
-constexpr int kFillBlocks = 32;     // of an SM, one after the other, that fill beside the others
-constexpr size_t kFillBeside = 6u << 20;  // elements that are filled beside one pass of the sort
-constexpr int kHeld = 4;  // rounds of 32 tokens that a warp keeps in registers
+constexpr int kHeld = 8;  // rounds of 32 tokens that a warp keeps in registers
+
+constexpr int kCluster = 8;           // blocks that sort a short list
+constexpr int kShortList = kCluster * kSortThreads * kHeld;
 
 struct SortPlan {
   int passes, bits;       // of a pass
@@ -147,23 +148,18 @@ SortPlan sort_plan(int T, int V) {
   while ((V >> b) != 0) ++b;  // the keys are 0 .. V (V: no row)
   p.passes = b <= 10 ? 1 : b <= 20 ? 2 : 3;
   p.bits = (b + p.passes - 1) / p.passes;
-  p.block = 2048;
-  while (p.block < 32768 && (T + p.block - 1) / p.block > 128) p.block *= 2;
+  if (T <= kShortList) {
+    p.block = std::max(1, (T + kCluster * kSortThreads - 1) / (kCluster * kSortThreads)) * kSortThreads;
+  } else {
+    p.block = 2048;
+    while (p.block < 32768 && (T + p.block - 1) / p.block > 128) p.block *= 2;
+  }
   p.blocks = (T + p.block - 1) / p.block;
   p.chunk = 32;
   while (p.chunk < 1024 && static_cast<long long>(p.chunk) * p.chunk * 16 < T) p.chunk *= 2;
   p.chunks = T > 2048 ? T / p.chunk : 0;  // a short list's long runs need no sums beforehand
   return p;
 }
-
-// The part of the table that one of the launches fills: elements [from, to),
-// from a multiple of 8.
-struct Fill {
-  float* out;
-  const uint16_t* add;  // bf16 or nullptr
-  size_t from, to;
-  int first;            // block that is the first to fill
-};
 
 struct SortArgs {
   const void* ids;
@@ -175,90 +171,54 @@ struct SortArgs {
   const uint32_t* tok_in;
   uint32_t* key_out;
   uint32_t* tok_out;
+  uint32_t* lists[4];       // keys and tokens, twice
   int pass, passes;
-  Fill fill;
 };
 
-MOE_DEV void fill_rows(const Fill& f) {
-  constexpr int kEach = 4;  // pieces of 8 that a thread has in flight
-  const size_t p0 = f.from / 8, p1 = f.to / 8;
-  const size_t block = blockIdx.x - f.first, blocks = gridDim.x - f.first;
-  const size_t step = static_cast<size_t>(blockDim.x) * kEach;
-  for (size_t p = p0 + block * step; p < p1; p += blocks * step) {
-    Piece<8, false> v[kEach] = {};
-    if (f.add) {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const size_t q = p + static_cast<size_t>(i) * blockDim.x + threadIdx.x;
-        v[i].load(f.add, (q < p1 ? q : p0) * 8);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const size_t q = p + static_cast<size_t>(i) * blockDim.x + threadIdx.x;
-      if (q < p1) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = v[i][e];
-        store_vec<8, true>(f.out, q * 8, o);
-      }
-    }
-  }
-  if (block == 0) {  // the table's last few
-    const size_t i = p1 * 8 + threadIdx.x;
-    if (i < f.to) f.out[i] = f.add ? __uint_as_float(static_cast<uint32_t>(f.add[i]) << 16) : 0.f;
-  }
-}
-
 MOE_DEV uint32_t sort_key(const SortArgs& a, int i) {
-  if (a.key_in) return a.key_in[i];
+  if (a.key_in) return __ldcg(a.key_in + i);
   const long long id = load_id(a.ids, a.ids64, i);
   return id >= 0 && id < a.V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
 }
 
-// The first pass's histograms of the blocks, and zeros for the later passes'.
-__global__ void __launch_bounds__(kSortThreads) embedding_hist_kernel(SortArgs a) {
-  __shared__ uint32_t h[kMaxBins];
-  griddep_launch_dependents();
-  if (static_cast<int>(blockIdx.x) >= a.blocks) {
-    fill_rows(a.fill);
-    return;
-  }
+// The first pass's histogram of block `block`, and zeros for the later passes'.
+MOE_DEV void first_histogram(const SortArgs& a, int block, uint32_t (&h)[kMaxBins]) {
   const int bins = 1 << a.bits;
   for (int d = threadIdx.x; d < bins; d += kSortThreads) h[d] = 0;
   __syncthreads();
-  const int i0 = blockIdx.x * a.block, i1 = min(a.T, i0 + a.block);
+  const int i0 = block * a.block, i1 = min(a.T, i0 + a.block);
 #pragma unroll 4
   for (int i = i0 + threadIdx.x; i < i1; i += kSortThreads) atomicAdd(&h[sort_key(a, i) & (bins - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-    a.hist[static_cast<size_t>(blockIdx.x) * bins + d] = h[d];
-    for (int q = 1; q < a.passes; ++q) a.hist[(static_cast<size_t>(q) * a.blocks + blockIdx.x) * bins + d] = 0;
+    a.hist[static_cast<size_t>(block) * bins + d] = h[d];
+    for (int q = 1; q < a.passes; ++q) a.hist[(static_cast<size_t>(q) * a.blocks + block) * bins + d] = 0;
   }
 }
 
-// One stable pass: a block's warps take its tokens in order, 32 at a time.
-__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a) {
-  __shared__ uint16_t cnt[kSortWarps][kMaxBins];
-  __shared__ uint32_t base[kMaxBins];
-  __shared__ uint32_t warp_total[kSortWarps];
-  griddep_launch_dependents();
-  griddep_wait();
-  if (static_cast<int>(blockIdx.x) >= a.blocks) {
-    fill_rows(a.fill);
-    return;
-  }
+struct SortSmem {
+  uint16_t cnt[kSortWarps][kMaxBins];
+  uint32_t base[kMaxBins];
+  uint32_t warp_total[kSortWarps];
+};
+
+// One stable pass over block `block`: its warps take its tokens in order, 32 at
+// a time.  Lists and histograms that other blocks have written are read from L2.
+MOE_DEV void sort_pass(const SortArgs& a, int block, SortSmem& sm) {
+  auto& cnt = sm.cnt;
+  auto& base = sm.base;
+  auto& warp_total = sm.warp_total;
   const int bins = 1 << a.bits, shift = a.pass * a.bits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_warp = a.block / kSortWarps;
-  const int w0 = blockIdx.x * a.block + warp * per_warp, w1 = min(a.T, w0 + per_warp);
+  const int w0 = min(a.T, block * a.block + warp * per_warp), w1 = min(min(a.T, (block + 1) * a.block), w0 + per_warp);
   // the first kHeld rounds' tokens stay in registers
   uint32_t key[kHeld], tok[kHeld];
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int i = w0 + 32 * k + lane;
     key[k] = i < w1 ? sort_key(a, i) : 0u;
-    tok[k] = i < w1 && a.key_in ? a.tok_in[i] : static_cast<uint32_t>(i);
+    tok[k] = i < w1 && a.key_in ? __ldcg(a.tok_in + i) : static_cast<uint32_t>(i);
   }
   for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads)
     reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
@@ -274,9 +234,9 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     if (d < bins) {
 #pragma unroll 8
       for (int b = 0; b < a.blocks; ++b) {
-        const uint32_t v = hist[static_cast<size_t>(b) * bins + d];
+        const uint32_t v = __ldcg(hist + static_cast<size_t>(b) * bins + d);
         total[k] += v;
-        if (b < static_cast<int>(blockIdx.x)) before[k] += v;
+        if (b < block) before[k] += v;
       }
     }
     local += total[k];
@@ -344,8 +304,72 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     if (r < rounds) place(r, key[r], tok[r]);
   for (int r = kHeld; r < rounds; ++r) {
     const int i = w0 + 32 * r + lane;
-    place(r, i < w1 ? sort_key(a, i) : 0u, i < w1 && a.key_in ? a.tok_in[i] : static_cast<uint32_t>(i));
+    place(r, i < w1 ? sort_key(a, i) : 0u, i < w1 && a.key_in ? __ldcg(a.tok_in + i) : static_cast<uint32_t>(i));
   }
+}
+
+// Long lists: a launch for the histograms and one for each pass.
+__global__ void __launch_bounds__(kSortThreads) embedding_hist_kernel(SortArgs a) {
+  __shared__ uint32_t h[kMaxBins];
+  griddep_launch_dependents();
+  first_histogram(a, blockIdx.x, h);
+}
+
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a) {
+  __shared__ SortSmem sm;
+  griddep_launch_dependents();
+  griddep_wait();
+  sort_pass(a, blockIdx.x, sm);
+}
+
+// Short lists: the whole sort by one cluster.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) embedding_sort_short_kernel(SortArgs a) {
+  __shared__ SortSmem sm;
+  griddep_launch_dependents();
+  const int block = blockIdx.x;
+  if (block < a.blocks) first_histogram(a, block, sm.base);
+  for (a.pass = 0; a.pass < a.passes; ++a.pass) {
+    cluster_sync_all();
+    a.key_out = a.lists[2 * (a.pass & 1)];
+    a.tok_out = a.lists[2 * (a.pass & 1) + 1];
+    if (block < a.blocks) sort_pass(a, block, sm);
+    a.key_in = a.key_out;
+    a.tok_in = a.tok_out;
+  }
+}
+
+// Every row of the table: zeros, or `add`.  It runs beside the sort before it
+// and ends after it, so that what waits for this kernel may read both.
+constexpr int kFillThreads = 512;
+constexpr int kFillEach = 4;     // pieces of 8 that a thread has in flight
+constexpr int kFillBlocks = 64;  // of an SM, one after the other (4: 160 us for 1 GB, 64: 142)
+
+__global__ void __launch_bounds__(kFillThreads) embedding_fill_kernel(float* out, const uint16_t* add, size_t n) {
+  griddep_launch_dependents();
+  const size_t pieces = n / 8, step = static_cast<size_t>(kFillThreads) * kFillEach;
+  for (size_t p = blockIdx.x * step; p < pieces; p += gridDim.x * step) {
+    Piece<8, false> v[kFillEach] = {};
+    if (add) {
+#pragma unroll
+      for (int i = 0; i < kFillEach; ++i)
+        v[i].load(add, min(p + static_cast<size_t>(i) * kFillThreads + threadIdx.x, pieces - 1) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kFillEach; ++i) {
+      const size_t q = p + static_cast<size_t>(i) * kFillThreads + threadIdx.x;
+      if (q < pieces) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[i][e];
+        store_vec<8, true>(out, q * 8, o);
+      }
+    }
+  }
+  if (blockIdx.x == 0) {  // the last few elements
+    const size_t i = pieces * 8 + threadIdx.x;
+    if (i < n) out[i] = add ? __uint_as_float(static_cast<uint32_t>(add[i]) << 16) : 0.f;
+  }
+  griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -360,6 +384,8 @@ struct SumArgs {
   float* d_table;
   float scale;
   int T, V, D, chunk, chunks;
+  int window_blocks;
+  int2* long_runs;         // [window_blocks, kSumWarps], with chunks
 };
 
 constexpr int kWindow = 8;     // sorted tokens of a warp
@@ -369,7 +395,7 @@ constexpr int kLong = 16;      // tokens past its window that a warp adds alone
 // A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
 template <int VEC>
 struct Shape {
-  static constexpr int kVecs = VEC == 8 ? 4 : 16;
+  static constexpr int kVecs = VEC == 8 ? 4 : 8;
   static constexpr int kColumns = 32 * kVecs * VEC;
 };
 template <int VEC, bool kF32>
@@ -384,47 +410,40 @@ MOE_DEV void load_row(const void* src, uint32_t row, int D, int v0, int nv, Piec
   for (int i = 0; i < N; ++i) v[i].load(src, at + static_cast<size_t>(min(v0 + 32 * i, nv - 1)) * VEC);
 }
 
-// acc += R rows of `src`.
-template <int VEC, bool kF32, int R, typename Index>
-MOE_DEV void add_step(const void* src, int D, int v0, int nv, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
-  Piece<VEC, kF32> v[R][Shape<VEC>::kVecs];
-#pragma unroll
-  for (int r = 0; r < R; ++r) load_row(src, row(r), D, v0, nv, v[r]);
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < Shape<VEC>::kVecs; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[i][e] += v[r][i][e];
-}
-
-// acc += rows row(0) .. row(n - 1), in that order.
-template <int VEC, bool kF32, int R = kAhead<VEC, kF32>, typename Index>
+// acc += rows row(0) .. row(n - 1) of `src`, in that order, R in flight (the
+// last of them again where there are fewer left).
+template <int VEC, bool kF32, typename Index>
 MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
-  int j = 0;
+  constexpr int R = kAhead<VEC, kF32>;
 #pragma unroll 1
-  for (; j + R <= n; j += R) add_step<VEC, kF32, R>(src, D, v0, nv, [&](int r) { return row(j + r); }, acc);
-#pragma unroll 1
-  for (; j < n; ++j) add_step<VEC, kF32, 1>(src, D, v0, nv, [&](int) { return row(j); }, acc);
+  for (int j = 0; j < n; j += R) {
+    Piece<VEC, kF32> v[R][Shape<VEC>::kVecs];
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_row(src, row(min(j + r, n - 1)), D, v0, nv, v[r]);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (j + r < n)
+#pragma unroll
+        for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[i][e] += v[r][i][e];
+  }
 }
 
-// Aligned runs of `chunk` sorted tokens with one id, a warp each (and turn of
-// columns).  Few warps have one, so each has many rows in flight.
+// Sum of an aligned run of `chunk` sorted tokens, where it has one id: warp
+// `job` of chunks x turns of columns.
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(32 * kSumWarps, 1) embedding_chunk_kernel(SumArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int c = blockIdx.x * kSumWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c >= a.chunks) return;
+MOE_DEV void sum_chunk(const SumArgs& a, int job) {
+  const int c = job % a.chunks, lane = threadIdx.x & 31;
+  const int nv = a.D / VEC, v0 = job / a.chunks * 32 * Shape<VEC>::kVecs + lane;
+  if (v0 - lane >= nv) return;
   const size_t p0 = static_cast<size_t>(c) * a.chunk;
   const uint32_t k = a.key[p0];
   if (k != a.key[p0 + a.chunk - 1] || k >= static_cast<uint32_t>(a.V)) return;
-  const int nv = a.D / VEC, v0 = blockIdx.y * 32 * Shape<VEC>::kVecs + lane;
   float acc[Shape<VEC>::kVecs][VEC] = {};
   for (int j = 0; j < a.chunk; j += 32) {
     const uint32_t tok = a.tok[p0 + j + lane];
-    add_rows<VEC, kF32, VEC == 8 ? 2 * kAhead<VEC, kF32> : kAhead<VEC, kF32>>(
-        a.d_out, a.D, v0, nv, 32, [&](int r) { return __shfl_sync(0xffffffffu, tok, r); }, acc);
+    add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, 32, [&](int r) { return __shfl_sync(0xffffffffu, tok, r); }, acc);
   }
 #pragma unroll
   for (int i = 0; i < Shape<VEC>::kVecs; ++i)
@@ -480,13 +499,78 @@ MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float
     }
 }
 
+// Long runs [start, end) (start < 0: none), each by the whole block: rows up to
+// the first chunk that lies inside, the chunks' sums, the rows behind them;
+// every warp takes a share.
+template <int VEC, bool kF32>
+MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], float (&red)[kSumWarps][Shape<VEC>::kColumns]) {
+  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nv = a.D / VEC;
+#pragma unroll 1
+  for (int w = 0; w < kSumWarps; ++w) {
+    const int start = runs[w].x, end = runs[w].y;
+    if (start < 0) continue;
+    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = a.chunks ? max(c0, end / a.chunk) : c0;
+    const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
+    const int tail = c0 < c1 ? c1 * a.chunk : end;
+    auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
+#pragma unroll 1
+    for (int col = 0; col < nv; col += 32 * kVecs) {
+      const int v0 = col + lane;
+      float acc[kVecs][VEC] = {};
+      const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
+      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
+      const int m0 = c0 + share(c1 - c0, warp), m1 = c0 + share(c1 - c0, warp + 1);
+      add_rows<VEC, true>(a.part, a.D, v0, nv, m1 - m0, [&](int r) { return m0 + r; }, acc);
+      const int t0 = tail + share(end - tail, warp), t1 = tail + share(end - tail, warp + 1);
+      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, t1 - t0, [&](int r) { return a.tok[t0 + r]; }, acc);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) red[warp][(32 * i + lane) * VEC + e] = acc[i][e];
+      __syncthreads();
+      const size_t dst = static_cast<size_t>(a.key[start]) * a.D;
+      for (int c = threadIdx.x; c < kColumns; c += 32 * kSumWarps) {
+        const int column = col * VEC + c;
+        if (column >= a.D) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
+        const float o[1] = {a.scale * sum};
+        if (a.add) add_vec<1>(a.d_table + dst + column, o);
+        else a.d_table[dst + column] = o[0];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The long runs that the windows of one block have found.
+template <int VEC, bool kF32>
+__global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_long_kernel(SumArgs a) {
+  __shared__ float red[kSumWarps][Shape<VEC>::kColumns];
+  __shared__ int2 runs[kSumWarps];
+  griddep_wait();
+  if (threadIdx.x < kSumWarps) runs[threadIdx.x] = a.long_runs[blockIdx.x * kSumWarps + threadIdx.x];
+  __syncthreads();
+  add_long_runs<VEC, kF32>(a, runs, red);
+}
+
+// A warp a window of sorted tokens: the rows whose tokens begin there.  Blocks
+// past the windows' sum the chunks; the long runs then wait for those.
 template <int VEC, bool kF32>
 __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumArgs a) {
-  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns, R = kAhead<VEC, kF32>;
+  constexpr int kVecs = Shape<VEC>::kVecs, R = kAhead<VEC, kF32>;
   static_assert(kWindow % R == 0);
-  __shared__ float red[kSumWarps][kColumns];
-  __shared__ int long_start[kSumWarps], long_end[kSumWarps];
+  __shared__ float red[kSumWarps][Shape<VEC>::kColumns];
+  __shared__ int2 runs[kSumWarps];
+  griddep_launch_dependents();
   griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= a.window_blocks) {
+    sum_chunk<VEC, kF32>(a, (blockIdx.x - a.window_blocks) * kSumWarps + (threadIdx.x >> 5));
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int p0 = (blockIdx.x * kSumWarps + warp) * kWindow;
   const int nv = a.D / VEC;
@@ -503,11 +587,11 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
       const int begin = p0 + 31 - __clz(begins);
       const int end = end_of(a.key, p0 + kWindow, a.T, last);
       len_past = end - (p0 + kWindow);
-      if (lane == 0) long_start[warp] = begin, long_end[warp] = end;
+      if (lane == 0) runs[warp] = make_int2(begin, end);
     }
   }
   const bool is_long = len_past > kLong;
-  if (lane == 0 && !is_long) long_start[warp] = -1;
+  if (lane == 0 && !is_long) runs[warp] = make_int2(-1, -1);
   if (begins) {
     const int first = __ffs(begins) - 1;
     // past the window, a run too long for this warp, or the tokens without a row
@@ -539,45 +623,13 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
       }
     }
   }
-  __syncthreads();
-  // Long runs, each by the whole block: rows up to the first chunk that lies
-  // inside, the chunks' sums, the rows behind them; every warp takes a share.
-  for (int w = 0; w < kSumWarps; ++w) {
-    const int start = long_start[w];
-    if (start < 0) continue;
-    const int end = long_end[w];
-    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = a.chunks ? max(c0, end / a.chunk) : c0;
-    const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
-    const int tail = c0 < c1 ? c1 * a.chunk : end;
-    auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
-    for (int col = 0; col < nv; col += 32 * kVecs) {
-      const int v0 = col + lane;
-      float acc[kVecs][VEC] = {};
-      const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
-      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
-      const int m0 = c0 + share(c1 - c0, warp), m1 = c0 + share(c1 - c0, warp + 1);
-      add_rows<VEC, true>(a.part, a.D, v0, nv, m1 - m0, [&](int r) { return m0 + r; }, acc);
-      const int t0 = tail + share(end - tail, warp), t1 = tail + share(end - tail, warp + 1);
-      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, t1 - t0, [&](int r) { return a.tok[t0 + r]; }, acc);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) red[warp][(32 * i + lane) * VEC + e] = acc[i][e];
-      __syncthreads();
-      const size_t dst = static_cast<size_t>(a.key[start]) * a.D;
-      for (int c = threadIdx.x; c < kColumns; c += 32 * kSumWarps) {
-        const int column = col * VEC + c;
-        if (column >= a.D) break;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
-        const float o[1] = {a.scale * sum};
-        if (a.add) add_vec<1>(a.d_table + dst + column, o);
-        else a.d_table[dst + column] = o[0];
-      }
-      __syncthreads();
-    }
+  if (a.chunks) {
+    __syncwarp();
+    if (lane == 0) a.long_runs[blockIdx.x * kSumWarps + warp] = runs[warp];
+    return;
   }
+  __syncthreads();
+  add_long_runs<VEC, kF32>(a, runs, red);
 }
 
 // fp32 rows are read 32 bytes at a time.
@@ -585,29 +637,16 @@ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
-// The next `elements` of the table for a launch whose first `first` blocks sort;
-// the fill's blocks are enough to keep the memory busy, and no more than have
-// something to do.
-unsigned fill_grid(Fill* f, size_t elements, size_t n, int first) {
-  f->from = f->to;
-  f->to = std::min(n, f->from + (elements + 7) / 8 * 8);
-  f->first = first;
-  const size_t per = static_cast<size_t>(kSortThreads) * 32, most = (f->to - f->from + per - 1) / per;
-  return static_cast<unsigned>(
-      first + std::min(most, static_cast<size_t>(kFillBlocks) * std::max(current_device_sms(), 1)));
-}
-
 template <int VEC, bool kF32>
 cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
-  if (a.chunks) {
-    const dim3 grid((a.chunks + kSumWarps - 1) / kSumWarps, (a.D + Shape<VEC>::kColumns - 1) / Shape<VEC>::kColumns);
-    const cudaError_t e = launch_kernel(embedding_chunk_kernel<VEC, kF32>, grid, dim3(32 * kSumWarps), 0, s, true, a);
-    if (e != cudaSuccess) return e;
-  }
-  constexpr int kPerBlock = kSumWarps * kWindow;
-  return launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3((a.T + kPerBlock - 1) / kPerBlock), dim3(32 * kSumWarps), 0,
-                       s, true, a);
+  const int turns = (a.D + Shape<VEC>::kColumns - 1) / Shape<VEC>::kColumns;
+  const unsigned grid = a.window_blocks + static_cast<unsigned>((static_cast<long long>(a.chunks) * turns + kSumWarps - 1) / kSumWarps);
+  const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(grid), dim3(32 * kSumWarps), 0, s, true, a);
+  if (e != cudaSuccess || !a.chunks) return e;
+  return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(a.window_blocks), dim3(32 * kSumWarps), 0, s, true, a);
 }
+
+int window_blocks(int T) { return (T + kSumWarps * kWindow - 1) / (kSumWarps * kWindow); }
 
 }  // namespace
 
@@ -618,7 +657,8 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s) {
 size_t embedding_bwd_scratch_bytes(int T, int V, int D) {
   const SortPlan p = sort_plan(T, V);
   return padded(static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits)) +
-         4 * padded(static_cast<size_t>(T) * sizeof(uint32_t)) + padded(static_cast<size_t>(p.chunks) * D * sizeof(float));
+         4 * padded(static_cast<size_t>(T) * sizeof(uint32_t)) + padded(static_cast<size_t>(p.chunks) * D * sizeof(float)) +
+         padded(p.chunks ? window_blocks(T) * kSumWarps * sizeof(int2) : 0);
 }
 
 cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaStream_t s) {
@@ -639,29 +679,31 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   q.bits = p.bits;
   q.passes = p.passes;
   q.hist = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits)));
-  uint32_t* lists[4];
-  for (auto& l : lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
+  for (auto& l : q.lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
-  // what the sorting passes can fill beside their own work, and the rest before them
-  const size_t n = static_cast<size_t>(a.V) * a.D, beside = a.T > 0 ? std::min(n, p.passes * kFillBeside) : 0;
-  Fill fill{a.d_table, static_cast<const uint16_t*>(a.add), 0, 0, 0};
-  const unsigned first = fill_grid(&fill, n - beside, n, p.blocks);
-  q.fill = fill;
+  int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? window_blocks(a.T) * kSumWarps * sizeof(int2) : 0));
   cudaError_t e = cudaSuccess;
-  if (first > 0) e = launch_kernel(embedding_hist_kernel, dim3(first), dim3(kSortThreads), 0, s, false, q);
-  if (e != cudaSuccess || a.T == 0) return e;
-  for (int i = 0; i < p.passes; ++i) {
-    q.pass = i;
-    q.key_out = lists[2 * (i & 1)];
-    q.tok_out = lists[2 * (i & 1) + 1];
-    const unsigned grid = fill_grid(&fill, i + 1 < p.passes ? kFillBeside : n, n, p.blocks);
-    q.fill = fill;
-    e = launch_kernel(embedding_sort_kernel, dim3(grid), dim3(kSortThreads), 0, s, true, q);
-    if (e != cudaSuccess) return e;
-    q.key_in = q.key_out;
-    q.tok_in = q.tok_out;
+  if (a.T > 0 && a.T <= kShortList) {
+    e = launch_kernel(embedding_sort_short_kernel, dim3(kCluster), dim3(kSortThreads), 0, s, false, q);
+  } else if (a.T > 0) {
+    e = launch_kernel(embedding_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, false, q);
+    for (q.pass = 0; q.pass < p.passes && e == cudaSuccess; ++q.pass) {
+      q.key_out = q.lists[2 * (q.pass & 1)];
+      q.tok_out = q.lists[2 * (q.pass & 1) + 1];
+      e = launch_kernel(embedding_sort_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, true, q);
+      q.key_in = q.key_out;
+      q.tok_in = q.tok_out;
+    }
   }
-  const SumArgs m{a.d_out, a.add, q.key_in, q.tok_in, part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks};
+  if (e != cudaSuccess) return e;
+  const size_t n = static_cast<size_t>(a.V) * a.D, per = static_cast<size_t>(kFillThreads) * kFillEach * 8;
+  const size_t fit = static_cast<size_t>(kFillBlocks) * std::max(current_device_sms(), 1);
+  e = launch_kernel(embedding_fill_kernel, dim3(static_cast<unsigned>(std::min((n + per - 1) / per, fit))), dim3(kFillThreads),
+                    0, s, a.T > 0, a.d_table, static_cast<const uint16_t*>(a.add), n);
+  if (e != cudaSuccess || a.T == 0) return e;
+  const int last = (p.passes - 1) & 1;
+  const SumArgs m{a.d_out, a.add, q.lists[2 * last], q.lists[2 * last + 1], part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks,
+                  window_blocks(a.T), long_runs};
   if (a.D % 8 == 0 && (!a.d_fp32 || on32(a.d_out))) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
   return a.d_fp32 ? launch_sums<1, true>(m, s) : launch_sums<1, false>(m, s);
 }

@@ -13,7 +13,11 @@ namespace {
 
 constexpr int kTile = 256;      // rows and columns of a pair's tile
 constexpr int kBK = 128;        // k of a stage
-constexpr int kGroupRows = 64;  // row tiles that are worked on side by side
+// Row tiles that are worked on side by side, all of them before the next run of
+// the vocabulary.  Without stores many share a read of W (64: 1245 us at 32768 x
+// 768 x 50001, 24: 1255); dz of few rows at a time is written with less
+// contention (24: 1425 us, 64: 1450, 128: 1540, 8: 1505).
+constexpr int kGroupStats = 64, kGroupDz = 24;
 
 enum Mode { kStats, kDz, kGrad };
 
@@ -81,6 +85,7 @@ struct Walk {
       u.kb1 = static_cast<int>(static_cast<long long>(p.nkb[which]) * (u.split + 1) / p.splits[which]);
       return true;
     } else {
+      constexpr int kGroup = kMode == kStats ? kGroupStats : kGroupDz;
       for (;;) {
         ++it;
         const int item = pair + it / p.run * npairs;
@@ -88,11 +93,11 @@ struct Walk {
         const int sub = it % p.run;
         // row tiles in groups; within a group all its rows before the next run of the vocabulary
         const int runs = (p.nnt + p.run - 1) / p.run;
-        const int g = item / (kGroupRows * runs);
-        const int in_group = least(kGroupRows, p.nmt - g * kGroupRows);
-        const int r = item - g * kGroupRows * runs;
+        const int g = item / (kGroup * runs);
+        const int in_group = least(kGroup, p.nmt - g * kGroup);
+        const int r = item - g * kGroup * runs;
         u.slot = r / in_group;
-        u.m = g * kGroupRows + r % in_group;
+        u.m = g * kGroup + r % in_group;
         u.n = u.slot * p.run + sub;
         if (u.n >= p.nnt) continue;
         u.first = sub == 0;

@@ -13,11 +13,12 @@ using namespace moe;
 static long bad = 0;
 #define CHECK(ok, ...) do { if (!(ok) && ++bad <= 10) { std::printf(__VA_ARGS__); std::printf("\n"); } } while (0)
 
+template <int kMode>
 void tiles(const VocabWork& w, int npairs, int runs, const char* what) {
   std::vector<int> seen(static_cast<size_t>(w.nmt) * w.nnt, 0);
   npairs = std::min(npairs, w.items);
   for (int pair = 0; pair < npairs; ++pair) {
-    Walk<kStats> walk;
+    Walk<kMode> walk;
     Unit u;
     int m = -1, slot = -1, open = 0, next = 0;
     while (walk.next(w, pair, npairs, u)) {
@@ -64,7 +65,7 @@ int main() {
     std::snprintf(what, sizeof what, "T %d V %d pairs %d", T, V, npairs);
     if (static_cast<long>(f.nmt) * f.nnt > 200000) continue;
     CHECK(f.rows_padded >= T && f.run * f.runs >= f.nnt, "%s: plan", what);
-    tiles(forward_work(f, 768), npairs, f.runs, what);
+    tiles<kStats>(forward_work(f, 768), npairs, f.runs, what);
     for (int D : ds) {
       const BackwardPlan b = backward_plan(T, D, V);
       CHECK(b.piece > 0 && static_cast<long>(b.piece) * b.pieces >= V && static_cast<long>(b.piece) * (b.pieces - 1) < V, "%s: pieces", what);
@@ -74,7 +75,7 @@ int main() {
       for (int i = 0; i < b.pieces; i += std::max(1, b.pieces - 1)) {
         const int Vc = std::min(b.piece, V - i * b.piece);
         const VocabWork d = dz_work(b, D, Vc);
-        tiles(d, npairs, ceil_div(d.nnt, d.run), what);
+        tiles<kDz>(d, npairs, ceil_div(d.nnt, d.run), what);
         const VocabWork w = grad_work(b, T, Vc);
         CHECK(w.splits[0] <= b.splits_x && w.splits[1] <= b.splits_w, "%s: splits", what);
         CHECK(i > 0 || w.splits[0] == b.splits_x, "%s: the first piece writes every part", what);
