@@ -4,13 +4,12 @@
 // Both are bound by memory.  The lookup gives a row to a few lanes, up to four
 // 16-byte pieces each.
 //
-// The gradient sorts the tokens by id (stable radix sort, most of 10 bits a
-// pass, so two passes up to a million ids).  Then a warp takes 8 sorted tokens
+// The gradient sorts the tokens by id (stable radix sort, up to 9 bits a pass:
+// two passes up to 262143 ids).  Then a warp takes 8 sorted tokens
 // and writes the rows of the table whose tokens begin there, sums in token order
 // in fp32: no sum depends on timing.  Rows without tokens (zeros, or `add`) are
-// most of a large table: all rows are filled with those, by a kernel that runs
-// beside the sort, since a sort keeps few SMs busy; the rows with tokens are then
-// written a second time.
+// most of a large table: all rows are filled with those beside the sort, which
+// keeps few SMs busy; the rows with tokens are then written a second time.
 // Frequent tokens would leave one warp with thousands of rows to add: aligned
 // runs of `chunk` sorted tokens with one id are summed by warps of their own
 // beforehand, and a long run is then added by a whole block.
@@ -130,11 +129,12 @@ cudaError_t launch_fwd(const EmbeddingArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxBins = 1024;
+constexpr int kMaxBins = 512;
 constexpr int kHeld = 8;  // rounds of 32 tokens that a warp keeps in registers
 
 constexpr int kCluster = 8;           // blocks that sort a short list
-constexpr int kShortList = kCluster * kSortThreads * kHeld;
+constexpr int kShortBlock = kSortThreads * kHeld;
+constexpr int kShortList = kCluster * kShortBlock;  // (its positions fit in 16 bits)
 
 struct SortPlan {
   int passes, bits;       // of a pass
@@ -146,10 +146,11 @@ SortPlan sort_plan(int T, int V) {
   SortPlan p;
   int b = 1;
   while ((V >> b) != 0) ++b;  // the keys are 0 .. V (V: no row)
-  p.passes = b <= 10 ? 1 : b <= 20 ? 2 : 3;
+  p.passes = (b + 8) / 9;
   p.bits = (b + p.passes - 1) / p.passes;
   if (T <= kShortList) {
-    p.block = std::max(1, (T + kCluster * kSortThreads - 1) / (kCluster * kSortThreads)) * kSortThreads;
+    p.block = kSortThreads;
+    while (p.block * kCluster < T) p.block *= 2;
   } else {
     p.block = 2048;
     while (p.block < 32768 && (T + p.block - 1) / p.block > 128) p.block *= 2;
@@ -165,7 +166,7 @@ struct SortArgs {
   const void* ids;
   int ids64;
   int T, V;
-  int block, blocks, bits;
+  int block, blocks, bits, log2_block;
   uint32_t* hist;           // [passes, blocks, 1 << bits]
   const uint32_t* key_in;   // nullptr: from ids
   const uint32_t* tok_in;
@@ -225,23 +226,17 @@ MOE_DEV void sort_pass(const SortArgs& a, int block, SortSmem& sm) {
   // where the block's tokens of each digit begin: all smaller digits, then the
   // same digit in earlier blocks
   const uint32_t* hist = a.hist + static_cast<size_t>(a.pass) * a.blocks * bins;
-  constexpr int kPer = kMaxBins / kSortThreads;
-  uint32_t total[kPer], before[kPer], local = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int d = threadIdx.x * kPer + k;
-    total[k] = before[k] = 0;
-    if (d < bins) {
+  static_assert(kMaxBins <= kSortThreads);
+  uint32_t total = 0, before = 0;
+  if (threadIdx.x < bins) {
 #pragma unroll 8
-      for (int b = 0; b < a.blocks; ++b) {
-        const uint32_t v = __ldcg(hist + static_cast<size_t>(b) * bins + d);
-        total[k] += v;
-        if (b < block) before[k] += v;
-      }
+    for (int b = 0; b < a.blocks; ++b) {
+      const uint32_t v = __ldcg(hist + static_cast<size_t>(b) * bins + threadIdx.x);
+      total += v;
+      if (b < block) before += v;
     }
-    local += total[k];
   }
-  uint32_t incl = local;
+  uint32_t incl = total;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -249,13 +244,9 @@ MOE_DEV void sort_pass(const SortArgs& a, int block, SortSmem& sm) {
   }
   if (lane == 31) warp_total[warp] = incl;
   __syncthreads();
-  uint32_t run = incl - local;
+  uint32_t run = incl - total;
   for (int w = 0; w < warp; ++w) run += warp_total[w];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    base[threadIdx.x * kPer + k] = run + before[k];
-    run += total[k];
-  }
+  if (threadIdx.x < bins) base[threadIdx.x] = run + before;
   const int rounds = (max(w1 - w0, 0) + 31) / 32;
   auto count = [&](int r, uint32_t k) {
     const bool there = w0 + 32 * r + lane < w1;
@@ -322,24 +313,123 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
   sort_pass(a, blockIdx.x, sm);
 }
 
-// Short lists: the whole sort by one cluster.
+// Short lists: the whole sort by one cluster, on chip.  Block b holds sorted
+// positions [b << log2_block, ...) of the list in shared memory; a warp takes its
+// tokens into registers, the blocks see one another's histograms, and every
+// token goes to its place in some block's memory, in the last pass to the lists.
+// It runs beside a fill that keeps the memory busy: with lists and histograms in
+// global memory 32768 tokens took 52 us there, 31 alone.
+struct ShortSmem {
+  uint32_t key[kShortBlock];
+  uint16_t tok[kShortBlock];
+  uint16_t cnt[kSortWarps][kMaxBins];
+  uint32_t hist[kMaxBins];
+  uint32_t base[kMaxBins];
+  uint32_t warp_total[kSortWarps];
+};
+
+MOE_DEV uint32_t load_remote(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) embedding_sort_short_kernel(SortArgs a) {
-  __shared__ SortSmem sm;
+  __shared__ ShortSmem sm;
   griddep_launch_dependents();
-  const int block = blockIdx.x;
-  if (block < a.blocks) first_histogram(a, block, sm.base);
-  for (a.pass = 0; a.pass < a.passes; ++a.pass) {
-    cluster_sync_all();
-    a.key_out = a.lists[2 * (a.pass & 1)];
-    a.tok_out = a.lists[2 * (a.pass & 1) + 1];
-    if (block < a.blocks) sort_pass(a, block, sm);
-    a.key_in = a.key_out;
-    a.tok_in = a.tok_out;
+  const int bins = 1 << a.bits, block = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_warp = a.block / kSortWarps;                      // a multiple of 32
+  const int here = max(0, min(a.block, a.T - block * a.block));   // tokens of this block
+  const int w0 = warp * per_warp, rounds = max(0, (min(here - w0, per_warp) + 31) / 32);
+  const uint32_t below = (1u << lane) - 1;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    uint32_t key[kHeld], tok[kHeld], d[kHeld], peers[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      const int i = w0 + 32 * r + lane;
+      const bool there = r < rounds && i < here;
+      key[r] = !there ? 0u : pass ? sm.key[i] : sort_key(a, block * a.block + i);
+      tok[r] = !there ? 0u : pass ? sm.tok[i] : static_cast<uint32_t>(block * a.block + i);
+      d[r] = there ? (key[r] >> shift) & (bins - 1) : 0xffffffffu;
+    }
+    for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads)
+      reinterpret_cast<uint32_t*>(&sm.cnt[0][0])[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      if (r >= rounds) break;
+      peers[r] = __match_any_sync(0xffffffffu, d[r]);
+      const bool first = d[r] != 0xffffffffu && (peers[r] & below) == 0;
+      // where this round's tokens of the digit go among the warp's
+      uint16_t before = 0;
+      if (first) {
+        before = sm.cnt[warp][d[r]];
+        sm.cnt[warp][d[r]] = static_cast<uint16_t>(before + __popc(peers[r]));
+      }
+      // (in the lower half the digit, in the upper the place)
+      const uint32_t lead = __shfl_sync(0xffffffffu, static_cast<uint32_t>(before), __ffs(peers[r]) - 1);
+      d[r] = d[r] == 0xffffffffu ? d[r] : d[r] | (lead + __popc(peers[r] & below)) << 16;
+      __syncwarp();
+    }
+    __syncthreads();
+    // the block's histogram, and each warp's place in it
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = sm.cnt[w][b];
+        sm.cnt[w][b] = static_cast<uint16_t>(sum);
+        sum += c;
+      }
+      sm.hist[b] = sum;
+    }
+    cluster_sync_all();  // and every block has its tokens in registers
+    uint32_t total = 0, before = 0;
+    if (threadIdx.x < bins) {
+#pragma unroll
+      for (int b = 0; b < kCluster; ++b) {
+        const uint32_t v = load_remote(&sm.hist[threadIdx.x], b);
+        total += v;
+        if (b < block) before += v;
+      }
+    }
+    uint32_t incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.warp_total[warp] = incl;
+    __syncthreads();
+    uint32_t run = incl - total;
+    for (int w = 0; w < warp; ++w) run += sm.warp_total[w];
+    if (threadIdx.x < bins) sm.base[threadIdx.x] = run + before;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      if (r >= rounds || d[r] == 0xffffffffu) continue;
+      const uint32_t digit = d[r] & 0xffffu, pos = sm.base[digit] + sm.cnt[warp][digit] + (d[r] >> 16);
+      if (pass + 1 == a.passes) {
+        a.lists[0][pos] = key[r];
+        a.lists[1][pos] = tok[r];
+      } else {
+        const uint32_t to = pos >> a.log2_block, at = pos & (a.block - 1);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(smem_u32(&sm.key[at]), to)), "r"(key[r]) : "memory");
+        asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(map_to_cta(smem_u32(&sm.tok[at]), to)),
+                     "h"(static_cast<uint16_t>(tok[r]))
+                     : "memory");
+      }
+    }
+    cluster_sync_all();  // the tokens have arrived; nobody reads this block's histogram any more
   }
 }
 
 // Every row of the table: zeros, or `add`.  It runs beside the sort before it
-// and ends after it, so that what waits for this kernel may read both.
+// and ends after it, so that what waits for this kernel may read both.  (In one
+// launch with the sort's cluster, as clusters too, it filled at 5.5 TB/s instead
+// of 7.5: clusters of 8 leave part of the SMs empty.)
 constexpr int kFillThreads = 512;
 constexpr int kFillEach = 4;     // pieces of 8 that a thread has in flight
 constexpr int kFillBlocks = 64;  // of an SM, one after the other (4: 160 us for 1 GB, 64: 142)
@@ -368,8 +458,8 @@ __global__ void __launch_bounds__(kFillThreads) embedding_fill_kernel(float* out
   if (blockIdx.x == 0) {  // the last few elements
     const size_t i = pieces * 8 + threadIdx.x;
     if (i < n) out[i] = add ? __uint_as_float(static_cast<uint32_t>(add[i]) << 16) : 0.f;
+    griddep_wait();  // (a block that waits keeps its place on the SM: one is enough)
   }
-  griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -388,18 +478,18 @@ struct SumArgs {
   int2* long_runs;         // [window_blocks, kSumWarps], with chunks
 };
 
-constexpr int kWindow = 8;     // sorted tokens of a warp
+constexpr int kWindow = 4;     // sorted tokens of a warp
 constexpr int kSumWarps = 8;
 constexpr int kLong = 16;      // tokens past its window that a warp adds alone
 
 // A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
-template <int VEC>
+template <int VEC, bool kF32>
 struct Shape {
-  static constexpr int kVecs = VEC == 8 ? 4 : 8;
+  static constexpr int kVecs = VEC == 1 ? 8 : kF32 ? 2 : 4;
   static constexpr int kColumns = 32 * kVecs * VEC;
 };
-template <int VEC, bool kF32>
-constexpr int kAhead = VEC == 8 && kF32 ? 2 : 4;
+template <int VEC, bool kF32, int kVecs>
+constexpr int kAhead = VEC == 1 ? 4 : 64 / (kVecs * Piece<VEC, kF32>::kWords);  // 64 registers
 
 // A lane's pieces of one row; lanes past the last column read another's (a load
 // under a condition would be waited for on the spot).
@@ -412,19 +502,19 @@ MOE_DEV void load_row(const void* src, uint32_t row, int D, int v0, int nv, Piec
 
 // acc += rows row(0) .. row(n - 1) of `src`, in that order, R in flight (the
 // last of them again where there are fewer left).
-template <int VEC, bool kF32, typename Index>
-MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, float (&acc)[Shape<VEC>::kVecs][VEC]) {
-  constexpr int R = kAhead<VEC, kF32>;
+template <int VEC, bool kF32, int kVecs, typename Index>
+MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, float (&acc)[kVecs][VEC]) {
+  constexpr int R = kAhead<VEC, kF32, kVecs>;
 #pragma unroll 1
   for (int j = 0; j < n; j += R) {
-    Piece<VEC, kF32> v[R][Shape<VEC>::kVecs];
+    Piece<VEC, kF32> v[R][kVecs];
 #pragma unroll
     for (int r = 0; r < R; ++r) load_row(src, row(min(j + r, n - 1)), D, v0, nv, v[r]);
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (j + r < n)
 #pragma unroll
-        for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+        for (int i = 0; i < kVecs; ++i)
 #pragma unroll
           for (int e = 0; e < VEC; ++e) acc[i][e] += v[r][i][e];
   }
@@ -434,19 +524,20 @@ MOE_DEV void add_rows(const void* src, int D, int v0, int nv, int n, Index row, 
 // `job` of chunks x turns of columns.
 template <int VEC, bool kF32>
 MOE_DEV void sum_chunk(const SumArgs& a, int job) {
+  constexpr int kVecs = Shape<VEC, kF32>::kVecs;
   const int c = job % a.chunks, lane = threadIdx.x & 31;
-  const int nv = a.D / VEC, v0 = job / a.chunks * 32 * Shape<VEC>::kVecs + lane;
+  const int nv = a.D / VEC, v0 = job / a.chunks * 32 * kVecs + lane;
   if (v0 - lane >= nv) return;
   const size_t p0 = static_cast<size_t>(c) * a.chunk;
   const uint32_t k = a.key[p0];
   if (k != a.key[p0 + a.chunk - 1] || k >= static_cast<uint32_t>(a.V)) return;
-  float acc[Shape<VEC>::kVecs][VEC] = {};
+  float acc[kVecs][VEC] = {};
   for (int j = 0; j < a.chunk; j += 32) {
     const uint32_t tok = a.tok[p0 + j + lane];
     add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, 32, [&](int r) { return __shfl_sync(0xffffffffu, tok, r); }, acc);
   }
 #pragma unroll
-  for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+  for (int i = 0; i < kVecs; ++i)
     if (v0 + 32 * i < nv)
       store_vec<VEC, true>(a.part, static_cast<size_t>(c) * a.D + static_cast<size_t>(v0 + 32 * i) * VEC, acc[i]);
 }
@@ -485,11 +576,11 @@ MOE_DEV void add_vec(float* p, const float (&v)[VEC]) {
   }
 }
 
-template <int VEC>
-MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float (&acc)[Shape<VEC>::kVecs][VEC]) {
+template <int VEC, int kVecs>
+MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float (&acc)[kVecs][VEC]) {
   float* dst = a.d_table + static_cast<size_t>(v) * a.D;
 #pragma unroll
-  for (int i = 0; i < Shape<VEC>::kVecs; ++i)
+  for (int i = 0; i < kVecs; ++i)
     if (v0 + 32 * i < nv) {
       float o[VEC];
 #pragma unroll
@@ -503,8 +594,9 @@ MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float
 // the first chunk that lies inside, the chunks' sums, the rows behind them;
 // every warp takes a share.
 template <int VEC, bool kF32>
-MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], float (&red)[kSumWarps][Shape<VEC>::kColumns]) {
-  constexpr int kVecs = Shape<VEC>::kVecs, kColumns = Shape<VEC>::kColumns;
+MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], int turn0, int turn1,
+                           float (&red)[kSumWarps][Shape<VEC, kF32>::kColumns]) {
+  constexpr int kVecs = Shape<VEC, kF32>::kVecs, kColumns = Shape<VEC, kF32>::kColumns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nv = a.D / VEC;
 #pragma unroll 1
@@ -516,8 +608,8 @@ MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], floa
     const int tail = c0 < c1 ? c1 * a.chunk : end;
     auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
 #pragma unroll 1
-    for (int col = 0; col < nv; col += 32 * kVecs) {
-      const int v0 = col + lane;
+    for (int turn = turn0; turn < turn1; ++turn) {
+      const int col = turn * 32 * kVecs, v0 = col + lane;
       float acc[kVecs][VEC] = {};
       const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
       add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
@@ -546,24 +638,25 @@ MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], floa
   }
 }
 
-// The long runs that the windows of one block have found.
+// The long runs that the windows of one block have found, a turn of columns a
+// block.
 template <int VEC, bool kF32>
 __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_long_kernel(SumArgs a) {
-  __shared__ float red[kSumWarps][Shape<VEC>::kColumns];
+  __shared__ float red[kSumWarps][Shape<VEC, kF32>::kColumns];
   __shared__ int2 runs[kSumWarps];
   griddep_wait();
   if (threadIdx.x < kSumWarps) runs[threadIdx.x] = a.long_runs[blockIdx.x * kSumWarps + threadIdx.x];
   __syncthreads();
-  add_long_runs<VEC, kF32>(a, runs, red);
+  add_long_runs<VEC, kF32>(a, runs, blockIdx.y, blockIdx.y + 1, red);
 }
 
 // A warp a window of sorted tokens: the rows whose tokens begin there.  Blocks
 // past the windows' sum the chunks; the long runs then wait for those.
 template <int VEC, bool kF32>
 __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumArgs a) {
-  constexpr int kVecs = Shape<VEC>::kVecs, R = kAhead<VEC, kF32>;
+  constexpr int kVecs = Shape<VEC, kF32>::kVecs, R = kAhead<VEC, kF32, kVecs>;
   static_assert(kWindow % R == 0);
-  __shared__ float red[kSumWarps][Shape<VEC>::kColumns];
+  __shared__ float red[kSumWarps][Shape<VEC, kF32>::kColumns];
   __shared__ int2 runs[kSumWarps];
   griddep_launch_dependents();
   griddep_wait();
@@ -618,7 +711,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
           if (j + 1 < stop && !(begins >> (j + 1) & 1)) continue;
           if (j + 1 == kWindow)
             add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past, [&](int q) { return a.tok[p0 + kWindow + q]; }, acc);
-          write_row<VEC>(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
+          write_row(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
         }
       }
     }
@@ -629,7 +722,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
     return;
   }
   __syncthreads();
-  add_long_runs<VEC, kF32>(a, runs, red);
+  add_long_runs<VEC, kF32>(a, runs, 0, (nv + 32 * kVecs - 1) / (32 * kVecs), red);
 }
 
 // fp32 rows are read 32 bytes at a time.
@@ -639,11 +732,15 @@ size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int VEC, bool kF32>
 cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
-  const int turns = (a.D + Shape<VEC>::kColumns - 1) / Shape<VEC>::kColumns;
+  const int turns = (a.D + Shape<VEC, kF32>::kColumns - 1) / Shape<VEC, kF32>::kColumns;
   const unsigned grid = a.window_blocks + static_cast<unsigned>((static_cast<long long>(a.chunks) * turns + kSumWarps - 1) / kSumWarps);
   const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(grid), dim3(32 * kSumWarps), 0, s, true, a);
   if (e != cudaSuccess || !a.chunks) return e;
-  return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(a.window_blocks), dim3(32 * kSumWarps), 0, s, true, a);
+  return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(a.window_blocks, turns), dim3(32 * kSumWarps), 0, s, true, a);
+}
+
+size_t hist_bytes(int T, const SortPlan& p) {
+  return T <= kShortList ? 0 : static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits);
 }
 
 int window_blocks(int T) { return (T + kSumWarps * kWindow - 1) / (kSumWarps * kWindow); }
@@ -656,7 +753,7 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s) {
 
 size_t embedding_bwd_scratch_bytes(int T, int V, int D) {
   const SortPlan p = sort_plan(T, V);
-  return padded(static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits)) +
+  return padded(hist_bytes(T, p)) +
          4 * padded(static_cast<size_t>(T) * sizeof(uint32_t)) + padded(static_cast<size_t>(p.chunks) * D * sizeof(float)) +
          padded(p.chunks ? window_blocks(T) * kSumWarps * sizeof(int2) : 0);
 }
@@ -677,8 +774,9 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   q.block = p.block;
   q.blocks = p.blocks;
   q.bits = p.bits;
+  while ((1 << q.log2_block) < p.block) ++q.log2_block;
   q.passes = p.passes;
-  q.hist = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits)));
+  q.hist = reinterpret_cast<uint32_t*>(take(hist_bytes(a.T, p)));
   for (auto& l : q.lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
   int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? window_blocks(a.T) * kSumWarps * sizeof(int2) : 0));
@@ -701,7 +799,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   e = launch_kernel(embedding_fill_kernel, dim3(static_cast<unsigned>(std::min((n + per - 1) / per, fit))), dim3(kFillThreads),
                     0, s, a.T > 0, a.d_table, static_cast<const uint16_t*>(a.add), n);
   if (e != cudaSuccess || a.T == 0) return e;
-  const int last = (p.passes - 1) & 1;
+  const int last = a.T <= kShortList ? 0 : (p.passes - 1) & 1;
   const SumArgs m{a.d_out, a.add, q.lists[2 * last], q.lists[2 * last + 1], part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks,
                   window_blocks(a.T), long_runs};
   if (a.D % 8 == 0 && (!a.d_fp32 || on32(a.d_out))) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
