@@ -658,6 +658,23 @@ cudaError_t tensor_map_blocks(CUtensorMap* m, const void* ptr, uint64_t rows, ui
   return make_weight_map(m, ptr, rows, cols, nblk, box_rows);
 }
 
+cudaError_t tensor_map_block_major(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                                   uint32_t box_blocks) {
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    cudaError_t e = get_encoder();
+    if (e != cudaSuccess) return e;
+  }
+  cuuint64_t dims[3] = {64, rows, blocks};
+  cuuint64_t strides[2] = {128, rows * 128};
+  cuuint32_t box[3] = {64, box_rows, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t tensor_map_f32_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
                               uint32_t box0, uint32_t box1) {
   {

@@ -279,6 +279,11 @@ cudaError_t tensor_map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64
 // read zeros (grouped_gemm.cu).
 cudaError_t tensor_map_blocks(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t nblk,
                               uint32_t box_rows = 64);
+// 3-D bf16 TMA descriptor of a matrix that is stored block by block of 64
+// columns, [blocks][rows][64], with a {64, box_rows, box_blocks} box and the
+// 128-byte swizzle; zero fill outside (grouped_gemm.cu).
+cudaError_t tensor_map_block_major(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                                   uint32_t box_blocks);
 // 3-D fp32 TMA descriptor of a packed [d2][d1][d0] array with a {box0, box1, 1}
 // box: 64-byte swizzle for 16-float boxes (128-byte for 32), none otherwise.
 cudaError_t tensor_map_f32_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,

@@ -13,14 +13,16 @@
 //
 // Backward, by pieces of the vocabulary:
 //   dz_v = a 2^(c z_v - lse / ln 2)  (+ the targets' own terms)
-// vocab_kernel<kDz> recomputes z and stores dz of the piece as bf16 [T, Vc];
+// vocab_kernel<kDz> recomputes z and stores dz of the piece as bf16;
 // vocab_kernel<kGrad> runs both products of it in one launch,
 //   dx [T, D] += dz W[piece],   dW[piece] = dz^T x,
 // so that the tiles of one fill the last wave of the other.  The values at the
 // targets (a q - p, where the two terms nearly cancel for a token that is
-// known well) come in fp32 from vocab_ce_rows_kernel or
-// vocab_distill_rows_kernel and replace the epilogue's.
-// dz is the one intermediate that is rounded to fewer than 32 bits: a bf16
+// known well) are formed in fp32 apart from it: a label's by vocab_ce_rows_kernel,
+// for the epilogue to store, a teacher's entries' by vocab_distill_targets_kernel,
+// over what the epilogue has stored.
+// dz is stored block by block of 64 columns, [Vc / 64][T][64], so that a warp's
+// 32 x 64 box is 4 KB in a row.  It is the one intermediate that is rounded to fewer than 32 bits: a bf16
 // operand is what the tensor cores take at full rate, and a relative rounding
 // of 2^-9 of each term averages out in sums over V or T.
 //
@@ -62,7 +64,7 @@ struct VocabArgs : VocabWork {
   int v0, Vc, Vcp;         // kDz, kGrad: the piece's first row, its rows, and those rounded up to 64
   float c;
   unsigned int* dev_err;
-  // targets: labels (K = 0), or sorted (id << 8 | entry) keys [T, K]
+  // targets: labels (K = 0), or kStats: sorted (id << 8 | entry) keys [T, K]
   const void* labels;
   int labels64;
   const uint32_t* keys;
@@ -72,7 +74,7 @@ struct VocabArgs : VocabWork {
   int rows_padded;
   const float* row_a;      // kDz: a of each row, lse log2(e)
   const float* row_l;
-  const uint16_t* value;   // kDz: dz at the targets [T] or [T, K]
+  const uint16_t* value;   // kDz, K = 0: dz at the labels [T]
   int direct[2];           // kGrad, dx and dW: stored as bf16; otherwise fp32 partials
   int accumulate;          // dx partials are added to those of the piece before
   const float* dx_part;    // [splits, T, D]
@@ -101,37 +103,34 @@ MOE_DEV long long load_index(const void* p, int is64, size_t i) {
 // A row's targets in ascending order of their columns.
 struct Targets {
   const uint32_t* keys;
-  int left;      // keys that remain, with the current one
-  int id;        // current column, or kNoTarget
+  int left;        // keys behind the current one
+  uint32_t ahead;  // the first of them, asked for before it is needed
+  int id;          // current column, or kNoTarget
   int entry;
 
-  MOE_DEV void set() {
-    if (left > 0) {
-      const uint32_t k = *keys;
-      id = static_cast<int>(k >> 8);
-      entry = static_cast<int>(k & 255u);
-    } else {
-      id = kNoTarget;
-    }
-  }
   MOE_DEV void step() {
-    ++keys;
-    --left;
-    set();
+    if (left == 0) {
+      id = kNoTarget;
+      return;
+    }
+    id = static_cast<int>(ahead >> 8);
+    entry = static_cast<int>(ahead & 255u);
+    if (--left > 0) ahead = *keys++;
   }
   // From the first target at or past column `col`.
   MOE_DEV void start(const VocabArgs& p, int row, int col) {
     left = 0;
     id = kNoTarget;
     entry = 0;
+    ahead = 0;
     keys = nullptr;
     if (row >= p.T) return;
     if (p.K == 0) {
       const long long l = load_index(p.labels, p.labels64, row);
       id = l >= col && l < p.V ? static_cast<int>(l) : kNoTarget;
-      left = 1;
       return;
     }
+    if (p.keys == nullptr) return;  // kDz: those come after it
     const uint32_t* k = p.keys + static_cast<size_t>(row) * p.K;
     const uint32_t want = static_cast<uint32_t>(col) << 8;
     int lo = 0, hi = p.K;
@@ -142,7 +141,8 @@ struct Targets {
     }
     keys = k + lo;
     left = p.K - lo;
-    set();
+    if (left > 0) ahead = *keys++;
+    step();
   }
   // Past the targets of the columns in between, which another warp has: few as
   // a rule, and a search where they are not.
@@ -154,10 +154,6 @@ struct Targets {
   MOE_DEV void next(const VocabArgs& p) {
     if (p.K == 0) id = kNoTarget;
     else step();
-  }
-  // Position of the current target among the row's keys.
-  MOE_DEV size_t at(const VocabArgs& p, int row) const {
-    return p.K == 0 ? static_cast<size_t>(row) : static_cast<size_t>(row + 1) * p.K - left;
   }
 };
 
@@ -422,15 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           put_row(mine, packed);
           const int end = p.v0 + cc + 64;
-          while (tg.id < end) {
+          if (tg.id < end) {
             const int j = tg.id - (end - 64);
-            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) = p.value[tg.at(p, row)];
+            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) =
+                p.value[row];
             tg.next(p);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&mapOut0, smem_u32(box), cc, warp_row0);
+            tma_store_3d(&mapOut0, smem_u32(box), 0, warp_row0, cc / 64);
             bulk_commit_group();
           }
         }
@@ -506,7 +503,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Rows: what the products need of them and what is left to do after them
 // ---------------------------------------------------------------------------
 constexpr int kRowWarps = 8;
-constexpr int kMaxK = MOE_MAX_TEACHER;
 
 // (maximum, sum) pairs joined; an empty one is (-inf, 0).
 MOE_DEV void join(float& m, float& s, float m2, float s2) {
@@ -516,13 +512,14 @@ MOE_DEV void join(float& m, float& s, float m2, float s2) {
   m = n;
 }
 
-// The teacher's entries of one row, by one warp, kPerLane of each lane: entry
-// j = lane + 32 i.  Entries outside the vocabulary or of -inf are none.
+// The teacher's entries of one row, by one warp: entry j = lane + 32 i in slot i
+// of kSlots = ceil(K / 32), rounded up to a power of two.  Entries outside the
+// vocabulary or of -inf are none.
+template <int kSlots>
 struct Teacher {
-  float p[kMaxK / 32];      // probability (0 where there is none)
-  float log_p[kMaxK / 32];
-  int id[kMaxK / 32];       // or -1
-  float mass;               // 1, or 0 for a row without entries
+  float p[kSlots];      // probability (0 where there is none)
+  float log_p[kSlots];
+  int id[kSlots];       // or -1
 };
 
 MOE_DEV float warp_max(float v) {
@@ -536,19 +533,24 @@ MOE_DEV float warp_sum(float v) {
   return v;
 }
 
-MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, Teacher& out) {
+MOE_DEV float teacher_logit(const VocabTargets& t, size_t at) {
+  return t.logits_fp32 ? static_cast<const float*>(t.logits)[at]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(t.logits)[at]);
+}
+
+template <int kSlots>
+MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, Teacher<kSlots>& out) {
   const int lane = threadIdx.x & 31;
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     out.id[i] = -1;
     out.p[i] = -INFINITY;
     const int j = lane + 32 * i;
-    if (32 * i < t.K && j < t.K) {
+    if (j < t.K) {
       const size_t at = static_cast<size_t>(row) * t.K + j;
       const long long id = load_index(t.ids, t.ids64, at);
-      const float l = t.logits_fp32 ? static_cast<const float*>(t.logits)[at]
-                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(t.logits)[at]);
+      const float l = teacher_logit(t, at);
       if (id >= 0 && id < V) {
         out.id[i] = static_cast<int>(id);
         out.p[i] = l * inv_tau;
@@ -560,33 +562,34 @@ MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, 
   const float ref = top == -INFINITY ? 0.f : top;
   float total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     out.log_p[i] = out.p[i] - ref;
     out.p[i] = expf(out.log_p[i]);
     total += out.p[i];
   }
   total = warp_sum(total);
-  out.mass = total == 0.f ? 0.f : 1.f;  // NaN entries keep their row's mass
   const float log_total = logf(total), inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     out.p[i] *= inv;
     out.log_p[i] -= log_total;
   }
 }
 
 // Sorts the row's keys (id << 8 | entry; none: all ones) in the warp's buffer.
-MOE_DEV void sort_keys(uint32_t* k, int K, const Teacher& t) {
+template <int kSlots>
+MOE_DEV void sort_keys(uint32_t* k, const Teacher<kSlots>& t) {
   const int lane = threadIdx.x & 31;
-  int n = 32;
-  while (n < K) n <<= 1;
+  constexpr int n = 32 * kSlots;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     const int j = lane + 32 * i;
-    if (j < n) k[j] = t.id[i] >= 0 ? (static_cast<uint32_t>(t.id[i]) << 8 | static_cast<uint32_t>(j)) : 0xffffffffu;
+    k[j] = t.id[i] >= 0 ? (static_cast<uint32_t>(t.id[i]) << 8 | static_cast<uint32_t>(j)) : 0xffffffffu;
   }
   __syncwarp();
+#pragma unroll 1
   for (int size = 2; size <= n; size <<= 1)
+#pragma unroll 1
     for (int d = size >> 1; d > 0; d >>= 1) {
       for (int i = lane; i < n / 2; i += 32) {
         const int a = 2 * i - (i & (d - 1)), b = a + d;
@@ -601,19 +604,20 @@ MOE_DEV void sort_keys(uint32_t* k, int K, const Teacher& t) {
 }
 
 // Forward of distillation: the rows' sorted keys.
+template <int kSlots>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets t, int T, int V, float inv_tau,
                                                                     uint32_t* keys, float* target) {
-  __shared__ uint32_t buf[kRowWarps][kMaxK];
+  __shared__ uint32_t buf[kRowWarps][32 * kSlots];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kRowWarps + warp;
   if (row >= T) return;
-  Teacher te;
+  Teacher<kSlots> te;
   read_teacher(t, row, V, inv_tau, te);
-  sort_keys(buf[warp], t.K, te);
+  sort_keys(buf[warp], te);
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     const int j = lane + 32 * i;
     if (j < t.K) {
       keys[static_cast<size_t>(row) * t.K + j] = buf[warp][j];
@@ -630,6 +634,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets
 // be off by 2^-24 of their size, is never formed.
 constexpr int kFinishWarps = 32;
 
+template <int kSlots>
 __global__ void __launch_bounds__(32 * kFinishWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
                         float c, float inv_tau, float* loss, float* lse) {
@@ -667,24 +672,24 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
   }
   const float log_s = log2f(s);
   if (lane == 0) lse[row] = (m + log_s) * kLn2;
-  if (t.K == 0) {
+  if constexpr (kSlots == 0) {
     if (lane == 0) {
       const long long id = load_index(t.ids, t.ids64, row);
       loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
     }
-    return;
-  }
-  Teacher te;
-  read_teacher(t, row, V, inv_tau, te);
-  float sum = 0.f;
+  } else {
+    Teacher<kSlots> te;
+    read_teacher(t, row, V, inv_tau, te);
+    float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) {
-    const int j = lane + 32 * i;
-    if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
-      sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+    for (int i = 0; i < kSlots; ++i) {
+      const int j = lane + 32 * i;
+      if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+        sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) loss[row] = sum;
   }
-  sum = warp_sum(sum);
-  if (lane == 0) loss[row] = sum;
 }
 
 // Backward of cross entropy: a and lse log2(e) of each row, and dz at its label,
@@ -705,41 +710,62 @@ __global__ void __launch_bounds__(256) vocab_ce_rows_kernel(const float* d_loss,
   value[row] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
 }
 
-// Backward of distillation: the same, with the sorted keys and dz at each of them,
-//   d_loss / temperature (q - p),
-// p summed over the entries of one id.
+// Backward of distillation: the same two numbers of each row; a token without
+// entries has neither.
 __global__ void __launch_bounds__(32 * kRowWarps)
-    vocab_distill_rows_kernel(const float* d_loss, const float* lse, const float* target, VocabTargets t, int T, int V,
-                              float inv_tau, float* row_a, float* row_l, uint32_t* keys, uint16_t* value) {
-  __shared__ uint32_t buf[kRowWarps][kMaxK];
-  __shared__ float prob[kRowWarps][kMaxK];
+    vocab_distill_rows_kernel(const float* d_loss, const float* lse, VocabTargets t, int T, int V, float inv_tau,
+                              float* row_a, float* row_l) {
   griddep_launch_dependents();
   griddep_wait();
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (row >= T) return;
+  bool any = false;
+  for (int j = lane; j < t.K; j += 32) {
+    const size_t at = static_cast<size_t>(row) * t.K + j;
+    const long long id = load_index(t.ids, t.ids64, at);
+    any |= id >= 0 && id < V && !(teacher_logit(t, at) * inv_tau == -INFINITY);
+  }
+  any = __any_sync(0xffffffffu, any);
+  if (lane == 0) {
+    row_a[row] = any ? d_loss[row] * inv_tau : 0.f;
+    row_l[row] = lse[row] * kLog2e;
+  }
+}
+
+// dz at the teacher's entries of a piece's columns,
+//   d_loss / temperature (q - p),
+// p summed over the entries of one id, in place of what the product's epilogue
+// has stored there.  (In the epilogue itself, a row's entries one after the
+// other, 64 of them cost 40 us of 425 at 8192 x 768 x 50001, and 225 of them 34 of
+// 72 at 353 x 320 x 78226.)  No programmatic launch: blocks that start while the
+// product still holds most SMs crowd the few that are free, and 353 rows of 225
+// entries then take 68 us instead of 22.
+template <int kSlots>
+__global__ void __launch_bounds__(32 * kRowWarps)
+    vocab_distill_targets_kernel(const float* row_a, const float* lse, const float* target, VocabTargets t, int T, int V,
+                                 float inv_tau, int v0, int Vc, uint16_t* dz) {
+  __shared__ uint32_t buf[kRowWarps][32 * kSlots];
+  __shared__ float prob[kRowWarps][32 * kSlots];
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kRowWarps + warp;
   if (row >= T) return;
-  Teacher te;
+  const float d = row_a[row], l = lse[row];
+  if (d == 0.f) return;
+  Teacher<kSlots> te;
   read_teacher(t, row, V, inv_tau, te);
 #pragma unroll
-  for (int i = 0; i < kMaxK / 32; ++i) prob[warp][lane + 32 * i] = te.p[i];
-  sort_keys(buf[warp], t.K, te);
-  const float d = te.mass == 0.f ? 0.f : d_loss[row] * inv_tau;
-  const float l = lse[row];
-  if (lane == 0) {
-    row_a[row] = d;
-    row_l[row] = l * kLog2e;
-  }
+  for (int i = 0; i < kSlots; ++i) prob[warp][lane + 32 * i] = te.p[i];
+  sort_keys(buf[warp], te);
   for (int i = lane; i < t.K; i += 32) {
-    const uint32_t key = buf[warp][i];
-    const size_t at = static_cast<size_t>(row) * t.K;
-    keys[at + i] = key;
-    if (key == 0xffffffffu) continue;
+    const uint32_t key = buf[warp][i], id = key >> 8;
+    const int column = static_cast<int>(id) - v0;
+    if (key == 0xffffffffu || column < 0 || column >= Vc || (i > 0 && buf[warp][i - 1] >> 8 == id)) continue;
     float p = 0.f;
-    int a = i;
-    while (a > 0 && (buf[warp][a - 1] >> 8) == (key >> 8)) --a;
-    for (; a < t.K && (buf[warp][a] >> 8) == (key >> 8); ++a) p += prob[warp][buf[warp][a] & 255u];
-    const float q = expf(target[at + (key & 255u)] * inv_tau - l);
-    value[at + i] = static_cast<uint16_t>(pack_bf16x2(d * (q - p), 0.f) & 0xffffu);
+    for (int a = i; a < t.K && buf[warp][a] >> 8 == id; ++a) p += prob[warp][buf[warp][a] & 255u];
+    const float q = expf(target[static_cast<size_t>(row) * t.K + (key & 255u)] * inv_tau - l);
+    dz[(static_cast<size_t>(column >> 6) * T + row) * 64 + (column & 63)] =
+        static_cast<uint16_t>(pack_bf16x2(d * (q - p), 0.f) & 0xffffu);
   }
 }
 
@@ -847,7 +873,6 @@ struct Take {
 struct BackwardRegions {
   float* row_a;
   float* row_l;
-  uint32_t* keys;
   uint16_t* value;
   uint16_t* dz;
   float* dx_part;
@@ -858,12 +883,17 @@ size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const Backwar
   const size_t rows = static_cast<size_t>(T);
   r->row_a = t.get<float>(rows);
   r->row_l = t.get<float>(rows);
-  r->keys = t.get<uint32_t>(rows * K);
-  r->value = t.get<uint16_t>(rows * std::max(K, 1));
+  r->value = t.get<uint16_t>(K == 0 ? rows : 0);
   r->dz = t.get<uint16_t>(rows * b.piece);
   r->dx_part = t.get<float>(b.pieces > 1 || b.splits_x > 1 ? rows * D * b.splits_x : 0);
   r->dw_part = t.get<float>(b.splits_w > 1 ? static_cast<size_t>(V) * D * b.splits_w : 0);
   return t.off;
+}
+
+// The kernel for a teacher of K entries.
+template <typename Kernel>
+Kernel by_slots(int K, Kernel k1, Kernel k2, Kernel k4, Kernel k8) {
+  return K <= 32 ? k1 : K <= 64 ? k2 : K <= 128 ? k4 : k8;
 }
 
 cudaError_t launch_sum(const float* part, int n_parts, size_t n, uint16_t* out, cudaStream_t s) {
@@ -908,13 +938,17 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
   const float inv_tau = 1.f / a.temperature;
   if (v.K) {
-    e = launch_kernel(vocab_keys_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false, a.targets,
-                      a.T, a.V, inv_tau, keys, v.target);
+    auto* k = by_slots(v.K, vocab_keys_kernel<1>, vocab_keys_kernel<2>, vocab_keys_kernel<4>, vocab_keys_kernel<8>);
+    e = launch_kernel(k, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false, a.targets, a.T, a.V, inv_tau,
+                      keys, v.target);
     if (e != cudaSuccess) return e;
   }
   e = launch_vocab<kStats>(std::min(st.pairs[kStats], v.items), mx, mw, mx, mx, mx, v, s, v.K != 0);
   if (e != cudaSuccess) return e;
-  return launch_kernel(vocab_finish_kernel, dim3(ceil_div(a.T, 32)), dim3(32 * kFinishWarps), 0, s, true,
+  auto* finish = v.K == 0 ? vocab_finish_kernel<0>
+                          : by_slots(v.K, vocab_finish_kernel<1>, vocab_finish_kernel<2>, vocab_finish_kernel<4>,
+                                     vocab_finish_kernel<8>);
+  return launch_kernel(finish, dim3(ceil_div(a.T, 32)), dim3(32 * kFinishWarps), 0, s, true,
                        static_cast<const float2*>(v.part), 2 * f.runs, f.rows_padded, a.targets,
                        static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau, a.loss, a.lse);
 }
@@ -940,7 +974,6 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   v.K = K;
   v.labels = a.targets.ids;
   v.labels64 = a.targets.ids64;
-  v.keys = r.keys;
   v.row_a = r.row_a;
   v.row_l = r.row_l;
   v.value = r.value;
@@ -960,7 +993,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   if (e != cudaSuccess) return e;
   const float inv_tau = 1.f / a.temperature;
   e = K ? launch_kernel(vocab_distill_rows_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
-                        a.d_loss, a.lse, a.target, a.targets, a.T, a.V, inv_tau, r.row_a, r.row_l, r.keys, r.value)
+                        a.d_loss, a.lse, a.targets, a.T, a.V, inv_tau, r.row_a, r.row_l)
         : launch_kernel(vocab_ce_rows_kernel, dim3(ceil_div(a.T, 256)), dim3(256), 0, s, false, a.d_loss, a.d_lse,
                         a.loss, a.lse, a.targets, a.T, a.V, r.row_a, r.row_l, r.value);
   if (e != cudaSuccess) return e;
@@ -969,11 +1002,19 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
     v.Vc = std::min(b.piece, a.V - v.v0);
     v.Vcp = ceil_div(v.Vc, 64) * 64;
     v.accumulate = i > 0;
-    if ((e = tensor_map_blocks(&mz, r.dz, a.T, v.Vcp, 2, 128)) != cudaSuccess) return e;
-    if ((e = tensor_map_2d(&mz_out, r.dz, a.T, v.Vcp, 32, 64)) != cudaSuccess) return e;
+    if ((e = tensor_map_block_major(&mz, r.dz, a.T, v.Vcp / 64, 128, 2)) != cudaSuccess) return e;
+    if ((e = tensor_map_block_major(&mz_out, r.dz, a.T, v.Vcp / 64, 32, 1)) != cudaSuccess) return e;
     v.VocabWork::operator=(dz_work(b, a.D, v.Vc));
     e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, true);
     if (e != cudaSuccess) return e;
+    if (K) {
+      auto* k = by_slots(K, vocab_distill_targets_kernel<1>, vocab_distill_targets_kernel<2>,
+                         vocab_distill_targets_kernel<4>, vocab_distill_targets_kernel<8>);
+      e = launch_kernel(k, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
+                        static_cast<const float*>(r.row_a), a.lse, a.target, a.targets, a.T, a.V, inv_tau, v.v0, v.Vc,
+                        r.dz);
+      if (e != cudaSuccess) return e;
+    }
     v.VocabWork::operator=(grad_work(b, a.T, v.Vc));
     e = launch_vocab<kGrad>(std::min(st.pairs[kGrad], v.n_units[0] + v.n_units[1]), mx, mw, mz, mdx, mdw, v, s, true);
     if (e != cudaSuccess) return e;

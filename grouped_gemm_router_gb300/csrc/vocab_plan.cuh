@@ -31,6 +31,13 @@ struct VocabWork {
   int splits[2], n_units[2], tiles_m[2], tiles_n;
 };
 
+// What a unit takes, in k blocks: its own, or the epilogue that runs beside the
+// next unit's (2.9 us where a block is 0.53).
+__host__ MOE_DEV int unit_cost(int nkb, int splits) {
+  const int blocks = (nkb + splits - 1) / splits;
+  return blocks > 5 ? blocks : 5;
+}
+
 __host__ MOE_DEV int least(int a, int b) { return a < b ? a : b; }
 
 struct Unit {
@@ -62,8 +69,7 @@ struct Walk {
         i -= len_a;
         which = small;
         const int r = na % npairs;
-        const int cost_a = (p.nkb[big] + p.splits[big] - 1) / p.splits[big];
-        const int cost_b = (p.nkb[small] + p.splits[small] - 1) / p.splits[small];
+        const int cost_a = unit_cost(p.nkb[big], p.splits[big]), cost_b = unit_cost(p.nkb[small], p.splits[small]);
         const int fill = r == 0 ? 0 : least(nb, (npairs - r) * (cost_a / cost_b));
         int len_f = 0;
         const int first = pair - r;
@@ -156,7 +162,8 @@ inline BackwardPlan backward_plan(int T, int D, int V) {
   // along it.
   const long kx = ceil_div(b.piece, kBK), kw = ceil_div(T, kBK);
   const long ux = static_cast<long>(b.nmt) * b.ndt, uw = static_cast<long>(ceil_div(b.piece, kTile)) * b.ndt;
-  const long share = std::max<long>(kMinSplitBlocks, (ux * kx + uw * kw + kPlanPairs - 1) / kPlanPairs);
+  const long work = ux * unit_cost(kx, 1) + uw * unit_cost(kw, 1);
+  const long share = std::max<long>(kMinSplitBlocks, (work + kPlanPairs - 1) / kPlanPairs);
   b.splits_x = static_cast<int>(std::min<long>(kMaxSplits, (kx + share - 1) / share));
   b.splits_w = b.pieces > 1 ? 1 : static_cast<int>(std::min<long>(kMaxSplits, (kw + share - 1) / share));
   return b;
