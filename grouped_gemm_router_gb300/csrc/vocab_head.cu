@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       // x and W are read again by other pairs, dz and the pairs are written for
       // later: kept over them, kDz took 1450 us instead of 1500 (32768 x 768 x
-      // 50001) and 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less.
+      // 50001) and 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less
+      // (and 72 us instead of 234 at 1 x 1664 x 61514, where all read one row).
       const uint64_t pol = kMode == kGrad ? l2_policy_evict_normal() : l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
@@ -223,6 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && walk.next(p, pair, npairs, u)) {
         const int m0 = u.m * kTile + 128 * rank, n0 = u.n * kTile + 128 * rank;
+        // x past the last token is not loaded (zeros at best): few tokens are read
+        // by all pairs at once, and then every read counts
+        const bool load_x = kMode == kGrad || m0 < p.T, peer_x = kMode == kGrad || u.m * kTile + 128 < p.T;
+        const uint32_t bytes = 2 * kStageBytes - (peer_x ? 0 : kOperandBytes);
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&ctl.empty[stage]), phase ^ 1u, abort_flag, dev_err)) {
             ok = false;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t full_leader = map_to_cta(smem_u32(&ctl.full[stage]), 0);
           const uint32_t sa = smem_base + stage * kStageBytes, sb = sa + kOperandBytes;
-          if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), 2 * kStageBytes);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), bytes);
           if constexpr (kMode == kGrad) {
             if (u.which == 0) {  // dz rows, W's rows as k
               tma_load_3d_pair(sa, &mapZ, full_leader, 0, m0, kb * (kBK / 64), pol);
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(sb, &mapX, full_leader, 0, kb * kBK, n0 / 64, pol);
             }
           } else {
-            tma_load_3d_pair(sa, &mapX, full_leader, 0, m0, kb * (kBK / 64), pol);
+            if (load_x) tma_load_3d_pair(sa, &mapX, full_leader, 0, m0, kb * (kBK / 64), pol);
             tma_load_3d_pair(sb, &mapW, full_leader, 0, p.v0 + n0, kb * (kBK / 64), pol);
           }
           ++issued;
@@ -647,7 +652,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
   float m = -INFINITY, s = 0.f;
   if (row0 + lane < T) {
     const float2* mine = part + row0 + lane;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 16;
     for (int i = warp; i < parts; i += kBatch * kFinishWarps) {
       float2 v[kBatch];
 #pragma unroll

@@ -413,7 +413,8 @@ moe_status moe_cross_entropy_forward(const void* x, const void* W, const void* l
  * d_loss [T] fp32 (not read where a token has no loss); d_lse [T] fp32 or
  * NULL; loss and lse: the forward's.  z is computed again, piece by piece of
  * the vocabulary; dz is rounded to bf16 for its two products, whose sums are
- * fp32. */
+ * fp32.  A token with neither gradient has dx = 0 whatever its x holds, but dW
+ * takes 0 x, so x has to be finite. */
 moe_status moe_cross_entropy_backward(const float* d_loss, const float* d_lse, const void* x,
                                       const void* W, const void* labels, moe_index_type labels_type,
                                       const float* loss, const float* lse, int32_t T, int32_t D,

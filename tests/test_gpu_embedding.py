@@ -62,7 +62,7 @@ def _check_backward(moe, ids, d_out, V, scale, add):
                                                       (F32, False, torch.int32), (F32, True, torch.int64)])
 @pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 300, 64), (31, 3, 8), (32, 1, 768), (33, 1, 1005), (64, 2, 72), (0, 5, 64),
                                    (0, 3, 13), (700, 2000, 768), (1001, 5003, 1005), (2049, 70, 8192), (5000, 1 << 20, 8),
-                                   (9000, 40, 264)])
+                                   (9000, 40, 264), (2048, 50, 40), (32768, 300, 24), (32769, 70000, 13), (50000, 262144, 16)])
 def test_backward(moe, T, V, D, grad_type, with_add, index):
     g = _gen(T + V + D)
     ids = torch.randint(-1, V + 1, (T,), generator=g, device="cuda", dtype=index)
@@ -94,6 +94,34 @@ def test_many_tokens_and_blocks(moe):
     d_out = torch.randint(-8, 9, (T, D), generator=g, device="cuda").float()
     want = torch.zeros(V, D, device="cuda").index_add_(0, ids, d_out)
     assert torch.equal(moe.embedding_backward(d_out, ids, V), want)
+
+
+def test_long_runs_of_odd_rows(moe):
+    """Lists past the on-chip sort, rows without 16-byte pieces, ids that come
+    thousands of times."""
+    g = _gen(9)
+    T, V, D = 40000, 700, 21
+    ids = (torch.rand(T, generator=g, device="cuda") ** 4 * V).long()
+    _check_backward(moe, ids, torch.randn(T, D, generator=g, device="cuda"), V, 2.0,
+                    torch.randn(V, D, generator=g, device="cuda").bfloat16())
+
+
+def test_calls_from_several_host_threads(moe):
+    from concurrent.futures import ThreadPoolExecutor
+    g = _gen(10)
+    ids = torch.randint(0, 500, (3000,), generator=g, device="cuda")
+    d_out = torch.randn(3000, 64, generator=g, device="cuda").bfloat16()
+    want = moe.embedding_backward(d_out, ids, 500)
+    torch.cuda.synchronize()
+
+    def work(_):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = [moe.embedding_backward(d_out, ids, 500) for _ in range(10)]
+            torch.cuda.current_stream().synchronize()
+        return all(torch.equal(o, want) for o in out)
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(8)))
 
 
 def test_offsets_past_32_bits(moe):

@@ -287,6 +287,33 @@ def test_pieces_of_the_vocabulary(moe):
     assert ((got["dW"].double() - dW).abs() <= (2.0 ** -8 + 2.0 ** -12) * size + 2.0 ** -8 * dW.abs()).all()
 
 
+def test_distillation_over_pieces(moe):
+    """Teacher entries in both pieces; one entry a token is cross entropy."""
+    T, D, V = 1 << 18, 64, 8500
+    g, x, W, labels = _inputs(T, D, V)
+    other = torch.randint(0, V, (T, 1), generator=g, device="cuda")
+    ids = torch.cat([labels.clamp(0, V - 1)[:, None], other], 1)
+    logits = torch.tensor([0.0, -float("inf")], device="cuda").repeat(T, 1)
+    f = moe.distill_forward(x, W, ids, logits)
+    c = moe.cross_entropy_forward(x, W, ids[:, 0].contiguous())
+    assert torch.equal(f["lse"], c["lse"]) and torch.equal(f["loss"], c["loss"])
+    dl = torch.rand(T, generator=g, device="cuda") / T
+    a = moe.distill_backward(dl, x, W, ids, logits, f["lse"], f["logits"])
+    b = moe.cross_entropy_backward(dl, x, W, ids[:, 0].contiguous(), c["loss"], c["lse"])
+    for n in a:  # an entry of -inf has p = 0: its dz is d q, as it was; the label's value goes two ways
+        assert (a[n].float() - b[n].float()).norm() <= 2.0 ** -8 * a[n].float().norm()
+    even = moe.distill_forward(x, W, ids, torch.zeros(T, 2, device="cuda"))
+    got = moe.distill_backward(dl, x, W, ids, torch.zeros(T, 2, device="cuda"), even["lse"], even["logits"])
+    rows = torch.arange(0, T, 997, device="cuda")
+    z = x[rows].double() @ W.double().t()
+    dz = torch.softmax(z, 1)
+    dz.scatter_add_(1, ids[rows], torch.full((len(rows), 2), -0.5, dtype=torch.float64, device="cuda"))
+    dz *= dl[rows].double()[:, None]
+    want = dz @ W.double()
+    tol = (2.0 ** -8 + 2.0 ** -12) * (dz.abs() @ W.double().abs()) + 2.0 ** -8 * want.abs()
+    assert ((got["dx"][rows].double() - want).abs() <= tol).all()
+
+
 def test_views_that_start_anywhere(moe):
     g, x, W, labels = _inputs(70, 64, 300)
     ids, logits = _teacher(g, 70, 300, 5)
@@ -354,6 +381,40 @@ def test_captured_and_on_streams(moe):
             out.append([step(*st) for _ in range(3)])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for os, w in zip(out, want) for o in os for a, b in zip(o, w))
+
+
+def test_calls_from_several_host_threads(moe):
+    from concurrent.futures import ThreadPoolExecutor
+    _, x, W, labels = _inputs(300, 128, 2000)
+    dl = torch.ones(300, device="cuda")
+    f = moe.cross_entropy_forward(x, W, labels)
+    want = moe.cross_entropy_backward(dl, x, W, labels, f["loss"], f["lse"])
+    torch.cuda.synchronize()
+
+    def work(_):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = []
+            for _ in range(5):
+                a = moe.cross_entropy_forward(x, W, labels)
+                out.append((a, moe.cross_entropy_backward(dl, x, W, labels, a["loss"], a["lse"])))
+            torch.cuda.current_stream().synchronize()
+        return all(torch.equal(a[n], f[n]) for a, _ in out for n in f) and all(torch.equal(b[n], want[n]) for _, b in out for n in b)
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(8)))
+
+
+def test_few_tokens_and_a_large_vocabulary(moe):
+    """One row of tiles: dx's reduction is split, dW's tiles are many."""
+    for T, D, V in ((1, 128, 40000), (8, 704, 30001), (130, 64, 70000)):
+        g, x, W, labels = _inputs(T, D, V)
+        _check_ce(moe, x, W, labels, g)
+        ids, logits = _teacher(g, T, V, 40)
+        f = moe.distill_forward(x, W, ids, logits, temperature=2.0)
+        dl = torch.randn(T, generator=g, device="cuda")
+        got = moe.distill_backward(dl, x, W, ids, logits, f["lse"], f["logits"], temperature=2.0)
+        _check_gradients(got, ref.distill_dz(_np(x), _np(W), ids.cpu().numpy(), _np(logits), 2.0, _np(dl)), _np(x), _np(W),
+                         f"distillation {T}")
 
 
 def test_neighbours_stay_as_they_are(moe):
