@@ -580,6 +580,65 @@ def measure_other_workloads(names, args, dev, moe, flush_l2, pk) -> dict:
     return res
 
 
+def run_lm_sweep(args):
+    """The two ends of a language model around the layer (embedding, cross
+    entropy, distillation from 64 teacher entries a token, and their gradients)
+    at the benchmark layer's tokens and width, as the vocabulary grows.  One
+    JSON line per vocabulary; times are CUDA events around a call, L2 flushed
+    before it."""
+    import torch
+    from grouped_gemm_router_gb300 import build
+    build.build()
+    from grouped_gemm_router_gb300 import moe
+
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    pk, pk_kind = peaks()
+    T, D, K = 32768, 768, 64
+    gen = torch.Generator(device=dev).manual_seed(11)
+    randn = lambda *s: torch.randn(*s, generator=gen, device=dev)
+    flush = torch.empty(512 * 1024 * 1024 // 4, dtype=torch.float32, device=dev)
+    sink = torch.empty((), dtype=torch.float32, device=dev)
+
+    def seconds(call):
+        for _ in range(args.warmup):
+            call()
+        evs = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(args.steps)]
+        for a, b in evs:
+            flush.fill_(1.0)
+            sink.copy_(flush.sum())
+            a.record()
+            call()
+            b.record()
+        torch.cuda.synchronize()
+        return float(np.mean([a.elapsed_time(b) for a, b in evs])) / 1e3
+
+    for V in (8192, 32768, 50001, 131072):
+        x, W = randn(T, D).bfloat16(), (randn(V, D) / D ** 0.5).bfloat16()
+        ids = torch.randint(0, V, (T,), generator=gen, device=dev)
+        t_ids, t_logits = torch.randint(0, V, (T, K), generator=gen, device=dev), randn(T, K)
+        dl = torch.full((T,), 1.0 / T, device=dev)
+        c, d = moe.cross_entropy_forward(x, W, ids), moe.distill_forward(x, W, t_ids, t_logits)
+        product, table = 2 * T * D * V, V * D * 2
+        calls = {  # name: call, FLOP, bytes it cannot do without
+            "embedding_forward": (lambda: moe.embedding_forward(ids, W), 0, 2 * T * D * 2),
+            "embedding_backward": (lambda: moe.embedding_backward(x, ids, V), 0, T * D * 2 + 2 * table),
+            "cross_entropy_forward": (lambda: moe.cross_entropy_forward(x, W, ids), product, T * D * 2 + table),
+            "cross_entropy_backward": (lambda: moe.cross_entropy_backward(dl, x, W, ids, c["loss"], c["lse"]),
+                                       3 * product, 2 * (T * D * 2 + table)),
+            "distill_forward": (lambda: moe.distill_forward(x, W, t_ids, t_logits), product, T * D * 2 + table),
+            "distill_backward": (lambda: moe.distill_backward(dl, x, W, t_ids, t_logits, d["lse"], d["logits"]),
+                                 3 * product, 2 * (T * D * 2 + table)),
+        }
+        line = {"sweep": "lm", "T": T, "D": D, "V": V, "teacher_entries": K, "peaks": pk_kind}
+        for name, (call, flops, nbytes) in calls.items():
+            t = seconds(call)
+            line[name] = {"us": t * 1e6, "tflops": flops / t / 1e12, "frac_tensor": flops / t / 1e12 / pk["bf16_tflops"],
+                          "frac_hbm": nbytes / t / 1e9 / pk["hbm_gbs"]}
+        assert moe.device_error() == 0
+        print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -592,9 +651,10 @@ def main():
                     help="streams (each with its own workspace) in the end-to-end host-buffer loop")
     ap.add_argument("--no-per-workload", action="store_true",
                     help="skip timing the other synthetic workloads after the headline one")
-    ap.add_argument("--sweep", choices=["fd", "t", "all", "chained"], default=None,
+    ap.add_argument("--sweep", choices=["fd", "t", "all", "chained", "lm"], default=None,
                     help="roofline placement of the grouped GEMMs over F/D or tokens per expert; "
-                         "'chained': chained vs unchained expert FFN (D <= 256)")
+                         "'chained': chained vs unchained expert FFN (D <= 256); "
+                         "'lm': embedding and vocabulary losses over the vocabulary")
     ap.add_argument("--chain-shape", default=None, metavar="TxDxF",
                     help="with --sweep chained: measure this one shape only")
     ap.add_argument("--backward", action="store_true",
@@ -605,6 +665,9 @@ def main():
         return
     if args.sweep == "chained":
         run_chain_sweep(args)
+        return
+    if args.sweep == "lm":
+        run_lm_sweep(args)
         return
     if args.sweep:
         run_sweep(args)
