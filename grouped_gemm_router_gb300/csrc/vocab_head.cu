@@ -52,9 +52,8 @@ constexpr int kBoxes = 4;      // 32-column boxes of an epilogue warp
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
-constexpr int kNoTarget = 0x7fffffff;
 
-// A warp's buffer: 32 rows of 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)
+// A warp's buffer for what it stores: 32 rows of 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)
 // (TMA's 128-byte swizzle, and free of bank conflicts when a lane has a row).
 constexpr int kBoxBytes = 4096;
 constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kBoxBytes + 1024;
@@ -64,7 +63,7 @@ struct VocabArgs : VocabWork {
   int v0, Vc, Vcp;         // kDz, kGrad: the piece's first row, its rows, and those rounded up to 64
   float c;
   unsigned int* dev_err;
-  // targets: labels (K = 0), or kStats: sorted (id << 8 | entry) keys [T, K]
+  // targets: labels (K = 0), or kStats: sorted keys [T, K]
   const void* labels;
   int labels64;
   const uint32_t* keys;
@@ -100,62 +99,70 @@ MOE_DEV long long load_index(const void* p, int is64, size_t i) {
   return is64 ? static_cast<const long long*>(p)[i] : static_cast<const int*>(p)[i];
 }
 
-// A row's targets in ascending order of their columns.
-struct Targets {
-  const uint32_t* keys;
-  int left;        // keys behind the current one
-  uint32_t ahead;  // the first of them, asked for before it is needed
-  int id;          // current column, or kNoTarget
-  int entry;
+// Order of a target among those of its row: first those of the columns that one
+// half of the epilogue has (bit 7 of the id), then the other's, each by column.
+// No target: all ones.
+__host__ MOE_DEV uint32_t target_key(uint32_t id, uint32_t entry) { return (id >> 7 & 1u) << 30 | id << 8 | entry; }
 
-  MOE_DEV void step() {
-    if (left == 0) {
-      id = kNoTarget;
-      return;
-    }
-    id = static_cast<int>(ahead >> 8);
-    entry = static_cast<int>(ahead & 255u);
-    if (--left > 0) ahead = *keys++;
+// A row's targets in one half of the columns, in ascending order.  The keys are
+// asked for three ahead: the next one is needed a few instructions later, and L2
+// takes hundreds of cycles.  (One ahead, and both halves' keys in one list: 1790
+// us instead of 1270 without targets, 32768 x 768 x 50001 with 64 a token.)
+struct Targets {
+  uint32_t now, next1, next2, next3;  // id << 8 | entry, or more than any of those
+  int pos;                            // the key after them
+
+  MOE_DEV uint32_t key(const VocabArgs& p, int row, int half, int i) const {
+    return i < p.K ? p.keys[static_cast<size_t>(row) * p.K + i] - (static_cast<uint32_t>(half) << 30) : 0xffffffffu;
+  }
+  MOE_DEV int id() const { return static_cast<int>(now >> 8); }
+  MOE_DEV int entry() const { return static_cast<int>(now & 255u); }
+  MOE_DEV void step(const VocabArgs& p, int row, int half) {
+    now = next1;
+    next1 = next2;
+    next2 = next3;
+    next3 = key(p, row, half, pos++);
   }
   // From the first target at or past column `col`.
-  MOE_DEV void start(const VocabArgs& p, int row, int col) {
-    left = 0;
-    id = kNoTarget;
-    entry = 0;
-    ahead = 0;
-    keys = nullptr;
+  MOE_DEV void start(const VocabArgs& p, int row, int half, int col) {
+    now = next1 = next2 = next3 = 0xffffffffu;
+    pos = p.K;
     if (row >= p.T) return;
     if (p.K == 0) {
       const long long l = load_index(p.labels, p.labels64, row);
-      id = l >= col && l < p.V ? static_cast<int>(l) : kNoTarget;
+      if (l >= col && l < p.V && (l >> 7 & 1) == half) now = static_cast<uint32_t>(l) << 8;
       return;
     }
     if (p.keys == nullptr) return;  // kDz: those come after it
     const uint32_t* k = p.keys + static_cast<size_t>(row) * p.K;
-    const uint32_t want = static_cast<uint32_t>(col) << 8;
+    const uint32_t want = static_cast<uint32_t>(half) << 30 | static_cast<uint32_t>(col) << 8;
     int lo = 0, hi = p.K;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (k[mid] < want) lo = mid + 1;
       else hi = mid;
     }
-    keys = k + lo;
-    left = p.K - lo;
-    if (left > 0) ahead = *keys++;
-    step();
-  }
-  // Past the targets of the columns in between, which another warp has: few as
-  // a rule, and a search where they are not.
-  MOE_DEV void skip(const VocabArgs& p, int row, int col) {
-    for (int i = 0; i < 3 && id < col; ++i) next(p);
-    if (id < col) start(p, row, col);
-  }
-  // What lies past the current target (of labels there is no other).
-  MOE_DEV void next(const VocabArgs& p) {
-    if (p.K == 0) id = kNoTarget;
-    else step();
+    now = key(p, row, half, lo);
+    next1 = key(p, row, half, lo + 1);
+    next2 = key(p, row, half, lo + 2);
+    next3 = key(p, row, half, lo + 3);
+    pos = lo + 4;
   }
 };
+
+// Element j of 32 registers, by halves.  (Through the warp's buffer in shared
+// memory, which the MMAs read at the same time: 400 us instead of 340, 32768 x 768
+// x 8192 with 64 targets a token; without targets 262.)
+MOE_DEV uint32_t pick(const uint32_t (&v)[32], int j) {
+  uint32_t t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = j & 16 ? v[i + 16] : v[i];
+#pragma unroll
+  for (int h = 8; h > 0; h >>= 1)
+#pragma unroll
+    for (int i = 0; i < h; ++i) t[i] = j & h ? t[i + h] : t[i];
+  return t[0];
+}
 
 // 128 bytes into a lane's row of its warp's buffer.
 MOE_DEV void put_row(uint8_t* mine, const uint32_t (&w)[32]) {
@@ -336,15 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col0 = u.n * kTile + c_first;  // first column of this warp (of the piece, in kDz)
       if constexpr (kMode != kGrad) {
         if (u.first) {
-          tg.start(p, row, p.v0 + col0);
+          tg.start(p, row, half, p.v0 + col0);
           run_max = -INFINITY;
           run_sum = 0.f;
           if constexpr (kMode == kDz) {
             row_a = row < p.T ? p.row_a[row] : 0.f;
             row_l = row < p.T ? p.row_l[row] : 0.f;
           }
-        } else {
-          tg.skip(p, row, p.v0 + col0);
         }
       }
       const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[buf]), (i >> 1) & 1, abort_flag, dev_err);
@@ -369,17 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int b = 0; b < kBoxes; ++b) {
-          const int end = col0 + b * 32 + 32;
-          if (__any_sync(0xffffffffu, tg.id < end)) {
-            // a lane writes its row and reads its targets back from it
-            put_row(mine, acc[b]);
-            while (tg.id < end) {
-              const int j = tg.id - (end - 32);
-              const float z = *reinterpret_cast<const float*>(mine + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4);
-              p.target[p.K == 0 ? static_cast<size_t>(row) : static_cast<size_t>(row) * p.K + tg.entry] = z;
-              tg.next(p);
+          // each turn takes at most one target of a lane out of the box
+          const int begin = col0 + b * 32;
+          while (__any_sync(0xffffffffu, tg.id() < begin + 32)) {
+            const float z = __uint_as_float(pick(acc[b], tg.id() - begin));
+            if (tg.id() < begin + 32) {
+              p.target[p.K == 0 ? static_cast<size_t>(row) : static_cast<size_t>(row) * p.K + tg.entry()] = z;
+              tg.step(p, row, half);
             }
-            __syncwarp();
           }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -423,11 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           put_row(mine, packed);
           const int end = p.v0 + cc + 64;
-          if (tg.id < end) {
-            const int j = tg.id - (end - 64);
-            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) =
-                p.value[row];
-            tg.next(p);
+          if (tg.id() < end) {
+            const int j = tg.id() - (end - 64);
+            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) = p.value[row];
+            tg.step(p, row, half);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -581,15 +582,16 @@ MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, 
   }
 }
 
-// Sorts the row's keys (id << 8 | entry; none: all ones) in the warp's buffer.
-template <int kSlots>
+// Sorts the row's keys in the warp's buffer: target_key, or id << 8 | entry.
+template <bool kHalves, int kSlots>
 MOE_DEV void sort_keys(uint32_t* k, const Teacher<kSlots>& t) {
   const int lane = threadIdx.x & 31;
   constexpr int n = 32 * kSlots;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int j = lane + 32 * i;
-    k[j] = t.id[i] >= 0 ? (static_cast<uint32_t>(t.id[i]) << 8 | static_cast<uint32_t>(j)) : 0xffffffffu;
+    const uint32_t id = static_cast<uint32_t>(t.id[i]), entry = static_cast<uint32_t>(j);
+    k[j] = t.id[i] < 0 ? 0xffffffffu : kHalves ? target_key(id, entry) : id << 8 | entry;
   }
   __syncwarp();
 #pragma unroll 1
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets
   if (row >= T) return;
   Teacher<kSlots> te;
   read_teacher(t, row, V, inv_tau, te);
-  sort_keys(buf[warp], te);
+  sort_keys<true>(buf[warp], te);
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int j = lane + 32 * i;
@@ -639,6 +641,18 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets
 // be off by 2^-24 of their size, is never formed.
 constexpr int kFinishWarps = 32;
 
+// Every kFinishWarps-th of a row's pairs from i on, kBatch of them in flight (few
+// tokens and a large vocabulary have thousands).
+template <int kBatch>
+MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, float& m, float& s) {
+  float2 v[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) v[j] = row[static_cast<size_t>(min(i + j * kFinishWarps, parts - 1)) * rows_padded];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (i + j * kFinishWarps < parts) join(m, s, v[j].x, v[j].y);
+}
+
 template <int kSlots>
 __global__ void __launch_bounds__(32 * kFinishWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
@@ -652,16 +666,9 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
   float m = -INFINITY, s = 0.f;
   if (row0 + lane < T) {
     const float2* mine = part + row0 + lane;
-    constexpr int kBatch = 16;
-    for (int i = warp; i < parts; i += kBatch * kFinishWarps) {
-      float2 v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        v[j] = mine[static_cast<size_t>(min(i + j * kFinishWarps, parts - 1)) * rows_padded];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (i + j * kFinishWarps < parts) join(m, s, v[j].x, v[j].y);
-    }
+    int i = warp;
+    for (; i + 12 * kFinishWarps < parts; i += 16 * kFinishWarps) join_pairs<16>(mine, i, parts, rows_padded, m, s);
+    for (; i < parts; i += 4 * kFinishWarps) join_pairs<4>(mine, i, parts, rows_padded, m, s);
   }
   got[warp][lane] = make_float2(m, s);
   __syncthreads();
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   read_teacher(t, row, V, inv_tau, te);
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) prob[warp][lane + 32 * i] = te.p[i];
-  sort_keys(buf[warp], te);
+  sort_keys<false>(buf[warp], te);
   for (int i = lane; i < t.K; i += 32) {
     const uint32_t key = buf[warp][i], id = key >> 8;
     const int column = static_cast<int>(id) - v0;
