@@ -582,55 +582,54 @@ MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, 
   }
 }
 
-// Sorts the row's keys in the warp's buffer: target_key, or id << 8 | entry.
-template <bool kHalves, int kSlots>
-MOE_DEV void sort_keys(uint32_t* k, const Teacher<kSlots>& t) {
+// Sorts 32 kSlots keys, key lane + 32 i in k[i], by a bitonic network: distances
+// from 32 on between a lane's own registers, shorter ones between lanes.
+template <int kSlots>
+MOE_DEV void sort_keys(uint32_t (&k)[kSlots]) {
   const int lane = threadIdx.x & 31;
-  constexpr int n = 32 * kSlots;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int j = lane + 32 * i;
-    const uint32_t id = static_cast<uint32_t>(t.id[i]), entry = static_cast<uint32_t>(j);
-    k[j] = t.id[i] < 0 ? 0xffffffffu : kHalves ? target_key(id, entry) : id << 8 | entry;
-  }
-  __syncwarp();
-#pragma unroll 1
-  for (int size = 2; size <= n; size <<= 1)
-#pragma unroll 1
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      for (int i = lane; i < n / 2; i += 32) {
-        const int a = 2 * i - (i & (d - 1)), b = a + d;
-        const uint32_t x = k[a], y = k[b];
-        if ((x > y) == ((a & size) == 0)) {
-          k[a] = y;
-          k[b] = x;
+  for (int size = 2; size <= 32 * kSlots; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (d >= 32) {
+          const int o = i ^ (d >> 5);
+          if (o < i) continue;
+          const bool up = ((32 * i) & size) == 0;
+          const uint32_t lo = min(k[i], k[o]), hi = max(k[i], k[o]);
+          k[i] = up ? lo : hi;
+          k[o] = up ? hi : lo;
+        } else {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, k[i], d);
+          const bool up = ((32 * i + lane) & size) == 0, first = (lane & d) == 0;
+          k[i] = first == up ? min(k[i], other) : max(k[i], other);
         }
       }
-      __syncwarp();
-    }
 }
 
 // Forward of distillation: the rows' sorted keys.
 template <int kSlots>
-__global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets t, int T, int V, float inv_tau,
-                                                                    uint32_t* keys, float* target) {
-  __shared__ uint32_t buf[kRowWarps][32 * kSlots];
+__global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets t, int T, int V, uint32_t* keys,
+                                                                    float* target) {
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kRowWarps + warp;
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (row >= T) return;
-  Teacher<kSlots> te;
-  read_teacher(t, row, V, inv_tau, te);
-  sort_keys<true>(buf[warp], te);
+  uint32_t k[kSlots];
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int j = lane + 32 * i;
-    if (j < t.K) {
-      keys[static_cast<size_t>(row) * t.K + j] = buf[warp][j];
-      if (te.id[i] < 0) target[static_cast<size_t>(row) * t.K + j] = 0.f;
-    }
+    const size_t at = static_cast<size_t>(row) * t.K + j;
+    const long long id = j < t.K ? load_index(t.ids, t.ids64, at) : -1;
+    const bool known = id >= 0 && id < V;
+    k[i] = known ? target_key(static_cast<uint32_t>(id), static_cast<uint32_t>(j)) : 0xffffffffu;
+    if (j < t.K && !known) target[at] = 0.f;
   }
+  sort_keys(k);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (lane + 32 * i < t.K) keys[static_cast<size_t>(row) * t.K + lane + 32 * i] = k[i];
 }
 
 // Joins a row's (maximum, sum) pairs and writes lse and the loss: 32 rows a
@@ -756,7 +755,7 @@ template <int kSlots>
 __global__ void __launch_bounds__(32 * kRowWarps)
     vocab_distill_targets_kernel(const float* row_a, const float* lse, const float* target, VocabTargets t, int T, int V,
                                  float inv_tau, int v0, int Vc, uint16_t* dz) {
-  __shared__ uint32_t buf[kRowWarps][32 * kSlots];
+  __shared__ uint32_t ids[kRowWarps][32 * kSlots];
   __shared__ float prob[kRowWarps][32 * kSlots];
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -766,16 +765,36 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   if (d == 0.f) return;
   Teacher<kSlots> te;
   read_teacher(t, row, V, inv_tau, te);
+  uint32_t k[kSlots];
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) prob[warp][lane + 32 * i] = te.p[i];
-  sort_keys<false>(buf[warp], te);
-  for (int i = lane; i < t.K; i += 32) {
-    const uint32_t key = buf[warp][i], id = key >> 8;
-    const int column = static_cast<int>(id) - v0;
-    if (key == 0xffffffffu || column < 0 || column >= Vc || (i > 0 && buf[warp][i - 1] >> 8 == id)) continue;
-    float p = 0.f;
-    for (int a = i; a < t.K && buf[warp][a] >> 8 == id; ++a) p += prob[warp][buf[warp][a] & 255u];
-    const float q = expf(target[static_cast<size_t>(row) * t.K + (key & 255u)] * inv_tau - l);
+  for (int i = 0; i < kSlots; ++i) {
+    prob[warp][lane + 32 * i] = te.p[i];
+    k[i] = te.id[i] < 0 ? 0xffffffffu : static_cast<uint32_t>(te.id[i]) << 8 | static_cast<uint32_t>(lane + 32 * i);
+  }
+  sort_keys(k);
+  __syncwarp();
+  // entries of one id lie side by side: the first of them writes for all
+  bool again = false;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    ids[warp][lane + 32 * i] = k[i];
+    const uint32_t left = __shfl_up_sync(0xffffffffu, k[i], 1), last = __shfl_sync(0xffffffffu, k[i > 0 ? i - 1 : 0], 31);
+    const uint32_t before = lane > 0 ? left : i > 0 ? last : 0xffffffffu;
+    again |= k[i] != 0xffffffffu && before >> 8 == k[i] >> 8;
+  }
+  again = __any_sync(0xffffffffu, again);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const uint32_t id = k[i] >> 8;
+    const int at = lane + 32 * i, column = static_cast<int>(id) - v0;
+    if (k[i] == 0xffffffffu || column < 0 || column >= Vc) continue;
+    float p = prob[warp][k[i] & 255u];
+    if (again) {
+      if (at > 0 && ids[warp][at - 1] >> 8 == id) continue;
+      for (int a = at + 1; a < 32 * kSlots && ids[warp][a] >> 8 == id; ++a) p += prob[warp][ids[warp][a] & 255u];
+    }
+    const float q = expf(target[static_cast<size_t>(row) * t.K + (k[i] & 255u)] * inv_tau - l);
     dz[(static_cast<size_t>(column >> 6) * T + row) * 64 + (column & 63)] =
         static_cast<uint16_t>(pack_bf16x2(d * (q - p), 0.f) & 0xffffu);
   }
@@ -951,7 +970,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   const float inv_tau = 1.f / a.temperature;
   if (v.K) {
     auto* k = by_slots(v.K, vocab_keys_kernel<1>, vocab_keys_kernel<2>, vocab_keys_kernel<4>, vocab_keys_kernel<8>);
-    e = launch_kernel(k, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false, a.targets, a.T, a.V, inv_tau,
+    e = launch_kernel(k, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false, a.targets, a.T, a.V,
                       keys, v.target);
     if (e != cudaSuccess) return e;
   }
