@@ -632,74 +632,84 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_keys_kernel(VocabTargets
     if (lane + 32 * i < t.K) keys[static_cast<size_t>(row) * t.K + lane + 32 * i] = k[i];
 }
 
+// Every kWarps-th of a row's pairs from i on, kBatch of them in flight.
+template <int kBatch, int kWarps>
+MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, float& m, float& s) {
+  float2 v[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) v[j] = row[static_cast<size_t>(min(i + j * kWarps, parts - 1)) * rows_padded];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (i + j * kWarps < parts) join(m, s, v[j].x, v[j].y);
+}
+
 // Joins a row's (maximum, sum) pairs and writes lse and the loss: 32 rows a
-// block, the pairs dealt to its 32 warps, then a row to each.  With the sum s relative to 2^m,
+// block, the pairs dealt to its warps, then the rows.  With the sum s relative
+// to 2^m,
 //   lse - z / temperature = ln 2 (log2 s - (c z - m)),
 // where c z - m is one fused product: for a target that outweighs the rest both
 // terms are next to 0, and the difference of the rounded lse and z, which would
 // be off by 2^-24 of their size, is never formed.
-constexpr int kFinishWarps = 32;
-
-// Every kFinishWarps-th of a row's pairs from i on, kBatch of them in flight (few
-// tokens and a large vocabulary have thousands).
-template <int kBatch>
-MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, float& m, float& s) {
-  float2 v[kBatch];
-#pragma unroll
-  for (int j = 0; j < kBatch; ++j) v[j] = row[static_cast<size_t>(min(i + j * kFinishWarps, parts - 1)) * rows_padded];
-#pragma unroll
-  for (int j = 0; j < kBatch; ++j)
-    if (i + j * kFinishWarps < parts) join(m, s, v[j].x, v[j].y);
-}
-
-template <int kSlots>
-__global__ void __launch_bounds__(32 * kFinishWarps)
+// kWarps: 32 where few blocks have thousands of pairs a row (1124 of 219 rows: 10
+// us of a call, with 8 warps 15), 8 where many blocks have few (98 of 32768 rows:
+// 12 us, with 32 warps 25).
+template <int kSlots, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
                         float c, float inv_tau, float* loss, float* lse) {
-  __shared__ float2 got[kFinishWarps][33];
+  __shared__ float2 got[kWarps][33];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * 32;
-  // lane: a row of the block; warp: every kFinishWarps-th pair of it
+  // lane: a row of the block; warp: every kWarps-th pair of it
   float m = -INFINITY, s = 0.f;
   if (row0 + lane < T) {
     const float2* mine = part + row0 + lane;
     int i = warp;
-    for (; i + 12 * kFinishWarps < parts; i += 16 * kFinishWarps) join_pairs<16>(mine, i, parts, rows_padded, m, s);
-    for (; i < parts; i += 4 * kFinishWarps) join_pairs<4>(mine, i, parts, rows_padded, m, s);
+    for (; i + 12 * kWarps < parts; i += 16 * kWarps) join_pairs<16, kWarps>(mine, i, parts, rows_padded, m, s);
+    for (; i < parts; i += 4 * kWarps) join_pairs<4, kWarps>(mine, i, parts, rows_padded, m, s);
   }
   got[warp][lane] = make_float2(m, s);
   __syncthreads();
-  // from here on a warp has one row
-  const int row = row0 + warp;
-  if (row >= T) return;
-  m = got[lane][warp].x;
-  s = got[lane][warp].y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, m2, s2);
-  }
-  const float log_s = log2f(s);
-  if (lane == 0) lse[row] = (m + log_s) * kLn2;
   if constexpr (kSlots == 0) {
-    if (lane == 0) {
-      const long long id = load_index(t.ids, t.ids64, row);
-      loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
-    }
-  } else {
-    Teacher<kSlots> te;
-    read_teacher(t, row, V, inv_tau, te);
-    float sum = 0.f;
+    const int row = row0 + lane;
+    if (warp > 0 || row >= T) return;
+    for (int i = 1; i < kWarps; ++i) join(m, s, got[i][lane].x, got[i][lane].y);
+    const float log_s = log2f(s);
+    const long long id = load_index(t.ids, t.ids64, row);
+    lse[row] = (m + log_s) * kLn2;
+    loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
+    return;
+  }
+  // from here on a warp has a row at a time
+  for (int r = warp; r < 32; r += kWarps) {
+    const int row = row0 + r;
+    if (row >= T) return;
+    m = lane < kWarps ? got[lane % kWarps][r].x : -INFINITY;
+    s = lane < kWarps ? got[lane % kWarps][r].y : 0.f;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      const int j = lane + 32 * i;
-      if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
-        sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      join(m, s, m2, s2);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) loss[row] = sum;
+    m = __shfl_sync(0xffffffffu, m, 0);
+    s = __shfl_sync(0xffffffffu, s, 0);
+    const float log_s = log2f(s);
+    if (lane == 0) lse[row] = (m + log_s) * kLn2;
+    if constexpr (kSlots > 0) {
+      Teacher<kSlots> te;
+      read_teacher(t, row, V, inv_tau, te);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const int j = lane + 32 * i;
+        if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+          sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) loss[row] = sum;
+    }
   }
 }
 
@@ -927,6 +937,18 @@ Kernel by_slots(int K, Kernel k1, Kernel k2, Kernel k4, Kernel k8) {
   return K <= 32 ? k1 : K <= 64 ? k2 : K <= 128 ? k4 : k8;
 }
 
+constexpr int kManyRows = 4096;
+
+template <int kWarps>
+cudaError_t launch_finish(const VocabForward& a, const VocabArgs& v, const ForwardPlan& f, float inv_tau, cudaStream_t s) {
+  auto* k = v.K == 0 ? vocab_finish_kernel<0, kWarps>
+                     : by_slots(v.K, vocab_finish_kernel<1, kWarps>, vocab_finish_kernel<2, kWarps>,
+                                vocab_finish_kernel<4, kWarps>, vocab_finish_kernel<8, kWarps>);
+  return launch_kernel(k, dim3(ceil_div(a.T, 32)), dim3(32 * kWarps), 0, s, true, static_cast<const float2*>(v.part),
+                       2 * f.runs, f.rows_padded, a.targets, static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau,
+                       a.loss, a.lse);
+}
+
 cudaError_t launch_sum(const float* part, int n_parts, size_t n, uint16_t* out, cudaStream_t s) {
   return launch_kernel(vocab_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0, s, true, part,
                        n_parts, n, out);
@@ -976,12 +998,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   }
   e = launch_vocab<kStats>(std::min(st.pairs[kStats], v.items), mx, mw, mx, mx, mx, v, s, v.K != 0);
   if (e != cudaSuccess) return e;
-  auto* finish = v.K == 0 ? vocab_finish_kernel<0>
-                          : by_slots(v.K, vocab_finish_kernel<1>, vocab_finish_kernel<2>, vocab_finish_kernel<4>,
-                                     vocab_finish_kernel<8>);
-  return launch_kernel(finish, dim3(ceil_div(a.T, 32)), dim3(32 * kFinishWarps), 0, s, true,
-                       static_cast<const float2*>(v.part), 2 * f.runs, f.rows_padded, a.targets,
-                       static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau, a.loss, a.lse);
+  return a.T < kManyRows ? launch_finish<32>(a, v, f, inv_tau, s) : launch_finish<8>(a, v, f, inv_tau, s);
 }
 
 size_t vocab_backward_workspace_bytes(int T, int D, int V, int K) {
