@@ -14,6 +14,7 @@
 // runs of `chunk` sorted tokens with one id are summed by warps of their own
 // beforehand, and a long run is then added by a whole block.
 #include <algorithm>
+#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_kernels.cuh"
@@ -132,25 +133,28 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 512;
 constexpr int kHeld = 8;  // rounds of 32 tokens that a warp keeps in registers
 
-constexpr int kCluster = 8;           // blocks that sort a short list
+constexpr int kMaxCluster = 16;        // most blocks that sort a short list together
 constexpr int kShortBlock = kSortThreads * kHeld;
-constexpr int kShortList = kCluster * kShortBlock;  // (its positions fit in 16 bits)
+constexpr int kShortList = kMaxCluster * kShortBlock;  // (its positions fit in 16 bits)
 
 struct SortPlan {
   int passes, bits;       // of a pass
   int block, blocks;      // tokens of a block
+  int cluster;            // blocks of a short list's cluster
   int chunk, chunks;      // aligned runs of sorted tokens
 };
 
 SortPlan sort_plan(int T, int V) {
-  SortPlan p;
+  SortPlan p = {};
   int b = 1;
   while ((V >> b) != 0) ++b;  // the keys are 0 .. V (V: no row)
   p.passes = (b + 8) / 9;
   p.bits = (b + p.passes - 1) / p.passes;
   if (T <= kShortList) {
+    // (8000 tokens: 16 blocks 28.7 us a call, 8 29.5, 4 32.3; 32768: 16 75, 8 84)
+    p.cluster = T <= 512 ? 1 : T <= 4096 ? 4 : kMaxCluster;
     p.block = kSortThreads;
-    while (p.block * kCluster < T) p.block *= 2;
+    while (p.block * p.cluster < T) p.block *= 2;
   } else {
     p.block = 2048;
     while (p.block < 32768 && (T + p.block - 1) / p.block > 128) p.block *= 2;
@@ -318,7 +322,8 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
 // tokens into registers, the blocks see one another's histograms, and every
 // token goes to its place in some block's memory, in the last pass to the lists.
 // It runs beside a fill that keeps the memory busy: with lists and histograms in
-// global memory 32768 tokens took 52 us there, 31 alone.
+// global memory 32768 tokens took 52 us there, 31 alone; on chip, by 8 blocks, 38
+// and 27.
 struct ShortSmem {
   uint32_t key[kShortBlock];
   uint16_t tok[kShortBlock];
@@ -334,6 +339,7 @@ MOE_DEV uint32_t load_remote(const uint32_t* p, uint32_t rank) {
   return v;
 }
 
+template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) embedding_sort_short_kernel(SortArgs a) {
   __shared__ ShortSmem sm;
   griddep_launch_dependents();
@@ -485,11 +491,11 @@ constexpr int kLong = 16;      // tokens past its window that a warp adds alone
 // A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
 template <int VEC, bool kF32>
 struct Shape {
-  static constexpr int kVecs = VEC == 1 ? 8 : kF32 ? 2 : 4;
+  static constexpr int kVecs = VEC == 1 ? 8 : kF32 ? 2 : 3;
   static constexpr int kColumns = 32 * kVecs * VEC;
 };
 template <int VEC, bool kF32, int kVecs>
-constexpr int kAhead = VEC == 1 ? 4 : 64 / (kVecs * Piece<VEC, kF32>::kWords);  // 64 registers
+constexpr int kAhead = VEC == 1 || kVecs * Piece<VEC, kF32>::kWords <= 16 ? 4 : 2;  // at most 64 registers
 
 // A lane's pieces of one row; lanes past the last column read another's (a load
 // under a condition would be waited for on the spot).
@@ -739,6 +745,34 @@ cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
   return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(a.window_blocks, turns), dim3(32 * kSumWarps), 0, s, true, a);
 }
 
+std::mutex g_mu;
+bool g_large_clusters[64];
+
+// Clusters of 16 have to be asked for, once on each device.
+cudaError_t allow_large_clusters() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_large_clusters[dev]) {
+    e = cudaFuncSetAttribute(embedding_sort_short_kernel<kMaxCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    g_large_clusters[dev] = e == cudaSuccess;
+  }
+  return e;
+}
+
+cudaError_t launch_sort_short(const SortArgs& q, int cluster, cudaStream_t s) {
+  if (cluster == kMaxCluster) {
+    const cudaError_t e = allow_large_clusters();
+    if (e != cudaSuccess) return e;
+  }
+  auto* k = cluster == 1   ? embedding_sort_short_kernel<1>
+            : cluster == 4 ? embedding_sort_short_kernel<4>
+                           : embedding_sort_short_kernel<kMaxCluster>;
+  return launch_kernel(k, dim3(cluster), dim3(kSortThreads), 0, s, false, q);
+}
+
 size_t hist_bytes(int T, const SortPlan& p) {
   return T <= kShortList ? 0 : static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits);
 }
@@ -782,7 +816,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? window_blocks(a.T) * kSumWarps * sizeof(int2) : 0));
   cudaError_t e = cudaSuccess;
   if (a.T > 0 && a.T <= kShortList) {
-    e = launch_kernel(embedding_sort_short_kernel, dim3(kCluster), dim3(kSortThreads), 0, s, false, q);
+    e = launch_sort_short(q, p.cluster, s);
   } else if (a.T > 0) {
     e = launch_kernel(embedding_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, false, q);
     for (q.pass = 0; q.pass < p.passes && e == cudaSuccess; ++q.pass) {

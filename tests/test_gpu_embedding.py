@@ -96,11 +96,12 @@ def test_many_tokens_and_blocks(moe):
     assert torch.equal(moe.embedding_backward(d_out, ids, V), want)
 
 
-def test_long_runs_of_odd_rows(moe):
-    """Lists past the on-chip sort, rows without 16-byte pieces, ids that come
-    thousands of times."""
-    g = _gen(9)
-    T, V, D = 40000, 700, 21
+@pytest.mark.parametrize("T,V", [(512, 3), (513, 3000), (4096, 100), (4097, 600000), (40000, 700), (65536, 900), (65537, 900)])
+def test_long_runs_of_odd_rows(moe, T, V):
+    """Lists at the edges of the on-chip sorts and past them, rows without
+    16-byte pieces, ids that come thousands of times."""
+    g = _gen(T)
+    D = 21
     ids = (torch.rand(T, generator=g, device="cuda") ** 4 * V).long()
     _check_backward(moe, ids, torch.randn(T, D, generator=g, device="cuda"), V, 2.0,
                     torch.randn(V, D, generator=g, device="cuda").bfloat16())
