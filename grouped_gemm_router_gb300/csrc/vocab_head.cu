@@ -672,43 +672,57 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   got[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if constexpr (kSlots == 0) {
+  if constexpr (kSlots == 0 && kWarps <= 8) {
+    // a lane a row, in the order of the shuffles below, so that a teacher of one
+    // entry gets a label's bits
     const int row = row0 + lane;
     if (warp > 0 || row >= T) return;
-    for (int i = 1; i < kWarps; ++i) join(m, s, got[i][lane].x, got[i][lane].y);
-    const float log_s = log2f(s);
+    float2 v[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v[i] = got[i][lane];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; ++i) join(v[i].x, v[i].y, v[i + o].x, v[i + o].y);
+    m = v[0].x;
+    const float log_s = log2f(v[0].y);
     const long long id = load_index(t.ids, t.ids64, row);
     lse[row] = (m + log_s) * kLn2;
     loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
-    return;
-  }
-  // from here on a warp has a row at a time
-  for (int r = warp; r < 32; r += kWarps) {
-    const int row = row0 + r;
-    if (row >= T) return;
-    m = lane < kWarps ? got[lane % kWarps][r].x : -INFINITY;
-    s = lane < kWarps ? got[lane % kWarps][r].y : 0.f;
+  } else {
+    // a warp a row
+    for (int r = warp; r < 32; r += kWarps) {
+      const int row = row0 + r;
+      if (row >= T) return;
+      m = lane < kWarps ? got[lane % kWarps][r].x : -INFINITY;
+      s = lane < kWarps ? got[lane % kWarps][r].y : 0.f;
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      join(m, s, m2, s2);
-    }
-    m = __shfl_sync(0xffffffffu, m, 0);
-    s = __shfl_sync(0xffffffffu, s, 0);
-    const float log_s = log2f(s);
-    if (lane == 0) lse[row] = (m + log_s) * kLn2;
-    if constexpr (kSlots > 0) {
-      Teacher<kSlots> te;
-      read_teacher(t, row, V, inv_tau, te);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        const int j = lane + 32 * i;
-        if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
-          sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        join(m, s, m2, s2);
       }
-      sum = warp_sum(sum);
-      if (lane == 0) loss[row] = sum;
+      m = __shfl_sync(0xffffffffu, m, 0);
+      s = __shfl_sync(0xffffffffu, s, 0);
+      const float log_s = log2f(s);
+      if (lane == 0) lse[row] = (m + log_s) * kLn2;
+      if constexpr (kSlots == 0) {
+        if (lane == 0) {
+          const long long id = load_index(t.ids, t.ids64, row);
+          loss[row] = id >= 0 && id < V ? (log_s - fmaf(target[row], c, -m)) * kLn2 : 0.f;
+        }
+      } else {
+        Teacher<kSlots> te;
+        read_teacher(t, row, V, inv_tau, te);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          const int j = lane + 32 * i;
+          if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+            sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) loss[row] = sum;
+      }
     }
   }
 }
