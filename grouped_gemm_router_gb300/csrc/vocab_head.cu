@@ -220,11 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ===================== TMA producer (both CTAs) =====================
     if (lane == 0) {
-      // x and W are read again by other pairs, dz and the pairs are written for
-      // later: kept over them, kDz took 1450 us instead of 1500 (32768 x 768 x
-      // 50001) and 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less
-      // (and 72 us instead of 234 at 1 x 1664 x 61514, where all read one row).
-      const uint64_t pol = kMode == kGrad ? l2_policy_evict_normal() : l2_policy_evict_last();
+      // What is loaded is read again by other pairs, what is stored is for later.
+      // Kept over it, kDz took 1450 us instead of 1500 (32768 x 768 x 50001) and
+      // 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less and kGrad 2 %;
+      // and lines that all pairs read at once cost less: kStats 72 us instead of 234
+      // at 1 x 1664 x 61514, the whole backward 236 instead of 284 at 8 x 704 x 194036.
+      const uint64_t pol = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -650,9 +651,9 @@ MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, fl
 // where c z - m is one fused product: for a target that outweighs the rest both
 // terms are next to 0, and the difference of the rounded lse and z, which would
 // be off by 2^-24 of their size, is never formed.
-// kWarps: 32 where few blocks have thousands of pairs a row (1124 of 219 rows: 10
-// us of a call, with 8 warps 15), 8 where many blocks have few (98 of 32768 rows:
-// 12 us, with 32 warps 25).
+// kWarps: 32 while all blocks fit the device at once (a call of 3149 x 896 x 11454:
+// 44.0 us, with 8 warps 45.4; of 2048 x 768 x 32768 with 8 entries 68.5 and 77.7),
+// 8 where they come in rounds (32768 rows: 12 us of a call, with 32 warps 25).
 template <int kSlots, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,

@@ -119,13 +119,21 @@ struct Walk {
   }
 };
 
+constexpr int kPlanPairs = 76;  // pairs that work is planned for (the plans decide the workspaces)
+
 inline int ceil_div(long a, long b) { return static_cast<int>((a + b - 1) / b); }
 
-// Vocabulary tiles of one item of the forward.  A longer run writes fewer
-// pairs; the items are dealt round robin, so it must leave each pair many.
+// Vocabulary tiles of one item.  A longer run writes fewer pairs; the items are
+// dealt round robin, so it must leave each pair many, or just one where that
+// takes no more rounds of tiles (219 x 576 x 143711: 43 us, with runs of one tile 50;
+// 30 x 4096 x 50346: 80 and 83).
 inline int run_of(int nmt, int nnt) {
   const long tiles = static_cast<long>(nmt) * nnt;
-  return tiles >= 64 * 76 ? 4 : tiles >= 24 * 76 ? 2 : 1;
+  if (nmt <= kPlanPairs) {
+    const int run = ceil_div(nnt, kPlanPairs / nmt);
+    if (run <= ceil_div(tiles, kPlanPairs)) return run;
+  }
+  return tiles >= 64 * kPlanPairs ? 4 : tiles >= 24 * kPlanPairs ? 2 : 1;
 }
 
 struct ForwardPlan {
@@ -144,7 +152,6 @@ inline ForwardPlan forward_plan(int T, int V) {
 constexpr size_t kPieceBytes = static_cast<size_t>(1) << 32;  // most bytes of dz that one piece holds
 constexpr int kMinSplitBlocks = 12;                           // k blocks that a split has at least
 constexpr int kMaxSplits = 16;
-constexpr int kPlanPairs = 76;  // pairs that the splits are planned for (the plan decides the workspace)
 
 struct BackwardPlan {
   int piece, pieces;       // vocabulary rows of a piece
