@@ -742,7 +742,8 @@ __global__ void __launch_bounds__(256) vocab_ce_rows_kernel(const float* d_loss,
   const float e = d_lse ? d_lse[row] : 0.f;
   row_a[row] = d + e;
   row_l[row] = lse[row] * kLog2e;
-  const float v = d * expm1f(-loss[row]) + e * expf(-loss[row]);
+  // (no gradient: 0 whatever the loss is, infinite or no number)
+  const float v = (d == 0.f ? 0.f : d * expm1f(-loss[row])) + (e == 0.f ? 0.f : e * expf(-loss[row]));
   value[row] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
 }
 

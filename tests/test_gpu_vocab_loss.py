@@ -102,6 +102,20 @@ SHAPES = [(1, 64, 1), (1, 768, 5003), (2, 64, 2), (3, 128, 63), (31, 192, 64), (
           (1001, 192, 5003), (20, 8192, 300)]
 
 
+def test_no_gradient_whatever_a_row_holds(moe):
+    """Labels that are words, rows of infinities and NaN, no gradient."""
+    _, x, W, labels = _inputs(300, 128, 700)
+    labels = labels.clamp(0, 699)
+    x[5], x[270] = float("inf"), float("nan")
+    f = moe.cross_entropy_forward(x, W, labels)
+    d = torch.ones(300, device="cuda")
+    d[5] = d[270] = 0
+    for de in (None, torch.zeros(300, device="cuda")):
+        got = moe.cross_entropy_backward(d, x, W, labels, f["loss"], f["lse"], d_lse=de)
+        assert torch.isfinite(got["dx"].float()).all() and not got["dx"][[5, 270]].any()
+        assert got["dx"][[4, 6, 269, 271]].any(dim=1).all()
+
+
 @pytest.mark.parametrize("T,D,V", SHAPES)
 @pytest.mark.parametrize("index", [torch.int64, torch.int32], ids=["i64", "i32"])
 def test_cross_entropy(moe, T, D, V, index):
