@@ -40,7 +40,8 @@ moe_status check_head(int32_t T, int32_t D, int32_t V) {
 
 moe_status check_teacher(const moe_teacher* t, int32_t T) {
   if (!t || !known_index(t->ids_type) || !known_type(t->logits_type)) return MOE_ERR_INVALID_ARG;
-  if (t->K < 1 || !(t->temperature > 0.f) || !std::isfinite(t->temperature) || !std::isfinite(1.f / t->temperature))
+  // (the kernels multiply by log2(e) / temperature)
+  if (t->K < 1 || !(t->temperature > 0.f) || !std::isfinite(t->temperature) || !std::isfinite(2.f / t->temperature))
     return MOE_ERR_INVALID_ARG;
   if (t->K > MOE_MAX_TEACHER) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T > 0 && !all_there({t->ids, t->logits})) return MOE_ERR_INVALID_ARG;

@@ -428,7 +428,7 @@ typedef struct {
   moe_index_type ids_type;
   moe_dtype logits_type;
   int32_t K;             /* 1 <= K <= MOE_MAX_TEACHER */
-  float temperature;     /* > 0, finite */
+  float temperature;     /* > 0, finite, and so that 2 / temperature is */
 } moe_teacher;
 
 /* Distillation from the teacher's entries, with p = softmax of its logits over

@@ -74,6 +74,12 @@ def test_refusals(N, call, bad):
     assert N.lib.moe_launch_count() == 0
 
 
+@pytest.mark.parametrize("call", [_dis, _dis_bwd])
+def test_a_temperature_whose_scale_overflows_is_refused(N, call):
+    """log2(e) / temperature is no finite number, though 1 / temperature is."""
+    assert call(N, tau=3.5e-39) == N.MOE_ERR_INVALID_ARG
+
+
 def test_missing_teacher(N):
     assert N.lib.moe_distill_forward(FAKE, FAKE, None, 4, 64, 10, FAKE, FAKE, FAKE, FAKE, BIG, None) == N.MOE_ERR_INVALID_ARG
 
