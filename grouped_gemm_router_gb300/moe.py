@@ -649,6 +649,12 @@ def _float_type(t, name):
     return kind
 
 
+def _in_32_bits(where, *sizes):
+    """The C ABI takes 32-bit sizes; larger ones would be cut."""
+    if max(sizes) >= 1 << 31 or min(sizes) < 0:
+        raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, where)
+
+
 def _matrix(t, name, of):
     if t.dim() != 2:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{of}]")
@@ -686,6 +692,7 @@ def embedding_forward(ids, table, scale=1.0, out_type=None):
     if (pi | pt) & 15:
         return embedding_forward(_aligned(ids), _aligned(table), scale, out_type)
     T = ids.shape[0]
+    _in_32_bits("moe_embedding_forward", T, V, D)
     out = _empty(T, D, dtype=out_type, device=table.device)
     st = lib.moe_embedding_forward(pi, ikind, pt, tkind, scale, T, V, D, out.data_ptr(), okind, _stream_of(table))
     if st:
@@ -721,6 +728,7 @@ def embedding_backward(d_out, ids, V, scale=1.0, add=None, workspace=None):
 
 
 def embedding_backward_workspace_size(T, V, D) -> int:
+    _in_32_bits("moe_embedding_backward_scratch_size", T, V, D)
     n = int(lib.moe_embedding_backward_scratch_size(T, V, D))
     if n == 0 and T > 0:
         raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, "moe_embedding_backward_scratch_size")
@@ -730,6 +738,7 @@ def embedding_backward_workspace_size(T, V, D) -> int:
 def vocab_workspace_size(T, D, V, n_teacher=0, backward=False) -> int:
     """Bytes of workspace of cross_entropy_* (n_teacher = 0) and distill_*."""
     name = "moe_vocab_backward_workspace_size" if backward else "moe_vocab_forward_workspace_size"
+    _in_32_bits(name, T, D, V, n_teacher)
     n = int(getattr(lib, name)(T, D, V, n_teacher))
     if n == 0 and T > 0:
         raise N.MoeError(N.MOE_ERR_UNSUPPORTED_SHAPE, name)
@@ -812,6 +821,7 @@ def _teacher(ids, logits, temperature, T, dev):
     if ids.dim() != 2:
         raise ValueError(f"teacher_ids has shape {tuple(ids.shape)}, expected [{T}, K]")
     K = ids.shape[1]
+    _in_32_bits("moe_teacher", K)
     _like(ids, "teacher_ids", ids.dtype, (T, K), dev)
     _like(logits, "teacher_logits", logits.dtype, (T, K), dev)
     return N.MoeTeacher(None, None, ikind, lkind, K, temperature)

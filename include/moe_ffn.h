@@ -370,7 +370,8 @@ typedef enum { MOE_I32 = 0, MOE_I64 = 1 } moe_index_type;
 /* Embedding lookup:  out[t] = scale * table[ids[t]], rounded once.
  *   ids [T] of type ids_type; an id outside [0, V) gives a row of zeros;
  *   table [V, D] of type table_type; out [T, D] of type out_type.
- * 1 <= D <= 8192, any D; 1 <= V <= MOE_MAX_VOCAB; 0 <= T <= 2^24; scale finite. */
+ * 1 <= D <= 8192, any D; 1 <= V <= MOE_MAX_VOCAB; 0 <= T <= 2^24; scale finite.
+ * Here and below no output may overlap an input. */
 moe_status moe_embedding_forward(const void* ids, moe_index_type ids_type, const void* table,
                                  moe_dtype table_type, float scale, int32_t T, int32_t V, int32_t D,
                                  void* out, moe_dtype out_type, void* stream);

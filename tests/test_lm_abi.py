@@ -140,6 +140,33 @@ def test_binding_refuses_wrong_tensors(N):
         moe.embedding_backward_workspace_size(4, 10, 8193)
 
 
+def test_sizes_past_32_bits_are_refused(N, monkeypatch):
+    """They are not cut to what their low halves say."""
+    import torch
+    from grouped_gemm_router_gb300 import moe
+    big = 1 << 32
+    for T, V, D in ((big + 4, 10, 64), (4, big + 10, 64), (4, 10, big + 64), (4, -10, 64)):
+        with pytest.raises(N.MoeError):
+            moe.embedding_backward_workspace_size(T, V, D)
+        for backward in (False, True):
+            with pytest.raises(N.MoeError):
+                moe.vocab_workspace_size(T, D, V, backward=backward)
+    with pytest.raises(N.MoeError):
+        moe.vocab_workspace_size(4, 64, 10, n_teacher=big)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(FakeCuda, "data_ptr", lambda t: FAKE, raising=False)
+    bf, i32, f = torch.bfloat16, torch.int32, torch.float32
+    ids, y = FakeCuda((4,), i32), FakeCuda((big + 4,), i32)
+    x, W = FakeCuda((4, 64), bf), FakeCuda((10, 64), bf)
+    wide, many = FakeCuda((10, big + 64), bf), FakeCuda((big + 10, 64), bf)
+    te, lg = FakeCuda((4, big + 8), i32), FakeCuda((4, big + 8), f)
+    for call in (lambda: moe.embedding_forward(ids, wide), lambda: moe.embedding_forward(ids, many),
+                 lambda: moe.embedding_forward(y, W), lambda: moe.embedding_backward(x, ids, big + 10),
+                 lambda: moe.cross_entropy_forward(x, many, ids), lambda: moe.distill_forward(x, W, te, lg)):
+        with pytest.raises(N.MoeError):
+            call()
+
+
 def _central(f, a, i, h=1e-5):
     a = a.copy()
     a[i] += h
