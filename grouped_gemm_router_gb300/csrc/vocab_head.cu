@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Kept over it, kDz took 1450 us instead of 1500 (32768 x 768 x 50001) and
       // 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less and kGrad 2 %;
       // and lines that all pairs read at once cost less: kStats 72 us instead of 234
-      // at 1 x 1664 x 61514, the whole backward 236 instead of 284 at 8 x 704 x 194036.
+      // at 1 x 1664 x 61514, the whole backward 230 instead of 284 at 8 x 704 x 194036.
       const uint64_t pol = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;

@@ -32,8 +32,8 @@ struct VocabWork {
 };
 
 // What a unit takes, in k blocks: its own, or the epilogue that runs beside the
-// next unit's, about five (backward of 8 x 704 x 194036: 266 us; with two 289,
-// with eight 303; of 90 x 1024 x 100000: 172, 181, 201).
+// next unit's, about five (backward of 8 x 704 x 194036: 230 us; with two 254,
+// with eight 272; of 90 x 1024 x 100000: 167, 180, 196).
 __host__ MOE_DEV int unit_cost(int nkb, int splits) {
   const int blocks = (nkb + splits - 1) / splits;
   return blocks > 5 ? blocks : 5;
