@@ -12,7 +12,7 @@
 // keeps few SMs busy; the rows with tokens are then written a second time.
 // Frequent tokens would leave one warp with thousands of rows to add: aligned
 // runs of `chunk` sorted tokens with one id are summed by warps of their own
-// beforehand, and a long run is then added by a whole block.
+// beforehand, the long runs are listed, and each is then added by a whole block.
 #include <algorithm>
 #include <mutex>
 
@@ -178,6 +178,7 @@ struct SortArgs {
   uint32_t* tok_out;
   uint32_t* lists[4];       // keys and tokens, twice
   int pass, passes;
+  uint32_t* n_long;         // set to 0
 };
 
 MOE_DEV uint32_t sort_key(const SortArgs& a, int i) {
@@ -307,6 +308,7 @@ MOE_DEV void sort_pass(const SortArgs& a, int block, SortSmem& sm) {
 __global__ void __launch_bounds__(kSortThreads) embedding_hist_kernel(SortArgs a) {
   __shared__ uint32_t h[kMaxBins];
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_long = 0;
   first_histogram(a, blockIdx.x, h);
 }
 
@@ -343,6 +345,7 @@ template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) embedding_sort_short_kernel(SortArgs a) {
   __shared__ ShortSmem sm;
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_long = 0;
   const int bins = 1 << a.bits, block = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_warp = a.block / kSortWarps;                      // a multiple of 32
@@ -480,12 +483,14 @@ struct SumArgs {
   float* d_table;
   float scale;
   int T, V, D, chunk, chunks;
-  int window_blocks;
-  int2* long_runs;         // [window_blocks, kSumWarps], with chunks
+  int window_blocks, chunk_blocks;
+  int2* long_runs;         // with chunks: [start, end) of each
+  uint32_t* n_long;
 };
 
 constexpr int kWindow = 4;     // sorted tokens of a warp
 constexpr int kSumWarps = 8;
+constexpr int kSumBlocks = 2;  // of an SM
 constexpr int kLong = 16;      // tokens past its window that a warp adds alone
 
 // A warp's columns of one turn: kVecs pieces of a lane, kAhead rows in flight.
@@ -596,82 +601,80 @@ MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float
     }
 }
 
-// Long runs [start, end) (start < 0: none), each by the whole block: rows up to
-// the first chunk that lies inside, the chunks' sums, the rows behind them;
+// One turn of columns of the long run [start, end), by the whole block: rows up
+// to the first chunk that lies inside, the chunks' sums, the rows behind them;
 // every warp takes a share.
 template <int VEC, bool kF32>
-MOE_DEV void add_long_runs(const SumArgs& a, const int2 (&runs)[kSumWarps], int turn0, int turn1,
-                           float (&red)[kSumWarps][Shape<VEC, kF32>::kColumns]) {
+MOE_DEV void add_long_run(const SumArgs& a, int start, int end, int turn,
+                          float (&red)[kSumWarps][Shape<VEC, kF32>::kColumns]) {
   constexpr int kVecs = Shape<VEC, kF32>::kVecs, kColumns = Shape<VEC, kF32>::kColumns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nv = a.D / VEC;
+  const int c0 = (start + a.chunk - 1) / a.chunk, c1 = a.chunks ? max(c0, end / a.chunk) : c0;
+  const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
+  const int tail = c0 < c1 ? c1 * a.chunk : end;
+  auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
+  const int col = turn * 32 * kVecs, v0 = col + lane;
+  float acc[kVecs][VEC] = {};
+  const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
+  add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
+  const int m0 = c0 + share(c1 - c0, warp), m1 = c0 + share(c1 - c0, warp + 1);
+  add_rows<VEC, true>(a.part, a.D, v0, nv, m1 - m0, [&](int r) { return m0 + r; }, acc);
+  const int t0 = tail + share(end - tail, warp), t1 = tail + share(end - tail, warp + 1);
+  add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, t1 - t0, [&](int r) { return a.tok[t0 + r]; }, acc);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) red[warp][(32 * i + lane) * VEC + e] = acc[i][e];
+  __syncthreads();
+  const size_t dst = static_cast<size_t>(a.key[start]) * a.D;
+  for (int c = threadIdx.x; c < kColumns; c += 32 * kSumWarps) {
+    const int column = col * VEC + c;
+    if (column >= a.D) break;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
+    const float o[1] = {a.scale * sum};
+    if (a.add) add_vec<1>(a.d_table + dst + column, o);
+    else a.d_table[dst + column] = o[0];
+  }
+  __syncthreads();
+}
+
+// The listed long runs, a turn of columns at a time.  (A block for each block of
+// windows, most of them with nothing to do: 187 us a call of 200000 x 768 into
+// 50001 rows instead of 174.)
+template <int VEC, bool kF32>
+__global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_long_kernel(SumArgs a, int turns) {
+  __shared__ float red[kSumWarps][Shape<VEC, kF32>::kColumns];
+  griddep_wait();
+  const int n = static_cast<int>(*a.n_long) * turns;
 #pragma unroll 1
-  for (int w = 0; w < kSumWarps; ++w) {
-    const int start = runs[w].x, end = runs[w].y;
-    if (start < 0) continue;
-    const int c0 = (start + a.chunk - 1) / a.chunk, c1 = a.chunks ? max(c0, end / a.chunk) : c0;
-    const int head = c0 < c1 ? c0 * a.chunk - start : end - start;
-    const int tail = c0 < c1 ? c1 * a.chunk : end;
-    auto share = [&](int n, int i) { return static_cast<int>(static_cast<long long>(n) * i / kSumWarps); };
-#pragma unroll 1
-    for (int turn = turn0; turn < turn1; ++turn) {
-      const int col = turn * 32 * kVecs, v0 = col + lane;
-      float acc[kVecs][VEC] = {};
-      const int h0 = start + share(head, warp), h1 = start + share(head, warp + 1);
-      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, h1 - h0, [&](int r) { return a.tok[h0 + r]; }, acc);
-      const int m0 = c0 + share(c1 - c0, warp), m1 = c0 + share(c1 - c0, warp + 1);
-      add_rows<VEC, true>(a.part, a.D, v0, nv, m1 - m0, [&](int r) { return m0 + r; }, acc);
-      const int t0 = tail + share(end - tail, warp), t1 = tail + share(end - tail, warp + 1);
-      add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, t1 - t0, [&](int r) { return a.tok[t0 + r]; }, acc);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) red[warp][(32 * i + lane) * VEC + e] = acc[i][e];
-      __syncthreads();
-      const size_t dst = static_cast<size_t>(a.key[start]) * a.D;
-      for (int c = threadIdx.x; c < kColumns; c += 32 * kSumWarps) {
-        const int column = col * VEC + c;
-        if (column >= a.D) break;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
-        const float o[1] = {a.scale * sum};
-        if (a.add) add_vec<1>(a.d_table + dst + column, o);
-        else a.d_table[dst + column] = o[0];
-      }
-      __syncthreads();
-    }
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int2 run = a.long_runs[i / turns];
+    add_long_run<VEC, kF32>(a, run.x, run.y, i % turns, red);
   }
 }
 
-// The long runs that the windows of one block have found, a turn of columns a
-// block.
+// A warp a window of sorted tokens: the rows whose tokens begin there.  The
+// first blocks sum the chunks, which takes longest (as the last ones: 76 us a call
+// of 32768 x 768 into 50001 rows instead of 70); the long runs, listed here, wait
+// for those.
 template <int VEC, bool kF32>
-__global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_long_kernel(SumArgs a) {
-  __shared__ float red[kSumWarps][Shape<VEC, kF32>::kColumns];
-  __shared__ int2 runs[kSumWarps];
-  griddep_wait();
-  if (threadIdx.x < kSumWarps) runs[threadIdx.x] = a.long_runs[blockIdx.x * kSumWarps + threadIdx.x];
-  __syncthreads();
-  add_long_runs<VEC, kF32>(a, runs, blockIdx.y, blockIdx.y + 1, red);
-}
-
-// A warp a window of sorted tokens: the rows whose tokens begin there.  Blocks
-// past the windows' sum the chunks; the long runs then wait for those.
-template <int VEC, bool kF32>
-__global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_rows_kernel(SumArgs a) {
   constexpr int kVecs = Shape<VEC, kF32>::kVecs, R = kAhead<VEC, kF32, kVecs>;
   static_assert(kWindow % R == 0);
   __shared__ float red[kSumWarps][Shape<VEC, kF32>::kColumns];
   __shared__ int2 runs[kSumWarps];
   griddep_launch_dependents();
   griddep_wait();
-  if (static_cast<int>(blockIdx.x) >= a.window_blocks) {
-    sum_chunk<VEC, kF32>(a, (blockIdx.x - a.window_blocks) * kSumWarps + (threadIdx.x >> 5));
+  const int block = static_cast<int>(blockIdx.x) - a.chunk_blocks;
+  if (block < 0) {
+    sum_chunk<VEC, kF32>(a, blockIdx.x * kSumWarps + (threadIdx.x >> 5));
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int p0 = (blockIdx.x * kSumWarps + warp) * kWindow;
+  const int p0 = (block * kSumWarps + warp) * kWindow;
   const int nv = a.D / VEC;
   const uint32_t none = static_cast<uint32_t>(a.V);  // tokens without a row, sorted to the end, and what lies past it
   const int at = p0 - 1 + lane;                      // lane 0 sees the token before the window
@@ -679,18 +682,12 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
   const uint32_t my_tok = a.tok[min(max(at, 0), a.T - 1)];
   const uint32_t k_before = __shfl_up_sync(0xffffffffu, k, 1);
   const uint32_t begins = __ballot_sync(0xffffffffu, lane >= 1 && lane <= kWindow && k != k_before && k < none) >> 1;
-  int len_past = 0;  // of the last run, behind the window
-  if (begins) {
-    const uint32_t last = __shfl_sync(0xffffffffu, k, kWindow);
-    if (last < none && __shfl_sync(0xffffffffu, k, kWindow + 1) == last) {
-      const int begin = p0 + 31 - __clz(begins);
-      const int end = end_of(a.key, p0 + kWindow, a.T, last);
-      len_past = end - (p0 + kWindow);
-      if (lane == 0) runs[warp] = make_int2(begin, end);
-    }
-  }
+  // tokens of the last run behind the window, as far as the lanes see
+  const uint32_t last = __shfl_sync(0xffffffffu, k, kWindow);
+  const int len_past = __popc(__ballot_sync(0xffffffffu, begins != 0 && lane > kWindow && k == last && last < none));
+  static_assert(kWindow + 1 + kLong < 32);
   const bool is_long = len_past > kLong;
-  if (lane == 0 && !is_long) runs[warp] = make_int2(-1, -1);
+  if (lane == 0) runs[warp] = make_int2(-1, -1);
   if (begins) {
     const int first = __ffs(begins) - 1;
     // past the window, a run too long for this warp, or the tokens without a row
@@ -716,19 +713,27 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) embedding_rows_kernel(SumAr
             for (int e = 0; e < VEC; ++e) acc[i][e] = begin ? x[r][i][e] : acc[i][e] + x[r][i][e];
           if (j + 1 < stop && !(begins >> (j + 1) & 1)) continue;
           if (j + 1 == kWindow)
-            add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past, [&](int q) { return a.tok[p0 + kWindow + q]; }, acc);
+            add_rows<VEC, kF32>(a.d_out, a.D, v0, nv, len_past,
+                                [&](int q) { return __shfl_sync(0xffffffffu, my_tok, kWindow + 1 + q); }, acc);
           write_row(a, __shfl_sync(0xffffffffu, k, j + 1), v0, nv, acc);
         }
       }
     }
   }
-  if (a.chunks) {
-    __syncwarp();
-    if (lane == 0) a.long_runs[blockIdx.x * kSumWarps + warp] = runs[warp];
-    return;
+  if (is_long) {
+    const int end = end_of(a.key, p0 + kWindow, a.T, last);
+    const int2 run = make_int2(p0 + 31 - __clz(begins), end);
+    // (any order will do: each run is added by itself)
+    if (lane == 0 && a.chunks) a.long_runs[atomicAdd(a.n_long, 1u)] = run;
+    else if (lane == 0) runs[warp] = run;
   }
+  if (a.chunks) return;
   __syncthreads();
-  add_long_runs<VEC, kF32>(a, runs, 0, (nv + 32 * kVecs - 1) / (32 * kVecs), red);
+#pragma unroll 1
+  for (int w = 0; w < kSumWarps; ++w)
+    if (runs[w].x >= 0)
+#pragma unroll 1
+      for (int turn = 0; turn * 32 * kVecs < nv; ++turn) add_long_run<VEC, kF32>(a, runs[w].x, runs[w].y, turn, red);
 }
 
 // fp32 rows are read 32 bytes at a time.
@@ -737,12 +742,14 @@ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int VEC, bool kF32>
-cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
+cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
   const int turns = (a.D + Shape<VEC, kF32>::kColumns - 1) / Shape<VEC, kF32>::kColumns;
-  const unsigned grid = a.window_blocks + static_cast<unsigned>((static_cast<long long>(a.chunks) * turns + kSumWarps - 1) / kSumWarps);
-  const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(grid), dim3(32 * kSumWarps), 0, s, true, a);
+  a.chunk_blocks = (a.chunks * turns + kSumWarps - 1) / kSumWarps;
+  const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(a.window_blocks + a.chunk_blocks),
+                                      dim3(32 * kSumWarps), 0, s, true, a);
   if (e != cudaSuccess || !a.chunks) return e;
-  return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(a.window_blocks, turns), dim3(32 * kSumWarps), 0, s, true, a);
+  const int fit = kSumBlocks * std::max(current_device_sms(), 1);
+  return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(fit), dim3(32 * kSumWarps), 0, s, true, a, turns);
 }
 
 std::mutex g_mu;
@@ -779,6 +786,9 @@ size_t hist_bytes(int T, const SortPlan& p) {
 
 int window_blocks(int T) { return (T + kSumWarps * kWindow - 1) / (kSumWarps * kWindow); }
 
+// Long runs of T sorted tokens at most, each with a token in its window.
+size_t most_long(int T) { return static_cast<size_t>(T) / (kLong + 2) + 1; }
+
 }  // namespace
 
 cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s) {
@@ -789,7 +799,7 @@ size_t embedding_bwd_scratch_bytes(int T, int V, int D) {
   const SortPlan p = sort_plan(T, V);
   return padded(hist_bytes(T, p)) +
          4 * padded(static_cast<size_t>(T) * sizeof(uint32_t)) + padded(static_cast<size_t>(p.chunks) * D * sizeof(float)) +
-         padded(p.chunks ? window_blocks(T) * kSumWarps * sizeof(int2) : 0);
+         padded(sizeof(uint32_t)) + padded(p.chunks ? most_long(T) * sizeof(int2) : 0);
 }
 
 cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaStream_t s) {
@@ -813,7 +823,8 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   q.hist = reinterpret_cast<uint32_t*>(take(hist_bytes(a.T, p)));
   for (auto& l : q.lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
-  int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? window_blocks(a.T) * kSumWarps * sizeof(int2) : 0));
+  q.n_long = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t)));
+  int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? most_long(a.T) * sizeof(int2) : 0));
   cudaError_t e = cudaSuccess;
   if (a.T > 0 && a.T <= kShortList) {
     e = launch_sort_short(q, p.cluster, s);
@@ -835,7 +846,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   if (e != cudaSuccess || a.T == 0) return e;
   const int last = a.T <= kShortList ? 0 : (p.passes - 1) & 1;
   const SumArgs m{a.d_out, a.add, q.lists[2 * last], q.lists[2 * last + 1], part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks,
-                  window_blocks(a.T), long_runs};
+                  window_blocks(a.T), 0, long_runs, q.n_long};
   if (a.D % 8 == 0 && (!a.d_fp32 || on32(a.d_out))) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);
   return a.d_fp32 ? launch_sums<1, true>(m, s) : launch_sums<1, false>(m, s);
 }
