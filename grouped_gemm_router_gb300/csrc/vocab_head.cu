@@ -60,6 +60,7 @@ constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kBoxBytes + 1024;
 
 struct VocabArgs : VocabWork {
   int T, V, D;
+  int box;                 // rows of a box of tokens
   int v0, Vc, Vcp;         // kDz, kGrad: the piece's first row, its rows, and those rounded up to 64
   float c;
   unsigned int* dev_err;
@@ -226,16 +227,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and lines that all pairs read at once cost less: kStats 72 us instead of 234
       // at 1 x 1664 x 61514, the whole backward 230 instead of 284 at 8 x 704 x 194036.
       const uint64_t pol = l2_policy_evict_last();
+      auto load_tokens = [&](uint32_t dst, const CUtensorMap& map, int row, int block, uint32_t full) {
+        tma_load_3d_pair(dst, &map, full, 0, row, block, pol);
+        if (p.box < 128) tma_load_3d_pair(dst + kOperandBytes / 2, &map, full, 0, row, block + 1, pol);
+      };
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
       bool ok = true;
       while (ok && walk.next(p, pair, npairs, u)) {
+        const bool dw = kMode == kGrad && u.which == 1;
         const int m0 = u.m * kTile + 128 * rank, n0 = u.n * kTile + 128 * rank;
-        // x past the last token is not loaded (zeros at best): few tokens are read
-        // by all pairs at once, and then every read counts
-        const bool load_x = kMode == kGrad || m0 < p.T, peer_x = kMode == kGrad || u.m * kTile + 128 < p.T;
-        const uint32_t bytes = 2 * kStageBytes - (peer_x ? 0 : kOperandBytes);
+        // rows past the last token are not loaded, nor zeroed: they hold anything, and
+        // nothing reads what comes of them
+        const bool here = dw || m0 < p.T, peer = dw || u.m * kTile + 128 < p.T;
+        const uint32_t bytes = 256 * ((peer ? 2 : 1) * p.box + 2 * (dw ? p.box : 128));
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&ctl.empty[stage]), phase ^ 1u, abort_flag, dev_err)) {
             ok = false;
@@ -246,14 +252,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[stage]), bytes);
           if constexpr (kMode == kGrad) {
             if (u.which == 0) {  // dz rows, W's rows as k
-              tma_load_3d_pair(sa, &mapZ, full_leader, 0, m0, kb * (kBK / 64), pol);
+              if (here) load_tokens(sa, mapZ, m0, kb * (kBK / 64), full_leader);
               tma_load_3d_pair(sb, &mapW, full_leader, 0, p.v0 + kb * kBK, n0 / 64, pol);
             } else {  // dz columns, tokens as k
-              tma_load_3d_pair(sa, &mapZ, full_leader, 0, kb * kBK, m0 / 64, pol);
-              tma_load_3d_pair(sb, &mapX, full_leader, 0, kb * kBK, n0 / 64, pol);
+              load_tokens(sa, mapZ, kb * kBK, m0 / 64, full_leader);
+              load_tokens(sb, mapX, kb * kBK, n0 / 64, full_leader);
             }
           } else {
-            if (load_x) tma_load_3d_pair(sa, &mapX, full_leader, 0, m0, kb * (kBK / 64), pol);
+            if (here) load_tokens(sa, mapX, m0, kb * (kBK / 64), full_leader);
             tma_load_3d_pair(sb, &mapW, full_leader, 0, p.v0 + n0, kb * (kBK / 64), pol);
           }
           ++issued;
@@ -301,8 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after_sync();
           const uint32_t sa = smem_base + stage * kStageBytes, sb = sa + kOperandBytes;
+          const int slices = kMode == kGrad && u.which == 1 ? p.box / 16 : kBK / 16;
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
+            if (kk >= slices) break;
             const uint32_t k_major = (kk >> 2) * 16384 + (kk & 3) * 32, mn_major = kk * 2048;
             const uint64_t adesc = smem_desc_sw128(sa + (a_mn ? mn_major : k_major), a_lbo, 1024);
             const uint64_t bdesc = smem_desc_sw128(sb + (b_mn ? mn_major : k_major), b_mn ? 16384 : 16, 1024);
@@ -947,6 +955,15 @@ size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const Backwar
   return t.off;
 }
 
+// Rows of a box of tokens: 128, with two blocks of columns, or as many as there
+// are (in slices of 16 of a reduction over them), with one.  TMA fills what lies
+// outside a tensor with zeros, which takes longer than loading as much (forward of
+// 8 x 704 x 194036: 78 us with 120 rows of zeros in every box, 58 so; two boxes of
+// one block instead of one of two throughout: 1480 us at 32768 x 768 x 50001 instead
+// of 1360).
+int token_box(int T) { return T < 128 ? (T + 15) / 16 * 16 : 128; }
+int box_blocks(int box) { return box < 128 ? 1 : 2; }
+
 // The kernel for a teacher of K entries.
 template <typename Kernel>
 Kernel by_slots(int K, Kernel k1, Kernel k2, Kernel k4, Kernel k8) {
@@ -1002,8 +1019,9 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   v.keys = keys;
   v.target = v.K ? a.target : t.get<float>(a.T);
   v.dev_err = st.dev_err;
+  v.box = token_box(a.T);
   CUtensorMap mx, mw;
-  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
+  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, box_blocks(v.box), v.box)) != cudaSuccess) return e;
   if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
   const float inv_tau = 1.f / a.temperature;
   if (v.K) {
@@ -1046,8 +1064,9 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   v.direct[1] = dw_direct;
   v.dx_part = r.dx_part;
   v.dev_err = st.dev_err;
+  v.box = token_box(a.T);
   CUtensorMap mx, mw, mz, mz_out, mdx, mdw;
-  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, 2, 128)) != cudaSuccess) return e;
+  if ((e = tensor_map_blocks(&mx, a.x, a.T, a.D, box_blocks(v.box), v.box)) != cudaSuccess) return e;
   if ((e = tensor_map_blocks(&mw, a.W, a.V, a.D, 2, 128)) != cudaSuccess) return e;
   e = dx_direct ? tensor_map_2d(&mdx, a.dx, a.T, a.D, 32, 64)
                 : tensor_map_f32_3d(&mdx, r.dx_part, a.D, a.T, b.splits_x, 32, 32);
@@ -1066,7 +1085,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
     v.Vc = std::min(b.piece, a.V - v.v0);
     v.Vcp = ceil_div(v.Vc, 64) * 64;
     v.accumulate = i > 0;
-    if ((e = tensor_map_block_major(&mz, r.dz, a.T, v.Vcp / 64, 128, 2)) != cudaSuccess) return e;
+    if ((e = tensor_map_block_major(&mz, r.dz, a.T, v.Vcp / 64, v.box, box_blocks(v.box))) != cudaSuccess) return e;
     if ((e = tensor_map_block_major(&mz_out, r.dz, a.T, v.Vcp / 64, 32, 1)) != cudaSuccess) return e;
     v.VocabWork::operator=(dz_work(b, a.D, v.Vc));
     e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, true);

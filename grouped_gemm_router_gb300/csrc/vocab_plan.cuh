@@ -29,14 +29,16 @@ struct VocabWork {
   // them, the tiles and the units that this makes
   int nkb[2];
   int splits[2], n_units[2], tiles_m[2], tiles_n;
+  int longer;  // which of the two has the longer units
 };
 
-// What a unit takes, in k blocks: its own, or the epilogue that runs beside the
-// next unit's, about five (backward of 8 x 704 x 194036: 230 us; with two 254,
-// with eight 272; of 90 x 1024 x 100000: 167, 180, 196).
+// What a unit takes, in k blocks: its own and one to begin with, or the epilogue
+// that runs beside the next unit's, about three (backward of 8 x 704 x 194036: 189
+// us; with its own blocks, but at least two of them 200, at least four 202; of 300 x
+// 1024 x 100000: 207, with at least three and none to begin with 222).
 __host__ MOE_DEV int unit_cost(int nkb, int splits) {
   const int blocks = (nkb + splits - 1) / splits;
-  return blocks > 5 ? blocks : 5;
+  return blocks > 2 ? blocks + 1 : 3;
 }
 
 __host__ MOE_DEV int least(int a, int b) { return a < b ? a : b; }
@@ -56,66 +58,79 @@ struct Walk {
   int it = -1;
 
   __host__ MOE_DEV bool next(const VocabWork& p, int pair, int npairs, Unit& u) {
-    if constexpr (kMode == kGrad) {
+    constexpr int kGroup = kMode == kStats ? kGroupStats : kGroupDz;
+    for (;;) {
       ++it;
-      // The class of longer units first, dealt round robin; then the other's:
-      // as many as fit go to the pairs that got one long unit less.
-      const int big = p.nkb[0] / p.splits[0] >= p.nkb[1] / p.splits[1] ? 0 : 1, small = big ^ 1;
-      const int na = p.n_units[big], nb = p.n_units[small];
-      int i = it, which = big, idx;
-      const int len_a = pair < na ? (na - pair - 1) / npairs + 1 : 0;
-      if (i < len_a) {
-        idx = pair + i * npairs;
-      } else {
-        i -= len_a;
-        which = small;
-        const int r = na % npairs;
-        const int cost_a = unit_cost(p.nkb[big], p.splits[big]), cost_b = unit_cost(p.nkb[small], p.splits[small]);
-        const int fill = r == 0 ? 0 : least(nb, (npairs - r) * (cost_a / cost_b));
-        int len_f = 0;
-        const int first = pair - r;
-        if (first >= 0 && first < fill) len_f = (fill - first - 1) / (npairs - r) + 1;
-        if (i < len_f) {
-          idx = first + i * (npairs - r);
-        } else {
-          idx = fill + (pair - r + npairs) % npairs + (i - len_f) * npairs;
-          if (idx >= nb) return false;
-        }
-      }
-      u.which = which;
-      u.n = idx % p.tiles_n;
-      idx /= p.tiles_n;
-      u.m = idx % p.tiles_m[which];
-      u.split = idx / p.tiles_m[which];
-      // splits differ by at most one block, and none is empty
-      u.kb0 = static_cast<int>(static_cast<long long>(p.nkb[which]) * u.split / p.splits[which]);
-      u.kb1 = static_cast<int>(static_cast<long long>(p.nkb[which]) * (u.split + 1) / p.splits[which]);
+      const int item = pair + it / p.run * npairs;
+      if (item >= p.items) return false;
+      const int sub = it % p.run;
+      // row tiles in groups; within a group all its rows before the next run of the vocabulary
+      const int runs = (p.nnt + p.run - 1) / p.run;
+      const int g = item / (kGroup * runs);
+      const int in_group = least(kGroup, p.nmt - g * kGroup);
+      const int r = item - g * kGroup * runs;
+      u.slot = r / in_group;
+      u.m = g * kGroup + r % in_group;
+      u.n = u.slot * p.run + sub;
+      if (u.n >= p.nnt) continue;
+      u.first = sub == 0;
+      u.last = sub == p.run - 1 || u.n == p.nnt - 1;
+      u.kb0 = 0;
+      u.kb1 = p.nkb[0];
+      u.which = 0;
+      u.split = 0;
       return true;
-    } else {
-      constexpr int kGroup = kMode == kStats ? kGroupStats : kGroupDz;
-      for (;;) {
-        ++it;
-        const int item = pair + it / p.run * npairs;
-        if (item >= p.items) return false;
-        const int sub = it % p.run;
-        // row tiles in groups; within a group all its rows before the next run of the vocabulary
-        const int runs = (p.nnt + p.run - 1) / p.run;
-        const int g = item / (kGroup * runs);
-        const int in_group = least(kGroup, p.nmt - g * kGroup);
-        const int r = item - g * kGroup * runs;
-        u.slot = r / in_group;
-        u.m = g * kGroup + r % in_group;
-        u.n = u.slot * p.run + sub;
-        if (u.n >= p.nnt) continue;
-        u.first = sub == 0;
-        u.last = sub == p.run - 1 || u.n == p.nnt - 1;
-        u.kb0 = 0;
-        u.kb1 = p.nkb[0];
-        u.which = 0;
-        u.split = 0;
-        return true;
-      }
     }
+  }
+};
+
+// kGrad: the class of longer units first, dealt round robin; then the other's: as
+// many as fit go to the pairs that got one long unit less, the rest to all.  Where
+// a pair's share of each begins is worked out once, not for every unit (1290 x 576
+// x 72446: 290 us, with those divisions 305).
+template <>
+struct Walk<kGrad> {
+  int stage = -1, idx = 0, step = 0, left = 0;
+
+  __host__ MOE_DEV void begin(const VocabWork& p, int pair, int npairs) {
+    const int a = p.longer, b = a ^ 1, na = p.n_units[a], nb = p.n_units[b];
+    const int r = na % npairs;  // the first r pairs have one more
+    const int cost_a = unit_cost(p.nkb[a], p.splits[a]), cost_b = unit_cost(p.nkb[b], p.splits[b]);
+    const int fill = r == 0 ? 0 : least(nb, (npairs - r) * (cost_a / cost_b));
+    int end;
+    if (stage == 0) {
+      idx = pair, step = npairs, end = na;
+    } else if (stage == 1) {
+      idx = pair >= r ? pair - r : fill, step = npairs - r, end = fill;
+    } else {
+      idx = fill + (pair - r + npairs) % npairs, step = npairs, end = nb;
+    }
+    left = idx < end ? (end - idx - 1) / step + 1 : 0;
+  }
+
+  __host__ MOE_DEV bool next(const VocabWork& p, int pair, int npairs, Unit& u) {
+    idx += step;
+    while (left == 0) {
+      if (++stage == 3) return false;
+      begin(p, pair, npairs);
+    }
+    --left;
+    const int which = stage == 0 ? p.longer : p.longer ^ 1;
+    const unsigned tile = static_cast<unsigned>(idx) / static_cast<unsigned>(p.tiles_n);
+    u.which = which;
+    u.n = idx - static_cast<int>(tile) * p.tiles_n;
+    u.split = 0;
+    u.m = static_cast<int>(tile);
+    u.kb0 = 0;
+    u.kb1 = p.nkb[which];
+    if (p.splits[which] > 1) {
+      // splits differ by at most one block, and none is empty
+      u.split = u.m / p.tiles_m[which];
+      u.m -= u.split * p.tiles_m[which];
+      u.kb0 = p.nkb[which] * u.split / p.splits[which];
+      u.kb1 = p.nkb[which] * (u.split + 1) / p.splits[which];
+    }
+    return true;
   }
 };
 
@@ -151,7 +166,7 @@ inline ForwardPlan forward_plan(int T, int V) {
 
 constexpr size_t kPieceBytes = static_cast<size_t>(1) << 32;  // most bytes of dz that one piece holds
 constexpr int kMinSplitBlocks = 12;                           // k blocks that a split has at least
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = kPlanPairs;                        // (32 x 64 x 150000: 59 us, with up to 16 splits 76)
 
 struct BackwardPlan {
   int piece, pieces;       // vocabulary rows of a piece
@@ -207,6 +222,7 @@ inline VocabWork grad_work(const BackwardPlan& b, int T, int Vc) {
   w.tiles_m[0] = b.nmt;
   w.tiles_m[1] = ceil_div(Vc, kTile);
   for (int i = 0; i < 2; ++i) w.n_units[i] = w.tiles_m[i] * w.tiles_n * w.splits[i];
+  w.longer = w.nkb[0] / w.splits[0] >= w.nkb[1] / w.splits[1] ? 0 : 1;
   return w;
 }
 
