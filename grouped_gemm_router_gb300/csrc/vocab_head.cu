@@ -18,13 +18,13 @@
 //   dx [T, D] += dz W[piece],   dW[piece] = dz^T x,
 // so that the tiles of one fill the last wave of the other.  The values at the
 // targets (a q - p, where the two terms nearly cancel for a token that is
-// known well) are formed in fp32 apart from it: a label's by vocab_ce_rows_kernel,
-// for the epilogue to store, a teacher's entries' by vocab_distill_targets_kernel,
-// over what the epilogue has stored.
+// known well) are formed in fp32 apart from it: a label's by the epilogue from the
+// loss, a teacher's entries' by vocab_distill_targets_kernel, over what the epilogue
+// has stored.
 // dz is stored block by block of 64 columns, [Vc / 64][T][64], so that a warp's
-// 32 x 64 box is 4 KB in a row.  It is the one intermediate that is rounded to fewer than 32 bits: a bf16
-// operand is what the tensor cores take at full rate, and a relative rounding
-// of 2^-9 of each term averages out in sums over V or T.
+// 32 x 64 box is 4 KB in a row.  It is the one intermediate that is rounded to fewer
+// than 32 bits: a bf16 operand is what the tensor cores take at full rate, and a
+// relative rounding of 2^-9 of each term averages out in sums over V or T.
 //
 // Shared-memory operand layouts (TMA, 128-byte swizzle): x, W and dz are all
 // read in boxes {64 columns, 128 rows, 2 column blocks} of the view
@@ -72,9 +72,11 @@ struct VocabArgs : VocabWork {
   float* target;           // kStats: z at the targets [T] or [T, K]
   float2* part;            // kStats: (maximum, sum) [2 runs, rows_padded]
   int rows_padded;
-  const float* row_a;      // kDz: a of each row, lse log2(e)
-  const float* row_l;
-  const uint16_t* value;   // kDz, K = 0: dz at the labels [T]
+  const float* row_a;      // kDz, K > 0: a of each row
+  const float* lse;        // kDz
+  const float* loss;       // kDz, K = 0
+  const float* d_loss;
+  const float* d_lse;
   int direct[2];           // kGrad, dx and dW: stored as bf16; otherwise fp32 partials
   int accumulate;          // dx partials are added to those of the piece before
   const float* dx_part;    // [splits, T, D]
@@ -150,6 +152,22 @@ struct Targets {
     pos = lo + 4;
   }
 };
+
+// a of a row: of cross entropy d_loss + d_lse, where a token without a loss has no
+// d_loss.
+MOE_DEV float factor_of(const VocabArgs& p, int row) {
+  if (p.K > 0) return p.row_a[row];
+  const long long id = load_index(p.labels, p.labels64, row);
+  return (id >= 0 && id < p.V ? p.d_loss[row] : 0.f) + (p.d_lse ? p.d_lse[row] : 0.f);
+}
+
+// dz at a token's label, d_loss (q - 1) + d_lse q with q - 1 = expm1(-loss), as
+// bf16.  (No gradient: 0 whatever the loss is, infinite or no number.)
+MOE_DEV uint16_t at_label(const VocabArgs& p, int row) {
+  const float d = p.d_loss[row], e = p.d_lse ? p.d_lse[row] : 0.f, loss = p.loss[row];
+  const float v = (d == 0.f ? 0.f : d * expm1f(-loss)) + (e == 0.f ? 0.f : e * expf(-loss));
+  return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+}
 
 // Element j of 32 registers, by halves.  (Through the warp's buffer in shared
 // memory, which the MMAs read at the same time: 400 us instead of 340, 32768 x 768
@@ -355,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           run_max = -INFINITY;
           run_sum = 0.f;
           if constexpr (kMode == kDz) {
-            row_a = row < p.T ? p.row_a[row] : 0.f;
-            row_l = row < p.T ? p.row_l[row] : 0.f;
+            row_a = row < p.T ? factor_of(p, row) : 0.f;
+            row_l = row < p.T ? p.lse[row] * kLog2e : 0.f;
           }
         }
       }
@@ -435,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int end = p.v0 + cc + 64;
           if (tg.id() < end) {
             const int j = tg.id() - (end - 64);
-            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) = p.value[row];
+            *reinterpret_cast<uint16_t*>(mine + (((j >> 3) ^ (lane & 7)) << 4) + (j & 7) * 2) = at_label(p, row);
             tg.step(p, row, half);
           }
           fence_proxy_async_smem();
@@ -735,45 +753,21 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 }
 
-// Backward of cross entropy: a and lse log2(e) of each row, and dz at its label,
-//   d_loss (q - 1) + d_lse q with q - 1 = expm1(-loss).
-__global__ void __launch_bounds__(256) vocab_ce_rows_kernel(const float* d_loss, const float* d_lse, const float* loss,
-                                                            const float* lse, VocabTargets t, int T, int V, float* row_a,
-                                                            float* row_l, uint16_t* value) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int row = blockIdx.x * 256 + threadIdx.x;
-  if (row >= T) return;
-  const long long id = load_index(t.ids, t.ids64, row);
-  const float d = id >= 0 && id < V ? d_loss[row] : 0.f;
-  const float e = d_lse ? d_lse[row] : 0.f;
-  row_a[row] = d + e;
-  row_l[row] = lse[row] * kLog2e;
-  // (no gradient: 0 whatever the loss is, infinite or no number)
-  const float v = (d == 0.f ? 0.f : d * expm1f(-loss[row])) + (e == 0.f ? 0.f : e * expf(-loss[row]));
-  value[row] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
-}
-
-// Backward of distillation: the same two numbers of each row; a token without
-// entries has neither.
+// Backward of distillation: a of each row; a token without entries has none.
 __global__ void __launch_bounds__(32 * kRowWarps)
-    vocab_distill_rows_kernel(const float* d_loss, const float* lse, VocabTargets t, int T, int V, float inv_tau,
-                              float* row_a, float* row_l) {
+    vocab_distill_rows_kernel(const float* d_loss, VocabTargets t, int T, int V, float inv_tau, float* row_a) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (row >= T) return;
   bool any = false;
-  for (int j = lane; j < t.K; j += 32) {
+  for (int j0 = 0; j0 < t.K && !any; j0 += 32) {
+    const int j = min(j0 + lane, t.K - 1);
     const size_t at = static_cast<size_t>(row) * t.K + j;
     const long long id = load_index(t.ids, t.ids64, at);
-    any |= id >= 0 && id < V && !(teacher_logit(t, at) * inv_tau == -INFINITY);
+    any = __any_sync(0xffffffffu, id >= 0 && id < V && !(teacher_logit(t, at) * inv_tau == -INFINITY));
   }
-  any = __any_sync(0xffffffffu, any);
-  if (lane == 0) {
-    row_a[row] = any ? d_loss[row] * inv_tau : 0.f;
-    row_l[row] = lse[row] * kLog2e;
-  }
+  if (lane == 0) row_a[row] = any ? d_loss[row] * inv_tau : 0.f;
 }
 
 // dz at the teacher's entries of a piece's columns,
@@ -833,20 +827,31 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   }
 }
 
-// bf16 sums of fp32 partials [n_parts, n] in their order, n a multiple of 8.
-__global__ void __launch_bounds__(256) vocab_sum_kernel(const float* part, int n_parts, size_t n, uint16_t* out) {
+// bf16 sums of fp32 partials [n_parts, n] in their order, n a multiple of 8: of dx,
+// then of dW, by `blocks` blocks each.
+struct Sum {
+  const float* part;
+  int n_parts, blocks;
+  size_t n;
+  uint16_t* out;
+};
+
+__global__ void __launch_bounds__(256) vocab_sum_kernel(Sum x, Sum w) {
   griddep_launch_dependents();
   griddep_wait();
-  const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
+  const bool of_x = static_cast<int>(blockIdx.x) < x.blocks;
+  const Sum& q = of_x ? x : w;
+  const size_t i = (static_cast<size_t>(of_x ? blockIdx.x : blockIdx.x - x.blocks) * 256 + threadIdx.x) * 8;
+  if (i >= q.n) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-  for (int s = 0; s < n_parts; ++s) {
-    const float4* f = reinterpret_cast<const float4*>(part + static_cast<size_t>(s) * n + i);
-    const float4 x = f[0], y = f[1];
-    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+#pragma unroll 4
+  for (int s = 0; s < q.n_parts; ++s) {
+    const float4* f = reinterpret_cast<const float4*>(q.part + static_cast<size_t>(s) * q.n + i);
+    const float4 u = f[0], v = f[1];
+    a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+    b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
   }
-  *reinterpret_cast<uint4*>(out + i) =
+  *reinterpret_cast<uint4*>(q.out + i) =
       make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
 }
 
@@ -936,8 +941,6 @@ struct Take {
 
 struct BackwardRegions {
   float* row_a;
-  float* row_l;
-  uint16_t* value;
   uint16_t* dz;
   float* dx_part;
   float* dw_part;
@@ -945,9 +948,7 @@ struct BackwardRegions {
 size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const BackwardPlan& b, BackwardRegions* r) {
   Take t{base};
   const size_t rows = static_cast<size_t>(T);
-  r->row_a = t.get<float>(rows);
-  r->row_l = t.get<float>(rows);
-  r->value = t.get<uint16_t>(K == 0 ? rows : 0);
+  r->row_a = t.get<float>(K == 0 ? 0 : rows);
   r->dz = t.get<uint16_t>(rows * b.piece);
   r->dx_part = t.get<float>(b.pieces > 1 || b.splits_x > 1 ? rows * D * b.splits_x : 0);
   r->dw_part = t.get<float>(b.splits_w > 1 ? static_cast<size_t>(V) * D * b.splits_w : 0);
@@ -981,9 +982,8 @@ cudaError_t launch_finish(const VocabForward& a, const VocabArgs& v, const Forwa
                        a.loss, a.lse);
 }
 
-cudaError_t launch_sum(const float* part, int n_parts, size_t n, uint16_t* out, cudaStream_t s) {
-  return launch_kernel(vocab_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0, s, true, part,
-                       n_parts, n, out);
+Sum sum_of(const float* part, int n_parts, size_t n, uint16_t* out) {
+  return Sum{part, n_parts, ceil_div(static_cast<long>(n / 8), 256), n, out};
 }
 
 }  // namespace
@@ -1056,8 +1056,10 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   v.labels = a.targets.ids;
   v.labels64 = a.targets.ids64;
   v.row_a = r.row_a;
-  v.row_l = r.row_l;
-  v.value = r.value;
+  v.lse = a.lse;
+  v.loss = a.loss;
+  v.d_loss = a.d_loss;
+  v.d_lse = a.d_lse;
   const bool dx_direct = b.pieces == 1 && b.splits_x == 1, dw_direct = b.splits_w == 1;
   v.direct[0] = dx_direct;
   v.direct[1] = dw_direct;
@@ -1074,11 +1076,11 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
                 : tensor_map_f32_3d(&mdw, r.dw_part, a.D, a.V, b.splits_w, 32, 32);
   if (e != cudaSuccess) return e;
   const float inv_tau = 1.f / a.temperature;
-  e = K ? launch_kernel(vocab_distill_rows_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
-                        a.d_loss, a.lse, a.targets, a.T, a.V, inv_tau, r.row_a, r.row_l)
-        : launch_kernel(vocab_ce_rows_kernel, dim3(ceil_div(a.T, 256)), dim3(256), 0, s, false, a.d_loss, a.d_lse,
-                        a.loss, a.lse, a.targets, a.T, a.V, r.row_a, r.row_l, r.value);
-  if (e != cudaSuccess) return e;
+  if (K) {
+    e = launch_kernel(vocab_distill_rows_kernel, dim3(ceil_div(a.T, kRowWarps)), dim3(32 * kRowWarps), 0, s, false,
+                      a.d_loss, a.targets, a.T, a.V, inv_tau, r.row_a);
+    if (e != cudaSuccess) return e;
+  }
   for (int i = 0; i < b.pieces; ++i) {
     v.v0 = i * b.piece;
     v.Vc = std::min(b.piece, a.V - v.v0);
@@ -1087,7 +1089,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
     if ((e = tensor_map_block_major(&mz, r.dz, a.T, v.Vcp / 64, v.box, box_blocks(v.box))) != cudaSuccess) return e;
     if ((e = tensor_map_block_major(&mz_out, r.dz, a.T, v.Vcp / 64, 32, 1)) != cudaSuccess) return e;
     v.VocabWork::operator=(dz_work(b, a.D, v.Vc));
-    e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, true);
+    e = launch_vocab<kDz>(std::min(st.pairs[kDz], v.items), mx, mw, mz, mz_out, mz_out, v, s, K != 0 || i > 0);
     if (e != cudaSuccess) return e;
     if (K) {
       auto* k = by_slots(K, vocab_distill_targets_kernel<1>, vocab_distill_targets_kernel<2>,
@@ -1101,12 +1103,10 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
     e = launch_vocab<kGrad>(std::min(st.pairs[kGrad], v.n_units[0] + v.n_units[1]), mx, mw, mz, mdx, mdw, v, s, true);
     if (e != cudaSuccess) return e;
   }
-  if (!dx_direct) {
-    e = launch_sum(r.dx_part, b.splits_x, static_cast<size_t>(a.T) * a.D, a.dx, s);
-    if (e != cudaSuccess) return e;
-  }
-  if (!dw_direct) e = launch_sum(r.dw_part, b.splits_w, static_cast<size_t>(a.V) * a.D, a.dW, s);
-  return e;
+  if (dx_direct && dw_direct) return cudaSuccess;
+  const Sum x = dx_direct ? Sum{} : sum_of(r.dx_part, b.splits_x, static_cast<size_t>(a.T) * a.D, a.dx);
+  const Sum w = dw_direct ? Sum{} : sum_of(r.dw_part, b.splits_w, static_cast<size_t>(a.V) * a.D, a.dW);
+  return launch_kernel(vocab_sum_kernel, dim3(x.blocks + w.blocks), dim3(256), 0, s, true, x, w);
 }
 
 }  // namespace moe

@@ -12,6 +12,7 @@ call the C ABI of libmoeffn.so on the current CUDA stream.  Tensor layouts:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -727,6 +728,7 @@ def embedding_backward(d_out, ids, V, scale=1.0, add=None, workspace=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)  # a size depends on nothing else (1 us a call)
 def embedding_backward_workspace_size(T, V, D) -> int:
     _in_32_bits("moe_embedding_backward_scratch_size", T, V, D)
     n = int(lib.moe_embedding_backward_scratch_size(T, V, D))
@@ -735,6 +737,7 @@ def embedding_backward_workspace_size(T, V, D) -> int:
     return n
 
 
+@functools.lru_cache(maxsize=1024)
 def vocab_workspace_size(T, D, V, n_teacher=0, backward=False) -> int:
     """Bytes of workspace of cross_entropy_* (n_teacher = 0) and distill_*."""
     name = "moe_vocab_backward_workspace_size" if backward else "moe_vocab_forward_workspace_size"
