@@ -670,12 +670,13 @@ __global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_rows_ker
   griddep_wait();
   const int block = static_cast<int>(blockIdx.x) - a.chunk_blocks;
   if (block < 0) {
-    sum_chunk<VEC, kF32>(a, blockIdx.x * kSumWarps + (threadIdx.x >> 5));
+    if (blockIdx.y == 0) sum_chunk<VEC, kF32>(a, blockIdx.x * kSumWarps + (threadIdx.x >> 5));
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int p0 = (block * kSumWarps + warp) * kWindow;
-  const int nv = a.D / VEC;
+  const int nv = a.D / VEC, turns = (nv + 32 * kVecs - 1) / (32 * kVecs);
+  const int turn0 = turns * blockIdx.y / gridDim.y, turn1 = turns * (blockIdx.y + 1) / gridDim.y;
   const uint32_t none = static_cast<uint32_t>(a.V);  // tokens without a row, sorted to the end, and what lies past it
   const int at = p0 - 1 + lane;                      // lane 0 sees the token before the window
   const uint32_t k = at < 0 ? 0xffffffffu : at < a.T ? a.key[at] : none;
@@ -694,7 +695,8 @@ __global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_rows_ker
     const uint32_t rows = __ballot_sync(0xffffffffu, lane >= 1 && lane <= kWindow && k < none) >> 1;
     const int stop = is_long ? 31 - __clz(begins) : 32 - __clz(rows);
 #pragma unroll 1
-    for (int v0 = lane; v0 - lane < nv; v0 += 32 * kVecs) {
+    for (int turn = turn0; turn < turn1; ++turn) {
+      const int v0 = turn * 32 * kVecs + lane;
       float acc[kVecs][VEC] = {};
 #pragma unroll 1
       for (int b = 0; b < stop; b += R) {
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_rows_ker
       }
     }
   }
-  if (is_long) {
+  if (is_long && !(a.chunks && blockIdx.y > 0)) {
     const int end = end_of(a.key, p0 + kWindow, a.T, last);
     const int2 run = make_int2(p0 + 31 - __clz(begins), end);
     // (any order will do: each run is added by itself)
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, kSumBlocks) embedding_rows_ker
   for (int w = 0; w < kSumWarps; ++w)
     if (runs[w].x >= 0)
 #pragma unroll 1
-      for (int turn = 0; turn * 32 * kVecs < nv; ++turn) add_long_run<VEC, kF32>(a, runs[w].x, runs[w].y, turn, red);
+      for (int turn = turn0; turn < turn1; ++turn) add_long_run<VEC, kF32>(a, runs[w].x, runs[w].y, turn, red);
 }
 
 // fp32 rows are read 32 bytes at a time.
@@ -745,10 +747,13 @@ template <int VEC, bool kF32>
 cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
   const int turns = (a.D + Shape<VEC, kF32>::kColumns - 1) / Shape<VEC, kF32>::kColumns;
   a.chunk_blocks = (a.chunks * turns + kSumWarps - 1) / kSumWarps;
-  const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(a.window_blocks + a.chunk_blocks),
+  const int fit = kSumBlocks * std::max(current_device_sms(), 1);
+  // few tokens: a window's columns are shared among blocks (562 x 3346 into 371 rows: 22
+  // us a call, with one block a window 51; 8000 x 1025 into 20000: 43 and 50)
+  const int share = std::min(turns, (fit + a.window_blocks - 1) / a.window_blocks);
+  const cudaError_t e = launch_kernel(embedding_rows_kernel<VEC, kF32>, dim3(a.window_blocks + a.chunk_blocks, share),
                                       dim3(32 * kSumWarps), 0, s, true, a);
   if (e != cudaSuccess || !a.chunks) return e;
-  const int fit = kSumBlocks * std::max(current_device_sms(), 1);
   return launch_kernel(embedding_long_kernel<VEC, kF32>, dim3(fit), dim3(32 * kSumWarps), 0, s, true, a, turns);
 }
 

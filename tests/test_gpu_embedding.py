@@ -107,6 +107,16 @@ def test_long_runs_of_odd_rows(moe, T, V):
                     torch.randn(V, D, generator=g, device="cuda").bfloat16())
 
 
+@pytest.mark.parametrize("T,V,D", [(1, 2, 4097), (40, 2, 8192), (562, 3, 3346), (2048, 9, 2056), (2049, 1, 8191), (3000, 5, 2056)])
+@pytest.mark.parametrize("grad_type,with_add", [(BF, True), (F32, False)])
+def test_few_tokens_of_wide_rows(moe, T, V, D, grad_type, with_add):
+    """A row's columns are shared among blocks, those of long runs too."""
+    g = _gen(T)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    add = torch.randn(V, D, generator=g, device="cuda").bfloat16() if with_add else None
+    _check_backward(moe, ids, torch.randn(T, D, generator=g, device="cuda").to(grad_type), V, 0.7, add)
+
+
 def test_calls_from_several_host_threads(moe):
     from concurrent.futures import ThreadPoolExecutor
     g = _gen(10)
