@@ -230,6 +230,17 @@ def test_distillation(moe, T, D, V, K, tau, lt, index):
         assert not got["dx"][1].any() and not got["dx"][2].any()
 
 
+@pytest.mark.parametrize("T,V,K", [(300, 20000, 251), (40, 30001, 256), (520, 5003, 100), (33, 9000, 38)])
+def test_logits_of_many_entries(moe, T, V, K):
+    """Every run of the vocabulary finds where a row's entries begin in it."""
+    D = 64
+    g, x, W, _ = _inputs(T, D, V)
+    ids = torch.rand(T, V, generator=g, device="cuda").argsort(dim=1)[:, :K].contiguous()
+    f = moe.distill_forward(x, W, ids, torch.randn(T, K, generator=g, device="cuda"))
+    z = (x.double() @ W.double().t()).gather(1, ids)
+    _close(f["logits"], _np(z), 2.0 ** -20 * _size(x, W), f"logits of {K}")
+
+
 def test_teacher_ids_side_by_side(moe):
     """All entries in neighbouring columns, at the edges of tiles, halves and boxes."""
     T, D, V, K = 200, 64, 1200, 64
