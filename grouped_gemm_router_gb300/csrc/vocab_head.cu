@@ -690,9 +690,10 @@ MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, fl
 // where c z - m is one fused product: for a target that outweighs the rest both
 // terms are next to 0, and the difference of the rounded lse and z, which would
 // be off by 2^-24 of their size, is never formed.
-// kWarps: 32 while all blocks fit the device at once (a call of 3149 x 896 x 11454:
-// 44.0 us, with 8 warps 45.4; of 2048 x 768 x 32768 with 8 entries 68.5 and 77.7),
-// 8 where they come in rounds (32768 rows: 12 us of a call, with 32 warps 25).
+// kWarps: 32 below 4096 rows, where few blocks have many pairs (a call of 219 x 576 x
+// 143711: 43.5 us, with 16 warps 45.1), 8 from 12288 rows on, where more warps only wait
+// for one another (32768 x 64 x 512 with 64 entries: 82, with 16 84, with 32 91), 16
+// between (7048 x 192 x 449 with 141 entries: 46, with 8 54, with 32 48).
 template <int kSlots, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
     vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   got[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if constexpr (kSlots == 0 && kWarps <= 8) {
+  if constexpr (kSlots == 0 && kWarps <= 16) {
     // a lane a row, in the order of the shuffles below, so that a teacher of one
     // entry gets a label's bits
     const int row = row0 + lane;
@@ -984,8 +985,6 @@ Kernel by_slots(int K, Kernel k1, Kernel k2, Kernel k4, Kernel k8) {
   return K <= 32 ? k1 : K <= 64 ? k2 : K <= 128 ? k4 : k8;
 }
 
-constexpr int kManyRows = 4096;
-
 template <int kWarps>
 cudaError_t launch_finish(const VocabForward& a, const VocabArgs& v, const ForwardPlan& f, float inv_tau, cudaStream_t s) {
   auto* k = v.K == 0 ? vocab_finish_kernel<0, kWarps>
@@ -1045,7 +1044,9 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   }
   e = launch_vocab<kStats>(std::min(st.pairs[kStats], v.items), mx, mw, mx, mx, mx, v, s, v.K != 0);
   if (e != cudaSuccess) return e;
-  return a.T < kManyRows ? launch_finish<32>(a, v, f, inv_tau, s) : launch_finish<8>(a, v, f, inv_tau, s);
+  return a.T < 4096    ? launch_finish<32>(a, v, f, inv_tau, s)
+         : a.T < 12288 ? launch_finish<16>(a, v, f, inv_tau, s)
+                       : launch_finish<8>(a, v, f, inv_tau, s);
 }
 
 size_t vocab_backward_workspace_bytes(int T, int D, int V, int K) {
