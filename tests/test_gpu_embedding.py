@@ -207,3 +207,32 @@ def test_captured_and_on_streams(moe):
             out.append([moe.embedding_backward(d, i, V) for _ in range(4)])
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for os, w in zip(out, want) for o in os)
+
+
+@pytest.mark.parametrize("T,D", [(5000, 768), (70000, 40)])
+def test_long_runs_in_a_captured_graph(moe, T, D):
+    """Replays find other long runs, many, few or none, in whatever order, and
+    give the bits of a call of its own."""
+    g = _gen(12)
+    V = 4000
+    skew = [(torch.rand(T, generator=g, device="cuda") ** p * V).long() for p in (6, 1.5)]
+    sets = [skew[0], torch.arange(T, device="cuda") % V, torch.full((T,), 7, device="cuda"), skew[1],
+            torch.full((T,), -1, device="cuda"), skew[0].flip(0).contiguous()]
+    d_out = torch.randn(T, D, generator=g, device="cuda").bfloat16()
+    want = [moe.embedding_backward(d_out, i, V) for i in sets]
+    for i, w in zip(sets, want):
+        assert all(torch.equal(moe.embedding_backward(d_out, i, V), w) for _ in range(3))
+    ids = sets[0].clone()
+    ws = torch.full((moe.embedding_backward_workspace_size(T, V, D),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        moe.embedding_backward(d_out, ids, V, workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = moe.embedding_backward(d_out, ids, V, workspace=ws)
+        for i, w in list(zip(sets, want)) * 2:
+            ids.copy_(i)
+            graph.replay()
+            s.synchronize()
+            assert torch.equal(got, w)
