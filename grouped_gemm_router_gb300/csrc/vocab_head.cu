@@ -599,7 +599,7 @@ MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, 
       const float l = teacher_logit(t, at);
       if (id >= 0 && id < V) {
         out.id[i] = static_cast<int>(id);
-        out.p[i] = l * inv_tau;
+        out.p[i] = l;
       }
     }
     top = fmaxf(top, out.p[i]);
@@ -609,7 +609,9 @@ MOE_DEV void read_teacher(const VocabTargets& t, int row, int V, float inv_tau, 
   float total = 0.f;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
-    out.log_p[i] = out.p[i] - ref;
+    // (the difference first, and of halves: neither it nor a logit over the
+    // temperature need lie in fp32's range)
+    out.log_p[i] = (0.5f * out.p[i] - 0.5f * ref) * (2.f * inv_tau);
     out.p[i] = expf(out.log_p[i]);
     total += out.p[i];
   }
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     const int j = min(j0 + lane, t.K - 1);
     const size_t at = static_cast<size_t>(row) * t.K + j;
     const long long id = load_index(t.ids, t.ids64, at);
-    any = __any_sync(0xffffffffu, id >= 0 && id < V && !(teacher_logit(t, at) * inv_tau == -INFINITY));
+    any = __any_sync(0xffffffffu, id >= 0 && id < V && teacher_logit(t, at) != -INFINITY);
   }
   if (lane == 0) row_a[row] = any ? d_loss[row] * inv_tau : 0.f;
 }
