@@ -6,10 +6,11 @@
 // Forward: with c = log2(e) / temperature, every token needs
 //   lse = ln 2 * log2 sum_v 2^(c z_v)
 // and z at its targets.  vocab_kernel<kStats> computes 256 x 256 tiles of z on
-// CTA pairs (tcgen05.mma.cta_group::2, fp32 in TMEM); its epilogue keeps the
-// running maximum and sum of a row in registers over a run of tiles, picks the
-// targets that lie in the tile, and writes one (maximum, sum) pair a row and
-// run.  vocab_finish_kernel joins them and writes lse and the loss.
+// CTA pairs (tcgen05.mma.cta_group::2, fp32 in TMEM, long sums in parts: parts_of
+// below); its epilogue keeps the running maximum and sum of a row in registers over
+// a run of tiles, picks the targets that lie in the tile, and writes one (maximum,
+// sum) pair a row and run.  vocab_finish_kernel joins them and writes lse and the
+// loss.
 //
 // Backward, by pieces of the vocabulary:
 //   dz_v = a 2^(c z_v - lse / ln 2)  (+ the targets' own terms)
@@ -61,6 +62,7 @@ constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kBoxBytes + 1024;
 struct VocabArgs : VocabWork {
   int T, V, D;
   int box;                 // rows of a box of tokens
+  int parts;               // sums that a logit is made of
   int v0, Vc, Vcp;         // kDz, kGrad: the piece's first row, its rows, and those rounded up to 64
   float c;
   unsigned int* dev_err;
@@ -96,6 +98,14 @@ MOE_DEV float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 8 columns of a warp's TMEM lanes, as tmem_ld_32cols.
+MOE_DEV void tmem_ld_8cols(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 
 MOE_DEV long long load_index(const void* p, int is64, size_t i) {
@@ -205,7 +215,8 @@ MOE_DEV void put_row(uint8_t* mine, const uint32_t (&w)[32]) {
     *reinterpret_cast<uint4*>(mine + ((c ^ turn) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 
-template <int kMode>
+// kParts: a logit is the sum of p.parts sums over D.
+template <int kMode, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
                  const __grid_constant__ CUtensorMap mapZ, const __grid_constant__ CUtensorMap mapOut0,
@@ -322,16 +333,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int i = 0;
       bool ok = true;
-      for (; ok && walk.next(p, pair, npairs, u); ++i) {
+      const int parts = kParts ? p.parts : 1;
+      for (int part = parts; ok; ++i) {
+        if (part == parts) {
+          if (!walk.next(p, pair, npairs, u)) break;
+          part = 0;
+        }
         const int buf = i & 1;
         if (!mbar_wait_cluster(smem_u32(&ctl.tempty[buf]), ((i >> 1) & 1) ^ 1u, abort_flag, dev_err)) break;
         tc_fence_after_sync();
+        const int first = kParts ? u.kb1 * part / parts : u.kb0;
+        const int end = kParts ? u.kb1 * (part + 1) / parts : u.kb1;
+        ++part;
         const uint32_t d_tmem = tmem_base + buf * 256;
         // kGrad: B is N-major, A M-major where the tokens are the reduction
         const uint32_t a_mn = kMode == kGrad && u.which == 1, b_mn = kMode == kGrad;
         const uint32_t idesc = idesc_bf16_f32_ab(kTile, kTile, a_mn, b_mn);
         const uint32_t a_lbo = a_mn ? 16384 : 16;
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+        for (int kb = first; kb < end; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&ctl.full[stage]), phase, abort_flag, dev_err)) {
             ok = false;
             break;
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t k_major = (kk >> 2) * 16384 + (kk & 3) * 32, mn_major = kk * 2048;
             const uint64_t adesc = smem_desc_sw128(sa + (a_mn ? mn_major : k_major), a_lbo, 1024);
             const uint64_t bdesc = smem_desc_sw128(sb + (b_mn ? mn_major : k_major), b_mn ? 16384 : 16, 1024);
-            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kb != u.kb0 || kk != 0) ? 1u : 0u);
+            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kb != first || kk != 0) ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&ctl.empty[stage]), 0x3);
           if (++stage == kStages) {
@@ -376,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float run_max = -INFINITY, run_sum = 0.f;
     Targets tg;
     float row_a = 0.f, row_l = 0.f;
-    for (int i = 0; walk.next(p, pair, npairs, u); ++i) {
-      const int buf = i & 1;
+    int i = 0;  // sums taken out of TMEM
+    while (walk.next(p, pair, npairs, u)) {
       const int warp_row0 = u.m * kTile + 128 * rank + q * 32;
       const int row = warp_row0 + lane;
       const int col0 = u.n * kTile + c_first;  // first column of this warp (of the piece, in kDz)
@@ -392,17 +411,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[buf]), (i >> 1) & 1, abort_flag, dev_err);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after_sync();
       uint32_t acc[kBoxes][32];
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + c_first;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c_first;
+      auto filled = [&] {
+        const bool got = mbar_wait_cluster(smem_u32(&ctl.tfull[i & 1]), (i >> 1) & 1, abort_flag, dev_err);
+        const bool all = __all_sync(0xffffffffu, got);
+        tc_fence_after_sync();
+        return all;
+      };
+      auto hand_back = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(i & 1 ? tempty_leader1 : tempty_leader0);
+        ++i;
+      };
+      bool ok = filled();
+      if (!ok) break;
 #pragma unroll
-      for (int b = 0; b < kBoxes; ++b) tmem_ld_32cols(taddr + b * 32, acc[b]);
+      for (int b = 0; b < kBoxes; ++b) tmem_ld_32cols(taddr + (i & 1) * 256 + b * 32, acc[b]);
       tmem_ld_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
+      hand_back();
+      if constexpr (kParts) {
+        // (8 columns at a time: 16 do not fit beside the 128 in registers)
+#pragma unroll 1
+        for (int part = 1; part < p.parts; ++part) {
+          if (!(ok = filled())) break;
+#pragma unroll
+          for (int g = 0; g < 16; ++g) {
+            uint32_t more[8];
+            tmem_ld_8cols(taddr + (i & 1) * 256 + g * 8, more);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t& to = acc[g / 4][g % 4 * 8 + j];
+              to = __float_as_uint(__uint_as_float(to) + __uint_as_float(more[j]));
+            }
+          }
+          hand_back();
+        }
+        if (!ok) break;
+      }
 
       if constexpr (kMode == kStats) {
         if (col0 + 128 > p.V) {  // columns past the vocabulary
@@ -685,8 +733,7 @@ MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, fl
     if (i + j * kWarps < parts) join(m, s, v[j].x, v[j].y);
 }
 
-// Joins a row's (maximum, sum) pairs and writes lse, the loss and a teacher's logits
-// (which are `fix` times what the product gave): 32 rows a
+// Joins a row's (maximum, sum) pairs and writes lse and the loss: 32 rows a
 // block, the pairs dealt to its warps, then the rows.  With the sum s relative
 // to 2^m,
 //   lse - z / temperature = ln 2 (log2 s - (c z - m)),
@@ -699,8 +746,8 @@ MOE_DEV void join_pairs(const float2* row, int i, int parts, int rows_padded, fl
 // between (7048 x 192 x 449 with 141 entries: 46, with 8 54, with 32 48).
 template <int kSlots, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
-    vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, float* target, int T, int V,
-                        float c, float inv_tau, float fix, float* loss, float* lse) {
+    vocab_finish_kernel(const float2* part, int parts, int rows_padded, VocabTargets t, const float* target, int T, int V,
+                        float c, float inv_tau, float* loss, float* lse) {
   __shared__ float2 got[kWarps][33];
   griddep_launch_dependents();
   griddep_wait();
@@ -761,11 +808,8 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
           const int j = lane + 32 * i;
-          if (j >= t.K) continue;
-          float* z = target + static_cast<size_t>(row) * t.K + j;
-          const float cut = *z;
-          if (te.id[i] >= 0 && te.p[i] != 0.f) sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(cut, c, -m)) * kLn2);
-          *z = cut * fix;
+          if (j < t.K && te.id[i] >= 0 && te.p[i] != 0.f)
+            sum += te.p[i] * (te.log_p[i] + (log_s - fmaf(target[static_cast<size_t>(row) * t.K + j], c, -m)) * kLn2);
         }
         sum = warp_sum(sum);
         if (lane == 0) loss[row] = sum;
@@ -881,18 +925,20 @@ __global__ void __launch_bounds__(256) vocab_sum_kernel(Sum x, Sum w) {
 // ---------------------------------------------------------------------------
 std::mutex g_mu;
 struct Setup {
-  int pairs[3] = {0, 0, 0};  // co-resident CTA pairs of each mode
+  int pairs[3] = {0, 0, 0};  // co-resident CTA pairs of each mode, with parts or without
   unsigned int* dev_err = nullptr;
 };
 Setup g_setup[64];
 
-const void* kernel_of(int mode) {
-  return mode == kStats ? reinterpret_cast<const void*>(vocab_kernel<kStats>)
-         : mode == kDz  ? reinterpret_cast<const void*>(vocab_kernel<kDz>)
-                        : reinterpret_cast<const void*>(vocab_kernel<kGrad>);
+const void* kernel_of(int mode, bool parts) {
+  return mode == kStats ? parts ? reinterpret_cast<const void*>(vocab_kernel<kStats, true>)
+                                : reinterpret_cast<const void*>(vocab_kernel<kStats, false>)
+         : mode == kDz  ? parts ? reinterpret_cast<const void*>(vocab_kernel<kDz, true>)
+                                : reinterpret_cast<const void*>(vocab_kernel<kDz, false>)
+                        : reinterpret_cast<const void*>(vocab_kernel<kGrad, false>);
 }
 
-cudaLaunchConfig_t pair_config(int mode, int pairs, cudaStream_t s, cudaLaunchAttribute (&attr)[2], bool pdl) {
+cudaLaunchConfig_t pair_config(int pairs, cudaStream_t s, cudaLaunchAttribute (&attr)[2], bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -921,14 +967,18 @@ cudaError_t setup(Setup* out) {
     const int sms = current_device_sms();
     if (sms < 2) return cudaErrorInvalidDevice;
     if ((e = device_error_address(&got.dev_err)) != cudaSuccess) return e;
-    for (int mode = 0; mode < 3; ++mode) {
-      e = cudaFuncSetAttribute(kernel_of(mode), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    for (int i = 0; i < 6; ++i) {
+      const int mode = i / 2;
+      const void* kernel = kernel_of(mode, i % 2 != 0);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e != cudaSuccess) return e;
       cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = pair_config(mode, sms / 2, nullptr, attr, false);
-      e = cudaOccupancyMaxActiveClusters(&got.pairs[mode], kernel_of(mode), &cfg);
+      cudaLaunchConfig_t cfg = pair_config(sms / 2, nullptr, attr, false);
+      int fit = 0;
+      e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
       if (e != cudaSuccess) return e;
-      if (got.pairs[mode] < 1) return cudaErrorInvalidConfiguration;
+      if (fit < 1) return cudaErrorInvalidConfiguration;
+      got.pairs[mode] = i % 2 ? std::min(got.pairs[mode], fit) : fit;
     }
     st = got;
   }
@@ -940,8 +990,11 @@ template <int kMode>
 cudaError_t launch_vocab(int pairs, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& z,
                          const CUtensorMap& out0, const CUtensorMap& out1, const VocabArgs& a, cudaStream_t s, bool pdl) {
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pair_config(kMode, pairs, s, attr, pdl);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_kernel<kMode>, x, w, z, out0, out1, a);
+  cudaLaunchConfig_t cfg = pair_config(pairs, s, attr, pdl);
+  auto* k = vocab_kernel<kMode, false>;
+  if constexpr (kMode != kGrad)
+    if (a.parts > 1) k = vocab_kernel<kMode, true>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, x, w, z, out0, out1, a);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -976,14 +1029,19 @@ size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const Backwar
   return t.off;
 }
 
-// What a product of D terms is multiplied by.  The tensor cores cut each sum of 16
-// products and what came before to 24 bits, where fp32 arithmetic rounds it: half a
-// unit of the last place is lost on average, 2^-24.5 of a partial sum that is on
-// average half of the last one, D / 16 times: 1.3e-9 D.  Measured: 0.9e-9 to 1.1e-9 D
-// for random and for aligned rows, D 256 to 8192.  With 2^-30 D put back, lse is off
-// by 4e-8 to 1.1e-7 of itself up to D 4096 (rows as of a trained model), without by
-// 1e-7 to 1.6e-6.
-double uncut(int D) { return 1.0 + D * 0x1p-30; }
+// Sums that a logit is made of.  The tensor cores add 16 products at a time to the
+// sum so far and cut the result to 24 bits, towards zero, where fp32 arithmetic
+// rounds it: a sum of n products of random sign comes out about 1e-9 n of itself too
+// small, of products of one sign up to three times that (2.4e-5 at 8192).  So at most
+// kPartBlocks k blocks, 896 products, are summed there, and the parts are added in
+// fp32: a logit is off by less than 1e-6 of the size of its sums (one sign: 2e-6 of
+// itself) at any width.
+// (8192 x 1024 x 50001 in two parts: 490 us, in one 460; 8192 x 4096 x 30001 in five
+// 1145, in one 1125; 4096 x 4096 x 30001 backward 1787 and 1770.  Parts of at most 512
+// products have half the error, but take 1490 us instead of 1390 for 32768 x 768 x
+// 50001; parts of 1024 save nothing but at 1024, and there a logit is 1e-6 off.)
+constexpr int kPartBlocks = 7;
+int parts_of(int D) { return ceil_div(ceil_div(D, kBK), kPartBlocks); }
 
 // Rows of a box of tokens: 128, with two blocks of columns, or as many as there
 // are (in slices of 16 of a reduction over them), with one.  TMA fills what lies
@@ -1006,8 +1064,8 @@ cudaError_t launch_finish(const VocabForward& a, const VocabArgs& v, const Forwa
                      : by_slots(v.K, vocab_finish_kernel<1, kWarps>, vocab_finish_kernel<2, kWarps>,
                                 vocab_finish_kernel<4, kWarps>, vocab_finish_kernel<8, kWarps>);
   return launch_kernel(k, dim3(ceil_div(a.T, 32)), dim3(32 * kWarps), 0, s, true, static_cast<const float2*>(v.part),
-                       2 * f.runs, f.rows_padded, a.targets, v.target, a.T, a.V, v.c, inv_tau,
-                       static_cast<float>(uncut(a.D)), a.loss, a.lse);
+                       2 * f.runs, f.rows_padded, a.targets, static_cast<const float*>(v.target), a.T, a.V, v.c, inv_tau,
+                       a.loss, a.lse);
 }
 
 Sum sum_of(const float* part, int n_parts, size_t n, uint16_t* out) {
@@ -1036,7 +1094,8 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* workspace, cudaStr
   v.V = v.Vc = v.Vcp = a.V;
   v.D = a.D;
   v.VocabWork::operator=(forward_work(f, a.D));
-  v.c = static_cast<float>(static_cast<double>(kLog2e) * uncut(a.D) / a.temperature);
+  v.c = kLog2e / a.temperature;
+  v.parts = parts_of(a.D);
   v.K = a.targets.K;
   v.labels = a.targets.ids;
   v.labels64 = a.targets.ids64;
@@ -1081,7 +1140,8 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* workspace, cudaS
   v.T = a.T;
   v.D = a.D;
   v.V = a.V;
-  v.c = static_cast<float>(static_cast<double>(kLog2e) * uncut(a.D) / a.temperature);
+  v.c = kLog2e / a.temperature;
+  v.parts = parts_of(a.D);
   v.K = K;
   v.labels = a.targets.ids;
   v.labels64 = a.targets.ids64;
