@@ -1032,7 +1032,7 @@ size_t backward_regions(uint8_t* base, int T, int D, int V, int K, const Backwar
 // Sums that a logit is made of.  The tensor cores add 16 products at a time to the
 // sum so far and cut the result to 24 bits, towards zero, where fp32 arithmetic
 // rounds it: a sum of n products of random sign comes out about 1e-9 n of itself too
-// small, of products of one sign up to three times that (2.4e-5 at 8192).  So at most
+// small, of products of one sign two to four times that (3.2e-5 at 8192).  So at most
 // kPartBlocks k blocks, 896 products, are summed there, and the parts are added in
 // fp32: a logit is off by less than 1e-6 of the size of its sums (one sign: 2e-6 of
 // itself) at any width.
