@@ -572,32 +572,23 @@ MOE_DEV int end_of(const uint32_t* key, int lo, int T, uint32_t k) {
   return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && key[lo + lane] <= k));
 }
 
-// The row's only addition to what it was filled with: nothing to wait for, and
-// no order that could change the result.
-template <int VEC>
-MOE_DEV void add_vec(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v[0]) : "memory");
-  } else {
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4)
-      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + k), "f"(v[k]), "f"(v[k + 1]), "f"(v[k + 2]),
-                   "f"(v[k + 3])
-                   : "memory");
-  }
-}
-
+// (`add` is read again, not added to what the row was filled with by an atomic of
+// the memory: that takes subnormal numbers for zeros.)
 template <int VEC, int kVecs>
 MOE_DEV void write_row(const SumArgs& a, uint32_t v, int v0, int nv, const float (&acc)[kVecs][VEC]) {
-  float* dst = a.d_table + static_cast<size_t>(v) * a.D;
+  const size_t row = static_cast<size_t>(v) * a.D;
+  Piece<VEC, false> with[kVecs] = {};
+  if (a.add) load_row(a.add, v, a.D, v0, nv, with);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
     if (v0 + 32 * i < nv) {
       float o[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) o[e] = a.scale * acc[i][e];
-      if (a.add) add_vec<VEC>(dst + (v0 + 32 * i) * VEC, o);
-      else store_vec<VEC, true>(dst, static_cast<size_t>(v0 + 32 * i) * VEC, o);
+      for (int e = 0; e < VEC; ++e) {
+        o[e] = a.scale * acc[i][e];
+        if (a.add) o[e] = __fadd_rn(with[i][e], o[e]);
+      }
+      store_vec<VEC, true>(a.d_table, row + static_cast<size_t>(v0 + 32 * i) * VEC, o);
     }
 }
 
@@ -634,9 +625,9 @@ MOE_DEV void add_long_run(const SumArgs& a, int start, int end, int turn,
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kSumWarps; ++i) sum += red[i][c];
-    const float o[1] = {a.scale * sum};
-    if (a.add) add_vec<1>(a.d_table + dst + column, o);
-    else a.d_table[dst + column] = o[0];
+    Piece<1, false> with = {};
+    if (a.add) with.load(a.add, dst + column);
+    a.d_table[dst + column] = a.add ? __fadd_rn(with[0], a.scale * sum) : a.scale * sum;
   }
   __syncthreads();
 }
