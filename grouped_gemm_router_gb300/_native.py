@@ -117,6 +117,7 @@ _SIGNATURES = {
                                     _vp, _sz, _vp]),
     "moe_permute_noalloc": (_i32, [_vp, MoeDims, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_device_error": (_i32, []),
+    "moe_selftest_embedding_by_passes": (_i32, [_vp, _i32, _vp, _i32, _f32, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
     "moe_selftest_wait_timeout": (_i32, [_i32, _vp, _vp]),
     "moe_launch_count": (ctypes.c_uint64, []),
     "moe_status_str": (ctypes.c_char_p, [_i32]),

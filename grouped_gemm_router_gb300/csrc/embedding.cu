@@ -136,23 +136,26 @@ constexpr int kHeld = 8;  // rounds of 32 tokens that a warp keeps in registers
 constexpr int kMaxCluster = 16;        // most blocks that sort a short list together
 constexpr int kShortBlock = kSortThreads * kHeld;
 constexpr int kShortList = kMaxCluster * kShortBlock;  // (its positions fit in 16 bits)
+constexpr int kPortable = 4096;  // longest list of a cluster that every device holds
 
 struct SortPlan {
   int passes, bits;       // of a pass
   int block, blocks;      // tokens of a block
-  int cluster;            // blocks of a short list's cluster
+  int cluster;            // blocks of a short list's cluster, 0 for a launch a pass
   int chunk, chunks;      // aligned runs of sorted tokens
 };
 
-SortPlan sort_plan(int T, int V) {
+// large_clusters: whether the device holds a cluster of kMaxCluster, more than the
+// portable 8.  Without, lists past kPortable take a launch a pass.
+SortPlan sort_plan(int T, int V, bool large_clusters) {
   SortPlan p = {};
   int b = 1;
   while ((V >> b) != 0) ++b;  // the keys are 0 .. V (V: no row)
   p.passes = (b + 8) / 9;
   p.bits = (b + p.passes - 1) / p.passes;
-  if (T <= kShortList) {
+  if (T <= (large_clusters ? kShortList : kPortable)) {
     // (8000 tokens: 16 blocks 28.7 us a call, 8 29.5, 4 32.3; 32768: 16 75, 8 84)
-    p.cluster = T <= 512 ? 1 : T <= 4096 ? 4 : kMaxCluster;
+    p.cluster = T <= 512 ? 1 : T <= kPortable ? 4 : kMaxCluster;
     p.block = kSortThreads;
     while (p.block * p.cluster < T) p.block *= 2;
   } else {
@@ -749,35 +752,49 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
 }
 
 std::mutex g_mu;
-bool g_large_clusters[64];
+int g_large_clusters[64];  // of a device: 0 not asked yet, 1 held, -1 not held
 
-// Clusters of 16 have to be asked for, once on each device.
-cudaError_t allow_large_clusters() {
+// Clusters of 16 have to be allowed and found to fit, once on each device.
+cudaError_t large_clusters(bool* held) {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_mu);
-  if (!g_large_clusters[dev]) {
-    e = cudaFuncSetAttribute(embedding_sort_short_kernel<kMaxCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    g_large_clusters[dev] = e == cudaSuccess;
+  int& known = g_large_clusters[dev];
+  if (known == 0) {
+    auto* k = embedding_sort_short_kernel<kMaxCluster>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    const bool ok = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&fit, k, &cfg) == cudaSuccess && fit > 0;
+    if (!ok) cudaGetLastError();  // a refusal is an answer, not this call's error
+    known = ok ? 1 : -1;
   }
-  return e;
+  *held = known == 1;
+  return cudaSuccess;
 }
 
 cudaError_t launch_sort_short(const SortArgs& q, int cluster, cudaStream_t s) {
-  if (cluster == kMaxCluster) {
-    const cudaError_t e = allow_large_clusters();
-    if (e != cudaSuccess) return e;
-  }
   auto* k = cluster == 1   ? embedding_sort_short_kernel<1>
             : cluster == 4 ? embedding_sort_short_kernel<4>
                            : embedding_sort_short_kernel<kMaxCluster>;
   return launch_kernel(k, dim3(cluster), dim3(kSortThreads), 0, s, false, q);
 }
 
-size_t hist_bytes(int T, const SortPlan& p) {
-  return T <= kShortList ? 0 : static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits);
+// (a list that a cluster of 16 may sort has room for the other way too: the size
+// depends on no device)
+size_t hist_bytes(int T, int V) {
+  const SortPlan p = sort_plan(T, V, false);
+  return p.cluster ? 0 : static_cast<size_t>(p.passes) * p.blocks * (sizeof(uint32_t) << p.bits);
 }
 
 int window_blocks(int T) { return (T + kSumWarps * kWindow - 1) / (kSumWarps * kWindow); }
@@ -792,14 +809,17 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t s) {
 }
 
 size_t embedding_bwd_scratch_bytes(int T, int V, int D) {
-  const SortPlan p = sort_plan(T, V);
-  return padded(hist_bytes(T, p)) +
+  const SortPlan p = sort_plan(T, V, true);
+  return padded(hist_bytes(T, V)) +
          4 * padded(static_cast<size_t>(T) * sizeof(uint32_t)) + padded(static_cast<size_t>(p.chunks) * D * sizeof(float)) +
          padded(sizeof(uint32_t)) + padded(p.chunks ? most_long(T) * sizeof(int2) : 0);
 }
 
 cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaStream_t s) {
-  const SortPlan p = sort_plan(a.T, a.V);
+  cudaError_t e = cudaSuccess;
+  bool large = false;
+  if (a.T > kPortable && a.T <= kShortList && !a.by_passes && (e = large_clusters(&large)) != cudaSuccess) return e;
+  const SortPlan p = sort_plan(a.T, a.V, large);
   uint8_t* at = static_cast<uint8_t*>(scratch);
   auto take = [&](size_t bytes) {
     uint8_t* r = at;
@@ -816,13 +836,12 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   q.bits = p.bits;
   while ((1 << q.log2_block) < p.block) ++q.log2_block;
   q.passes = p.passes;
-  q.hist = reinterpret_cast<uint32_t*>(take(hist_bytes(a.T, p)));
+  q.hist = reinterpret_cast<uint32_t*>(take(hist_bytes(a.T, a.V)));
   for (auto& l : q.lists) l = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(a.T) * sizeof(uint32_t)));
   float* part = reinterpret_cast<float*>(take(static_cast<size_t>(p.chunks) * a.D * sizeof(float)));
   q.n_long = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t)));
   int2* long_runs = reinterpret_cast<int2*>(take(p.chunks ? most_long(a.T) * sizeof(int2) : 0));
-  cudaError_t e = cudaSuccess;
-  if (a.T > 0 && a.T <= kShortList) {
+  if (a.T > 0 && p.cluster) {
     e = launch_sort_short(q, p.cluster, s);
   } else if (a.T > 0) {
     e = launch_kernel(embedding_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, s, false, q);
@@ -840,7 +859,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaS
   e = launch_kernel(embedding_fill_kernel, dim3(static_cast<unsigned>(std::min((n + per - 1) / per, fit))), dim3(kFillThreads),
                     0, s, a.T > 0, a.d_table, static_cast<const uint16_t*>(a.add), n);
   if (e != cudaSuccess || a.T == 0) return e;
-  const int last = a.T <= kShortList ? 0 : (p.passes - 1) & 1;
+  const int last = p.cluster ? 0 : (p.passes - 1) & 1;
   const SumArgs m{a.d_out, a.add, q.lists[2 * last], q.lists[2 * last + 1], part, a.d_table, a.scale, a.T, a.V, a.D, p.chunk, p.chunks,
                   window_blocks(a.T), 0, long_runs, q.n_long};
   if (a.D % 8 == 0 && (!a.d_fp32 || on32(a.d_out))) return a.d_fp32 ? launch_sums<8, true>(m, s) : launch_sums<8, false>(m, s);

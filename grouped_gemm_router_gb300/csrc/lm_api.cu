@@ -62,6 +62,20 @@ moe_status zero_weight_gradient(void* dW, int32_t V, int32_t D, cudaStream_t s) 
   return cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * D * 2, s));
 }
 
+moe_status embedding_backward(const void* d_out, moe_dtype d_type, const void* ids, moe_index_type ids_type,
+                              float scale, const void* add, int32_t T, int32_t V, int32_t D, float* d_table,
+                              void* scratch, size_t scratch_bytes, void* stream, int by_passes) {
+  const moe_status st = check_table(T, V, D);
+  if (st != MOE_OK) return st;
+  if (!known_index(ids_type) || !known_type(d_type) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (!d_table || (T > 0 && !all_there({d_out, ids}))) return MOE_ERR_INVALID_ARG;
+  if (!all_on_16({d_out, ids, add, d_table})) return MOE_ERR_INVALID_ARG;
+  const moe_status ws = check_workspace(scratch, scratch_bytes, embedding_bwd_scratch_bytes(T, V, D));
+  if (ws != MOE_OK) return ws;
+  EmbeddingBwdArgs a{d_out, d_type == MOE_FP32, ids, ids_type == MOE_I64, scale, add, T, V, D, d_table, by_passes};
+  return cuda_status(launch_embedding_bwd(a, scratch, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -89,15 +103,14 @@ size_t moe_embedding_backward_scratch_size(int32_t T, int32_t V, int32_t D) {
 moe_status moe_embedding_backward(const void* d_out, moe_dtype d_type, const void* ids, moe_index_type ids_type,
                                   float scale, const void* add, int32_t T, int32_t V, int32_t D, float* d_table,
                                   void* scratch, size_t scratch_bytes, void* stream) {
-  const moe_status st = check_table(T, V, D);
-  if (st != MOE_OK) return st;
-  if (!known_index(ids_type) || !known_type(d_type) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
-  if (!d_table || (T > 0 && !all_there({d_out, ids}))) return MOE_ERR_INVALID_ARG;
-  if (!all_on_16({d_out, ids, add, d_table})) return MOE_ERR_INVALID_ARG;
-  const moe_status ws = check_workspace(scratch, scratch_bytes, embedding_bwd_scratch_bytes(T, V, D));
-  if (ws != MOE_OK) return ws;
-  EmbeddingBwdArgs a{d_out, d_type == MOE_FP32, ids, ids_type == MOE_I64, scale, add, T, V, D, d_table};
-  return cuda_status(launch_embedding_bwd(a, scratch, static_cast<cudaStream_t>(stream)));
+  return embedding_backward(d_out, d_type, ids, ids_type, scale, add, T, V, D, d_table, scratch, scratch_bytes, stream, 0);
+}
+
+moe_status moe_selftest_embedding_by_passes(const void* d_out, moe_dtype d_type, const void* ids,
+                                            moe_index_type ids_type, float scale, const void* add, int32_t T, int32_t V,
+                                            int32_t D, float* d_table, void* scratch, size_t scratch_bytes,
+                                            void* stream) {
+  return embedding_backward(d_out, d_type, ids, ids_type, scale, add, T, V, D, d_table, scratch, scratch_bytes, stream, 1);
 }
 
 size_t moe_vocab_forward_workspace_size(int32_t T, int32_t D, int32_t V, int32_t n_teacher) {

@@ -224,6 +224,7 @@ struct EmbeddingBwdArgs {
   const void* add;    // [V, D] bf16 or nullptr
   int T, V, D;
   float* d_table;     // [V, D]
+  int by_passes;      // sort as on a device that holds no cluster of 16
 };
 size_t embedding_bwd_scratch_bytes(int T, int V, int D);
 cudaError_t launch_embedding_bwd(const EmbeddingBwdArgs& a, void* scratch, cudaStream_t s);

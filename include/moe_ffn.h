@@ -490,6 +490,14 @@ moe_status moe_device_error(void);
  * usable: nothing faults and nothing is left running. */
 moe_status moe_selftest_wait_timeout(int timeout_us, int32_t* gave_up, void* stream);
 
+/* moe_embedding_backward as it runs on a device that holds no thread-block
+ * cluster of 16: 4097 to 65536 tokens are sorted by a launch a pass, not on chip.
+ * The result has the same bits. */
+moe_status moe_selftest_embedding_by_passes(const void* d_out, moe_dtype d_type, const void* ids,
+                                            moe_index_type ids_type, float scale, const void* add, int32_t T,
+                                            int32_t V, int32_t D, float* d_table, void* scratch,
+                                            size_t scratch_bytes, void* stream);
+
 /* Number of kernels this library has launched since it was loaded. */
 uint64_t moe_launch_count(void);
 
