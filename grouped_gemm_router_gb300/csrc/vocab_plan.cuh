@@ -164,7 +164,10 @@ inline ForwardPlan forward_plan(int T, int V) {
   return f;
 }
 
-constexpr size_t kPieceBytes = static_cast<size_t>(1) << 32;  // most bytes of dz that one piece holds
+// Most bytes of dz that one piece holds, except that it may have kLeastPiece columns at
+// any number of tokens: past 2^20 those are more, 64 GiB at 2^24.
+constexpr size_t kPieceBytes = static_cast<size_t>(1) << 32;
+constexpr int kLeastPiece = 8 * kTile;
 constexpr int kMinSplitBlocks = 12;                           // k blocks that a split has at least
 constexpr int kMaxSplits = kPlanPairs;                        // (32 x 64 x 150000: 59 us, with up to 16 splits 76)
 
@@ -176,7 +179,7 @@ struct BackwardPlan {
 inline BackwardPlan backward_plan(int T, int D, int V) {
   BackwardPlan b;
   const long most = static_cast<long>(kPieceBytes / 2 / static_cast<size_t>(std::max(T, 1))) / kTile * kTile;
-  b.pieces = ceil_div(V, std::max<long>(most, 8 * kTile));
+  b.pieces = ceil_div(V, std::max<long>(most, kLeastPiece));
   b.piece = b.pieces == 1 ? ceil_div(V, 64) * 64 : ceil_div(ceil_div(V, b.pieces), kTile) * kTile;
   b.pieces = ceil_div(V, b.piece);
   b.nmt = ceil_div(T, kTile);

@@ -739,7 +739,9 @@ def embedding_backward_workspace_size(T, V, D) -> int:
 
 @functools.lru_cache(maxsize=1024)
 def vocab_workspace_size(T, D, V, n_teacher=0, backward=False) -> int:
-    """Bytes of workspace of cross_entropy_* (n_teacher = 0) and distill_*."""
+    """Bytes of workspace of cross_entropy_* (n_teacher = 0) and distill_*.  A
+    backward's holds the logits' gradient of a piece of the vocabulary in bf16: 2 T V
+    bytes, but at most the larger of 4 GiB and 4096 T, and fp32 sums beside it."""
     name = "moe_vocab_backward_workspace_size" if backward else "moe_vocab_forward_workspace_size"
     _in_32_bits(name, T, D, V, n_teacher)
     n = int(getattr(lib, name)(T, D, V, n_teacher))

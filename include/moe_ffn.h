@@ -398,7 +398,11 @@ moe_status moe_embedding_backward(const void* d_out, moe_dtype d_type, const voi
  * 2e-6 of itself too near to 0, others less than 1e-6 of the size of their sums;
  * where 24 bits hold every sum, z is exact.  Workspaces start on 256 bytes and
  * hold nothing between calls; the size functions return 0 for a bad shape.
- * n_teacher is 0 for the cross entropy. */
+ * n_teacher is 0 for the cross entropy.  The forward's is a float pair or so a
+ * token and 256 to 1024 words.  The backward's holds the logits' gradient of a
+ * piece of the vocabulary in bf16, 2 T V bytes but at most the larger of 4 GiB and
+ * 4096 T (2048 words, 64 GiB at T = 2^24), and fp32 sums of dx and dW where their
+ * reductions are cut. */
 size_t moe_vocab_forward_workspace_size(int32_t T, int32_t D, int32_t V, int32_t n_teacher);
 size_t moe_vocab_backward_workspace_size(int32_t T, int32_t D, int32_t V, int32_t n_teacher);
 
