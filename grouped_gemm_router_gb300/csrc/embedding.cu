@@ -154,7 +154,8 @@ SortPlan sort_plan(int T, int V, bool large_clusters) {
   p.passes = (b + 8) / 9;
   p.bits = (b + p.passes - 1) / p.passes;
   if (T <= (large_clusters ? kShortList : kPortable)) {
-    // (8000 tokens: 16 blocks 28.7 us a call, 8 29.5, 4 32.3; 32768: 16 75, 8 84)
+    // (8000 tokens into 5001 rows of 64: 16 blocks 22.3 us a call, 8 22.6, 4 24.2; 32768
+    // into 50001 rows of 768, tied: 16 69, 8 76)
     p.cluster = T <= 512 ? 1 : T <= kPortable ? 4 : kMaxCluster;
     p.block = kSortThreads;
     while (p.block * p.cluster < T) p.block *= 2;

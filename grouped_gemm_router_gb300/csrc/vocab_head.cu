@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== TMA producer (both CTAs) =====================
     if (lane == 0) {
       // What is loaded is read again by other pairs, what is stored is for later.
-      // Kept over it, kDz took 1450 us instead of 1500 (32768 x 768 x 50001) and
-      // 2270 instead of 2350 (8192 x 2048 x 131072), kStats 1 % less and kGrad 2 %
-      // (a forward of 1 x 1664 x 61514 46.1 us instead of 47.2).
+      // Kept over it, kDz takes 1486 us instead of 1493 (32768 x 768 x 50001) and
+      // 2328 instead of 2392 (8192 x 2048 x 131072), kStats 1242 and 2133 instead of
+      // 1266 and 2161, kGrad 2627 and 4586 instead of 2691 and 4808.
       const uint64_t pol = l2_policy_evict_last();
       auto load_tokens = [&](uint32_t dst, const CUtensorMap& map, int row, int block, uint32_t full) {
         tma_load_3d_pair(dst, &map, full, 0, row, block, pol);

@@ -14,9 +14,10 @@ namespace {
 constexpr int kTile = 256;      // rows and columns of a pair's tile
 constexpr int kBK = 128;        // k of a stage
 // Row tiles that are worked on side by side, all of them before the next run of
-// the vocabulary.  Without stores many share a read of W (64: 1245 us at 32768 x
-// 768 x 50001, 24: 1255); dz of few rows at a time is written with less
-// contention (24: 1425 us, 64: 1450, 128: 1540, 8: 1505).
+// the vocabulary.  Without stores many share a read of W (64: 1242 us at 32768 x
+// 768 x 50001, 24: 1260; 2133 and 2167 at 8192 x 2048 x 131072); dz of few rows at a
+// time is written with less contention (24: 1486 us, 64: 1492, 128: 1528, 8: 1518; of
+// the wider case's 32 row tiles 24 2328, 64 2310, 8 2391).
 constexpr int kGroupStats = 64, kGroupDz = 24;
 
 enum Mode { kStats, kDz, kGrad };
